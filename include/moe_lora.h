@@ -384,6 +384,97 @@ moe_status moe_merge_lora(const moe_shape *shape, const moe_weights *weights, vo
  * gradient to dx). src and dst may not overlap (MOE_ERR_INVALID_ARG).  */
 moe_status moe_accumulate(int32_t dtype, int64_t n, const void *src, void *dst, void *stream);
 
+/* ---- The residual stream around a block.
+ *
+ * Dropout, here and in the two operators below, is counter-based: whether
+ * element i of a tensor is kept depends only on (seed, offset + site, i), so a
+ * backward draws its forward's mask again and no mask is stored. rng points to
+ * two int64 on the device, {seed, offset}: a captured graph draws a new mask
+ * when the caller changes them between replays. site (host) tells the calls of
+ * one step apart; two calls of equal seed and offset + site use one mask.
+ * Philox4x32-10 with key = seed and counter = (i / 8, offset + site) gives 16
+ * bits per element (element i: half i % 2, low first, of word i % 8 / 2); it is
+ * kept when they are >= t = round(65536 p) and then scaled by
+ * 65536 / (65536 - t). A dropped element is 0 whatever its value. t = 0 (p = 0,
+ * or below 2^-17) drops nothing, and rng may then be NULL. p outside [0, 1), or
+ * t = 65536, is MOE_ERR_INVALID_ARG.
+ *
+ *   dst[i] = kept(i) ? scale * src[i] : 0,  i < n
+ * The same call on a gradient is the backward. dst may be src; otherwise the two
+ * may not overlap. Any n >= 0 up to 2^40, any alignment.  */
+moe_status moe_dropout(int32_t dtype, int64_t n, float p, const int64_t *rng, int64_t site,
+                       const void *src, void *dst, void *stream);
+
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm;
+
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1, /* gate [H] */
+  MOE_GATE_TOKEN = 2,   /* gate [T] */
+  MOE_GATE_FULL = 3     /* gate [T, H] */
+} moe_gate;
+
+/* The residual stream after a block (post, gate, dropout, add) and the input of
+ * the next (pre), in one pass:
+ *   v  = post(y)                       the norm after the block
+ *   h' = h + alpha * g * dropout(v)    stored in `dtype`; g = gate or sigmoid(gate)
+ *   x' = pre(h')                       the norm before the next block, of h' as stored
+ * A norm of row u is (weight_shift + w) * (u - mean) * rstd + b with
+ * rstd = 1 / sqrt(mean((u - mean)^2) + eps); RMS: mean = 0, no b. Statistics and
+ * sums are float32. Dropout's element index is t * H + c. */
+typedef struct {
+  int32_t T, H, dtype;
+  int32_t post, pre;     /* moe_norm */
+  int32_t gate;          /* moe_gate */
+  int32_t gate_sigmoid;  /* nonzero: g = sigmoid(gate) */
+  float alpha, eps, weight_shift, dropout;
+} moe_residual;
+
+/* Vectors [H] of `dtype`; those of a norm or gate that is not there, and b of an
+ * RMS norm, are not read. b may be NULL (none). gate: see moe_gate. */
+typedef struct {
+  const void *w_post, *b_post, *gate, *w_pre, *b_pre;
+} moe_residual_params;
+
+/* Gradients of the above, same shapes and dtype; NULL: not wanted. */
+typedef struct {
+  void *dw_post, *db_post, *dgate, *dw_pre, *db_pre;
+} moe_residual_grads;
+
+/*   h      [T, H] in, NULL: 0 (no stream yet);   y [T, H] in, NULL: no block output
+ *          (h' = h; post and gate must be none, dropout 0). Not both NULL.
+ *   h_out  [T, H] out; may be h; NULL only without y (nothing new to store)
+ *   x_out  [T, H] out; NULL exactly when pre is none
+ *   stats  [T, 4] float32 out, for the backward: post mean, post rstd, pre mean,
+ *          pre rstd (0 for a norm that is not there); NULL: not wanted
+ * moe_residual_norm_bwd, from dh_out (gradient at h', NULL: 0) and dx_out
+ * (gradient at x', required exactly when pre is not none):
+ *   h_out  [T, H] in, h' as stored (h when y was NULL); read when pre is not none
+ *   y, params, stats, rng, site   as in the forward (stats required with a norm;
+ *          y read with a post norm or a gate)
+ *   dh     [T, H] out, the gradient at h; may be dh_out; NULL: not wanted
+ *   dy     [T, H] out, the gradient at y; NULL: not wanted
+ *   grads  NULL: none wanted
+ *   ws     moe_residual_norm_workspace_bytes
+ * Sums over tokens are formed in float32 in an order that depends on T and H
+ * alone, so results repeat bit for bit. Errors: T < 1, H < 1, an unknown norm,
+ * gate or dtype, eps < 0 or not finite, H > 16384 or not a multiple of 8
+ * (MOE_ERR_UNSUPPORTED), a pointer off a 16-byte boundary (rng, of 8-byte
+ * numbers, and a gate per token with its gradient excepted), an
+ * output that overlaps an input or another output (apart from h_out = h and
+ * dh = dh_out). */
+moe_status moe_residual_norm_workspace_bytes(const moe_residual *desc, size_t *bwd_ws);
+moe_status moe_residual_norm_fwd(const moe_residual *desc, const void *h, const void *y,
+                                 const moe_residual_params *params, const int64_t *rng,
+                                 int64_t site, void *h_out, void *x_out, float *stats,
+                                 void *stream);
+moe_status moe_residual_norm_bwd(const moe_residual *desc, const void *dh_out, const void *dx_out,
+                                 const void *h_out, const void *y,
+                                 const moe_residual_params *params, const float *stats,
+                                 const int64_t *rng, int64_t site, void *dh, void *dy,
+                                 const moe_residual_grads *grads, void *ws, size_t ws_bytes,
+                                 void *stream);
+
 const char *moe_status_str(moe_status status);
 
 /* Text of the last error raised on the calling thread ("" if none). */
@@ -401,7 +492,8 @@ typedef enum {
   MOE_K_DOWN_BWD = 8, MOE_K_GATE_UP_BWD = 9, MOE_K_LORA_SIDE = 10, MOE_K_LORA_WGRAD = 11,
   MOE_K_UNPERMUTE = 12, MOE_K_BASE_WGRAD = 13, MOE_K_ROUTER_FWD = 14, MOE_K_ROUTER_BWD = 15,
   MOE_K_ACCUMULATE = 16, MOE_K_MERGE = 17, MOE_K_DY_GATHER = 18, MOE_K_DW_SUM = 19,
-  MOE_K_ROW_SCALE = 20, MOE_K_COUNT = 21
+  MOE_K_ROW_SCALE = 20, MOE_K_DROPOUT = 21, MOE_K_RESIDUAL_NORM = 22,
+  MOE_K_RESIDUAL_NORM_BWD = 23, MOE_K_COUNT = 24
 } moe_kernel_id;
 moe_status moe_kernel_timer_enable(int32_t on);
 /* Time only the kernels whose bit (1u << id) is set in mask (all, by default):

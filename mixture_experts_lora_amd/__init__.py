@@ -16,13 +16,15 @@ sections "What is torch._grouped_mm?", "Faster LoRA MoE training" and
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
 import torch
 
 from . import _lib
-from ._lib import MoeBaseGrads, MoeLoraGrads, MoeSaved, MoeShape, MoeWeights, ROUTER_IDS, check
+from ._lib import (GATE_IDS, MoeBaseGrads, MoeLoraGrads, MoeResidual, MoeResidualGrads,
+                   MoeResidualParams, MoeSaved, MoeShape, MoeWeights, NORM_IDS, ROUTER_IDS, check)
 
 __all__ = [
     "Shape", "moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
@@ -32,7 +34,8 @@ __all__ = [
     "moe_grouped_lora_bwd", "moe_grouped_full_bwd", "moe_workspace_bytes_lean",
     "moe_grouped_lora_fwd_lean", "moe_grouped_lora_bwd_recompute", "moe_router_workspace_bytes",
     "moe_router_fwd", "moe_router_bwd", "moe_accumulate", "moe_merge_workspace_bytes",
-    "moe_merge_lora", "kernel_timer", "ROUTER_IDS",
+    "moe_merge_lora", "Residual", "moe_residual_norm_workspace_bytes", "moe_residual_norm_fwd",
+    "moe_residual_norm_bwd", "moe_dropout", "kernel_timer", "ROUTER_IDS", "NORM_IDS", "GATE_IDS",
     "library_path",
 ]
 
@@ -424,6 +427,143 @@ def moe_merge_lora(shape: Shape, weights: dict, w_gu_merged=None, w_d_merged=Non
         _ptr(w_gu_merged, (E, 2 * I, H), dt, "w_gu_merged", optional=True),
         _ptr(w_d_merged, (E, H, I), dt, "w_d_merged", optional=True), wsp, wsb,
         _stream(stream)), "moe_merge_lora")
+
+
+@dataclass(frozen=True)
+class Residual:
+    """The residual stream around a block: h' = h + alpha * g * dropout(post(y)), x' = pre(h').
+    post, pre: "none", "rms" or "layer"; gate: "none", "channel" [H], "token" [T] or "full"
+    [T, H], passed through a sigmoid with gate_sigmoid. A norm's weight is weight_shift + w."""
+    T: int
+    H: int
+    dtype: str = "bf16"       # "bf16", "f16" or "f32"
+    post: str = "none"
+    pre: str = "rms"
+    gate: str = "none"
+    gate_sigmoid: bool = False
+    alpha: float = 1.0
+    eps: float = 1e-5
+    weight_shift: float = 0.0
+    dropout: float = 0.0
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return _TORCH_DTYPES[self.dtype]
+
+    def c(self) -> MoeResidual:
+        return MoeResidual(self.T, self.H, _ABI_DTYPES[self.dtype], NORM_IDS[self.post],
+                           NORM_IDS[self.pre], GATE_IDS[self.gate], int(self.gate_sigmoid),
+                           float(self.alpha), float(self.eps), float(self.weight_shift),
+                           float(self.dropout))
+
+    def param_shapes(self) -> dict:
+        """Shapes of the vectors this operator takes: w_post, b_post, gate, w_pre, b_pre."""
+        s = {}
+        for which in ("post", "pre"):
+            if getattr(self, which) != "none":
+                s["w_" + which] = (self.H,)
+            if getattr(self, which) == "layer":
+                s["b_" + which] = (self.H,)
+        if self.gate != "none":
+            s["gate"] = {"channel": (self.H,), "token": (self.T,), "full": (self.T, self.H)}[self.gate]
+        return s
+
+
+def _on_device(t):
+    """The launches of a call run on its tensors' device, whichever device is current."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
+        return torch.cuda.device(t.device)
+    return contextlib.nullcontext()
+
+
+def _same_device(*tensors):
+    first = None
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            if first is None:
+                first = t.device
+            elif t.device != first:
+                raise ValueError(f"tensors on {first} and {t.device}")
+
+
+def _rng(rng, p):
+    if p == 0.0:
+        return None
+    return _ptr(rng, (2,), torch.int64, "rng")
+
+
+def moe_dropout(src, dst, p, rng, site=0, stream=None):
+    """dst = src with each element dropped with probability p, the others scaled by 1 / (1 - p).
+    rng: int64 [2] on the GPU, {seed, offset}; the mask depends on (seed, offset + site, element
+    index) alone, so the same call on a gradient is the backward. dst may be src."""
+    key, dt = _dtype_of(src, "src")
+    _same_device(src, dst, rng)
+    with _on_device(src):
+        check(_lib.load().moe_dropout(
+            _ABI_DTYPES[key], src.numel(), float(p), _rng(rng, p), int(site),
+            _ptr(src, tuple(src.shape), dt, "src"), _ptr(dst, tuple(src.shape), dt, "dst"),
+            _stream(stream)), "moe_dropout")
+
+
+def moe_residual_norm_workspace_bytes(desc: Residual) -> int:
+    """Workspace bytes of moe_residual_norm_bwd (the forward needs none)."""
+    n = ctypes.c_size_t()
+    check(_lib.load().moe_residual_norm_workspace_bytes(ctypes.byref(desc.c()), ctypes.byref(n)),
+          "moe_residual_norm_workspace_bytes")
+    return n.value
+
+
+def _residual_params(desc: Residual, params):
+    shapes, params = desc.param_shapes(), params or {}
+    return MoeResidualParams(**{n: _ptr(params.get(n), s, desc.torch_dtype, n,
+                                        optional=n.startswith("b_"))
+                                for n, s in shapes.items()})
+
+
+def moe_residual_norm_fwd(desc: Residual, h, y, params, h_out, x_out, stats, rng=None, site=0,
+                          stream=None):
+    """h_out = h + alpha * g * dropout(post(y)); x_out = pre(h_out). h None: no stream yet;
+    y None: no block output (x_out = pre(h), h_out optional). params: dict of desc.param_shapes().
+    stats: float32 [T, 4] for the backward, or None. h_out may be h."""
+    rows, dt = (desc.T, desc.H), desc.torch_dtype
+    _same_device(h, y, h_out, x_out, stats, rng, *(params or {}).values())
+    q = _residual_params(desc, params)
+    with _on_device(h if h is not None else y):
+        check(_lib.load().moe_residual_norm_fwd(
+            ctypes.byref(desc.c()), _ptr(h, rows, dt, "h", optional=True),
+            _ptr(y, rows, dt, "y", optional=True), ctypes.byref(q), _rng(rng, desc.dropout),
+            int(site), _ptr(h_out, rows, dt, "h_out", optional=y is None),
+            _ptr(x_out, rows, dt, "x_out", optional=True),
+            _ptr(stats, (desc.T, 4), torch.float32, "stats", optional=True), _stream(stream)),
+            "moe_residual_norm_fwd")
+
+
+def moe_residual_norm_bwd(desc: Residual, dh_out, dx_out, h_out, y, params, stats, dh, dy, grads,
+                          ws, rng=None, site=0, stream=None):
+    """Backward of moe_residual_norm_fwd from the gradients at h_out (None: 0) and x_out (None
+    exactly when there is no pre norm): writes dh, dy and the vectors of grads (keys dw_post,
+    db_post, dgate, dw_pre, db_pre); any of them may be None or left out. dh may be dh_out."""
+    rows, dt = (desc.T, desc.H), desc.torch_dtype
+    grads = grads or {}
+    _same_device(dh_out, dx_out, h_out, y, stats, dh, dy, ws, rng, *(params or {}).values(),
+                 *grads.values())
+    q = _residual_params(desc, params)
+    unknown = set(grads) - {"d" + n for n in desc.param_shapes()}
+    if unknown:
+        raise ValueError(f"no such gradient here: {sorted(unknown)}")
+    g = MoeResidualGrads(**{"d" + n: _ptr(grads.get("d" + n), s, dt, "d" + n, optional=True)
+                            for n, s in desc.param_shapes().items()})
+    need = moe_residual_norm_workspace_bytes(desc) if any(v is not None for v in grads.values()) else 0
+    wsp, wsb = _ws(ws, need, "ws")
+    with _on_device(dh_out if dh_out is not None else dx_out):
+        check(_lib.load().moe_residual_norm_bwd(
+            ctypes.byref(desc.c()), _ptr(dh_out, rows, dt, "dh_out", optional=True),
+            _ptr(dx_out, rows, dt, "dx_out", optional=True),
+            _ptr(h_out, rows, dt, "h_out", optional=True), _ptr(y, rows, dt, "y", optional=True),
+            ctypes.byref(q), _ptr(stats, (desc.T, 4), torch.float32, "stats", optional=True),
+            _rng(rng, desc.dropout), int(site), _ptr(dh, rows, dt, "dh", optional=True),
+            _ptr(dy, rows, dt, "dy", optional=True), ctypes.byref(g), wsp, wsb, _stream(stream)),
+            "moe_residual_norm_bwd")
 
 
 class kernel_timer:

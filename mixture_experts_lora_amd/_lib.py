@@ -15,7 +15,10 @@ KERNEL_IDS = {"route": 0, "permute": 1, "gather": 2, "gate_up_fwd": 3, "down_fwd
               "combine": 5, "combine_bwd": 6, "route_bwd": 7, "down_bwd": 8, "gate_up_bwd": 9,
               "lora_side": 10, "lora_wgrad": 11, "unpermute": 12, "base_wgrad": 13,
               "router_fwd": 14, "router_bwd": 15, "accumulate": 16, "merge": 17,
-              "dy_gather": 18, "dw_sum": 19, "row_scale": 20}
+              "dy_gather": 18, "dw_sum": 19, "row_scale": 20, "dropout": 21, "residual_norm": 22,
+              "residual_norm_bwd": 23}
+NORM_IDS = {"none": 0, "rms": 1, "layer": 2}
+GATE_IDS = {"none": 0, "channel": 1, "token": 2, "full": 3}
 
 EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
            "moe_grouped_lora_fwd", "moe_unpermute_combine", "moe_unpermute_combine_bwd",
@@ -25,6 +28,8 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
            "moe_merge_workspace_bytes", "moe_merge_lora", "moe_permute_noalloc",
            "moe_grouped_lora_combine_bwd", "moe_grouped_lora_fwd_gather",
            "moe_grouped_lora_combine_bwd_gather",
+           "moe_dropout", "moe_residual_norm_workspace_bytes", "moe_residual_norm_fwd",
+           "moe_residual_norm_bwd",
            "moe_status_str",
            "moe_last_error",
            "moe_kernel_timer_enable", "moe_kernel_timer_select", "moe_kernel_timer_reset",
@@ -51,6 +56,20 @@ class MoeLoraGrads(ctypes.Structure):
 
 class MoeBaseGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dw_gu", "dw_d")]
+
+
+class MoeResidual(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "dtype", "post", "pre", "gate",
+                                              "gate_sigmoid")] + \
+               [(n, ctypes.c_float) for n in ("alpha", "eps", "weight_shift", "dropout")]
+
+
+class MoeResidualParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w_post", "b_post", "gate", "w_pre", "b_pre")]
+
+
+class MoeResidualGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dw_post", "db_post", "dgate", "dw_pre", "db_pre")]
 
 
 _lib = None
@@ -126,6 +145,16 @@ def load() -> ctypes.CDLL:
                                            ctypes.POINTER(ctypes.c_size_t)]),
         "moe_merge_lora": (st, [ctypes.POINTER(MoeShape), ctypes.POINTER(MoeWeights), P, P, P,
                                 ctypes.c_size_t, P]),
+        "moe_dropout": (st, [I32, ctypes.c_int64, ctypes.c_float, P, ctypes.c_int64, P, P, P]),
+        "moe_residual_norm_workspace_bytes": (st, [ctypes.POINTER(MoeResidual),
+                                                   ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_residual_norm_fwd": (st, [ctypes.POINTER(MoeResidual), P, P,
+                                       ctypes.POINTER(MoeResidualParams), P, ctypes.c_int64, P, P,
+                                       P, P]),
+        "moe_residual_norm_bwd": (st, [ctypes.POINTER(MoeResidual), P, P, P, P,
+                                       ctypes.POINTER(MoeResidualParams), P, P, ctypes.c_int64, P,
+                                       P, ctypes.POINTER(MoeResidualGrads), P, ctypes.c_size_t,
+                                       P]),
         "moe_status_str": (ctypes.c_char_p, [st]),
         "moe_last_error": (ctypes.c_char_p, []),
         "moe_kernel_timer_enable": (st, [I32]),

@@ -2,6 +2,8 @@
 // launches on the caller's stream. Declarations and the contract of every
 // entry point are in include/moe_lora.h.
 #include <algorithm>
+#include <cmath>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -749,6 +751,283 @@ moe_status moe_accumulate(int32_t dtype, int64_t n, const void* src, void* dst, 
   }
   hipError_t e = moe::launch_accumulate(dtype, n, src, dst, as_stream(stream), moe::active_timer());
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_accumulate");
+}
+
+namespace {
+
+struct Range {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+
+bool ranges_overlap(const Range& a, const Range& b) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
+}
+
+// No output may overlap an input or another output; the pairs in `same` (an
+// output and an input) may be one and the same buffer.
+moe_status check_ranges(std::initializer_list<Range> outs, std::initializer_list<Range> ins,
+                        const void* same_out, const void* same_in) {
+  for (const Range& o : outs) {
+    for (const Range& i : ins)
+      if (ranges_overlap(o, i) && !(o.p == same_out && i.p == same_in && o.p == i.p))
+        return fail(MOE_ERR_INVALID_ARG, std::string(o.name) + " overlaps " + i.name);
+    for (const Range& other : outs)
+      if (&o != &other && ranges_overlap(o, other))
+        return fail(MOE_ERR_INVALID_ARG, std::string(o.name) + " overlaps " + other.name);
+  }
+  return MOE_OK;
+}
+
+bool known_dtype(int32_t dtype) {
+  return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16;
+}
+
+// Fills the threshold and scale of dropout probability p.
+moe_status make_drop(float p, const int64_t* rng, int64_t site, moe::DropArgs* d) {
+  if (!(p >= 0.f && p < 1.f))
+    return fail(MOE_ERR_INVALID_ARG, "dropout must be in [0, 1), got " + std::to_string(p));
+  const uint32_t t = static_cast<uint32_t>(static_cast<double>(p) * 65536.0 + 0.5);
+  if (t >= 65536)
+    return fail(MOE_ERR_INVALID_ARG, "dropout rounds to 1 in steps of 2^-16");
+  if (t != 0) {
+    CHECK_PTR(rng);
+    if (reinterpret_cast<uintptr_t>(rng) & 7)
+      return fail(MOE_ERR_INVALID_ARG, "rng does not start on an 8-byte boundary");
+  }
+  d->rng = rng;
+  d->site = static_cast<uint64_t>(site);
+  d->thr = t;
+  d->scale = static_cast<float>(65536.0 / (65536.0 - t));
+  return MOE_OK;
+}
+
+moe_status check_residual(const moe_residual* r) {
+  if (!r) return fail(MOE_ERR_INVALID_ARG, "null descriptor");
+  if (r->T < 1 || r->H < 1) return fail(MOE_ERR_INVALID_ARG, "T and H must be >= 1");
+  if (!known_dtype(r->dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype");
+  for (int32_t n : {r->post, r->pre})
+    if (n < MOE_NORM_NONE || n > MOE_NORM_LAYER)
+      return fail(MOE_ERR_INVALID_ARG, "unknown norm " + std::to_string(n));
+  if (r->gate < MOE_GATE_NONE || r->gate > MOE_GATE_FULL)
+    return fail(MOE_ERR_INVALID_ARG, "unknown gate " + std::to_string(r->gate));
+  if (!(r->eps >= 0.f) || !std::isfinite(r->eps))
+    return fail(MOE_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (r->H % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "H must be a multiple of 8");
+  if (r->H > 16384) return fail(MOE_ERR_UNSUPPORTED, "H > 16384 is not supported");
+  return MOE_OK;
+}
+
+inline int64_t esize(int32_t dtype) { return dtype == MOE_F32 ? 4 : 2; }
+
+int64_t gate_bytes(const moe_residual* r) {
+  const int64_t e = esize(r->dtype);
+  if (r->gate == MOE_GATE_CHANNEL) return r->H * e;
+  if (r->gate == MOE_GATE_TOKEN) return r->T * e;
+  return r->gate == MOE_GATE_FULL ? int64_t(r->T) * r->H * e : 0;
+}
+
+// The vectors that `r` reads, checked; the others are nulled.
+moe_status residual_params(const moe_residual* r, const moe_residual_params* q,
+                           moe::ResidualArgs* a) {
+  const bool any = r->post != MOE_NORM_NONE || r->pre != MOE_NORM_NONE || r->gate != MOE_GATE_NONE;
+  if (any) CHECK_PTR(q);
+  a->T = r->T;
+  a->H = r->H;
+  a->post = r->post;
+  a->pre = r->pre;
+  a->gate_kind = r->gate;
+  a->gate_sigmoid = r->gate_sigmoid != 0;
+  a->alpha = r->alpha;
+  a->eps = r->eps;
+  a->shift = r->weight_shift;
+  a->inv_h = 1.0f / static_cast<float>(r->H);
+  if (r->post != MOE_NORM_NONE) {
+    CHECK_PTR(q->w_post);
+    CHECK_ROWS(q->w_post);
+    a->w_post = q->w_post;
+    if (r->post == MOE_NORM_LAYER) {
+      CHECK_ROWS(q->b_post);
+      a->b_post = q->b_post;
+    }
+  }
+  if (r->pre != MOE_NORM_NONE) {
+    CHECK_PTR(q->w_pre);
+    CHECK_ROWS(q->w_pre);
+    a->w_pre = q->w_pre;
+    if (r->pre == MOE_NORM_LAYER) {
+      CHECK_ROWS(q->b_pre);
+      a->b_pre = q->b_pre;
+    }
+  }
+  if (r->gate != MOE_GATE_NONE) {
+    CHECK_PTR(q->gate);
+    if (r->gate != MOE_GATE_TOKEN) CHECK_ROWS(q->gate);
+    a->gate = q->gate;
+  }
+  return MOE_OK;
+}
+
+// Which column sums the backward forms, in the order of ResidualBwdArgs::colsum.
+int residual_slots(const moe_residual* r, int32_t (&slot)[5]) {
+  const bool want[5] = {r->pre != MOE_NORM_NONE, r->pre == MOE_NORM_LAYER,
+                        r->post != MOE_NORM_NONE, r->post == MOE_NORM_LAYER,
+                        r->gate == MOE_GATE_CHANNEL};
+  int n = 0;
+  for (int i = 0; i < 5; ++i) slot[i] = want[i] ? n++ : -1;
+  return n;
+}
+
+size_t residual_ws_bytes(const moe_residual* r) {
+  int32_t slot[5];
+  return static_cast<size_t>(residual_slots(r, slot)) * r->H * sizeof(float) *
+         moe::residual_bwd_groups(r->T, r->H);
+}
+
+}  // namespace
+
+moe_status moe_dropout(int32_t dtype, int64_t n, float p, const int64_t* rng, int64_t site,
+                       const void* src, void* dst, void* stream) {
+  if (!known_dtype(dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype");
+  if (n < 0 || n > (int64_t(1) << 40))
+    return fail(MOE_ERR_INVALID_ARG, "n must be in [0, 2^40]");
+  moe::DropArgs d{};
+  moe_status st = make_drop(p, rng, site, &d);
+  if (st != MOE_OK || n == 0) return st;
+  CHECK_PTR(src);
+  CHECK_PTR(dst);
+  const int64_t bytes = n * esize(dtype);
+  st = check_ranges({{dst, bytes, "dst"}}, {{src, bytes, "src"}, {d.thr ? rng : nullptr, 16, "rng"}},
+                    dst, src);
+  if (st != MOE_OK) return st;
+  hipError_t e = moe::launch_dropout(dtype, n, d, src, dst, as_stream(stream), moe::active_timer());
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_dropout");
+}
+
+moe_status moe_residual_norm_workspace_bytes(const moe_residual* desc, size_t* bwd_ws) {
+  moe_status st = check_residual(desc);
+  if (st != MOE_OK) return st;
+  CHECK_PTR(bwd_ws);
+  *bwd_ws = residual_ws_bytes(desc);
+  return MOE_OK;
+}
+
+moe_status moe_residual_norm_fwd(const moe_residual* desc, const void* h, const void* y,
+                                 const moe_residual_params* params, const int64_t* rng,
+                                 int64_t site, void* h_out, void* x_out, float* stats,
+                                 void* stream) {
+  moe_status st = check_residual(desc);
+  if (st != MOE_OK) return st;
+  if (!h && !y) return fail(MOE_ERR_INVALID_ARG, "h and y are both NULL");
+  moe::ResidualArgs a{};
+  if ((st = make_drop(desc->dropout, rng, site, &a.drop)) != MOE_OK) return st;
+  if (!y && (desc->post != MOE_NORM_NONE || desc->gate != MOE_GATE_NONE || a.drop.thr))
+    return fail(MOE_ERR_INVALID_ARG, "a post norm, a gate or dropout needs y");
+  if ((st = residual_params(desc, params, &a)) != MOE_OK) return st;
+  if (y) CHECK_PTR(h_out);
+  if (desc->pre != MOE_NORM_NONE) CHECK_PTR(x_out);
+  else if (x_out) return fail(MOE_ERR_INVALID_ARG, "x_out without a pre norm");
+  if (!h_out && !x_out) return fail(MOE_ERR_INVALID_ARG, "no output");
+  CHECK_ROWS(h);
+  CHECK_ROWS(y);
+  CHECK_ROWS(h_out);
+  CHECK_ROWS(x_out);
+  CHECK_ROWS(stats);
+  const int64_t row = desc->H * esize(desc->dtype), rows = row * desc->T;
+  st = check_ranges({{h_out, rows, "h_out"}, {x_out, rows, "x_out"}, {stats, int64_t(desc->T) * 16, "stats"}},
+                    {{h, rows, "h"}, {y, rows, "y"}, {a.w_post, row, "w_post"}, {a.b_post, row, "b_post"},
+                     {a.gate, gate_bytes(desc), "gate"}, {a.w_pre, row, "w_pre"}, {a.b_pre, row, "b_pre"},
+                     {a.drop.thr ? rng : nullptr, 16, "rng"}},
+                    h_out, h);
+  if (st != MOE_OK) return st;
+  a.h = h;
+  a.y = y;
+  a.h_out = h_out;
+  a.x_out = x_out;
+  a.stats = reinterpret_cast<float4*>(stats);
+  hipError_t e = moe::launch_residual_fwd(desc->dtype, a, as_stream(stream), moe::active_timer());
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_residual_norm_fwd");
+}
+
+moe_status moe_residual_norm_bwd(const moe_residual* desc, const void* dh_out, const void* dx_out,
+                                 const void* h_out, const void* y,
+                                 const moe_residual_params* params, const float* stats,
+                                 const int64_t* rng, int64_t site, void* dh, void* dy,
+                                 const moe_residual_grads* grads, void* ws, size_t ws_bytes,
+                                 void* stream) {
+  moe_status st = check_residual(desc);
+  if (st != MOE_OK) return st;
+  const bool pre = desc->pre != MOE_NORM_NONE, post = desc->post != MOE_NORM_NONE;
+  const bool gate = desc->gate != MOE_GATE_NONE;
+  moe::ResidualBwdArgs q{};
+  if ((st = make_drop(desc->dropout, rng, site, &q.f.drop)) != MOE_OK) return st;
+  if ((st = residual_params(desc, params, &q.f)) != MOE_OK) return st;
+  if (pre) {
+    CHECK_PTR(dx_out);
+    CHECK_PTR(h_out);
+  } else {
+    if (dx_out) return fail(MOE_ERR_INVALID_ARG, "dx_out without a pre norm");
+    CHECK_PTR(dh_out);
+  }
+  if (pre || post) CHECK_PTR(stats);
+  if (post || gate) CHECK_PTR(y);
+  const moe_residual_grads none{};
+  const moe_residual_grads& g = grads ? *grads : none;
+  q.colsum[0] = pre ? g.dw_pre : nullptr;
+  q.colsum[1] = desc->pre == MOE_NORM_LAYER ? g.db_pre : nullptr;
+  q.colsum[2] = post ? g.dw_post : nullptr;
+  q.colsum[3] = desc->post == MOE_NORM_LAYER ? g.db_post : nullptr;
+  q.colsum[4] = desc->gate == MOE_GATE_CHANNEL ? g.dgate : nullptr;
+  q.dgate = desc->gate == MOE_GATE_TOKEN || desc->gate == MOE_GATE_FULL ? g.dgate : nullptr;
+  // those that are wanted take the partials' places in order
+  for (int i = 0; i < 5; ++i) q.slot[i] = q.colsum[i] ? q.nslots++ : -1;
+  if (!dh && !dy && !q.nslots && !q.dgate) return fail(MOE_ERR_INVALID_ARG, "no output");
+  CHECK_ROWS(dh_out);
+  CHECK_ROWS(dx_out);
+  CHECK_ROWS(h_out);
+  CHECK_ROWS(y);
+  CHECK_ROWS(stats);
+  CHECK_ROWS(dh);
+  CHECK_ROWS(dy);
+  CHECK_ROWS(ws);
+  CHECK_ROWS(g.dw_post);
+  CHECK_ROWS(g.db_post);
+  CHECK_ROWS(g.dw_pre);
+  CHECK_ROWS(g.db_pre);
+  if (desc->gate != MOE_GATE_TOKEN) CHECK_ROWS(g.dgate);
+  const size_t need = residual_ws_bytes(desc);
+  if (q.nslots) {
+    CHECK_PTR(ws);
+    if (ws_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "residual workspace needs " + std::to_string(need) + " bytes");
+  }
+  const int64_t row = desc->H * esize(desc->dtype), rows = row * desc->T;
+  st = check_ranges(
+      {{dh, rows, "dh"}, {dy, rows, "dy"}, {q.dgate, gate_bytes(desc), "dgate"},
+       {q.colsum[0], row, "dw_pre"}, {q.colsum[1], row, "db_pre"}, {q.colsum[2], row, "dw_post"},
+       {q.colsum[3], row, "db_post"}, {q.colsum[4], row, "dgate"},
+       {q.nslots ? ws : nullptr, static_cast<int64_t>(need), "ws"}},
+      {{dh_out, rows, "dh_out"}, {dx_out, rows, "dx_out"}, {pre ? h_out : nullptr, rows, "h_out"},
+       {post || gate ? y : nullptr, rows, "y"}, {pre || post ? stats : nullptr, int64_t(desc->T) * 16, "stats"},
+       {q.f.w_post, row, "w_post"}, {q.f.b_post, row, "b_post"}, {q.f.gate, gate_bytes(desc), "gate"},
+       {q.f.w_pre, row, "w_pre"}, {q.f.b_pre, row, "b_pre"},
+       {q.f.drop.thr ? rng : nullptr, 16, "rng"}},
+      dh, dh_out);
+  if (st != MOE_OK) return st;
+  q.f.y = y;
+  q.f.stats = pre || post ? reinterpret_cast<float4*>(const_cast<float*>(stats)) : nullptr;
+  q.dh_out = dh_out;
+  q.dx_out = dx_out;
+  q.h_out = h_out;
+  q.dh = dh;
+  q.dy = dy;
+  q.groups = moe::residual_bwd_groups(desc->T, desc->H);
+  q.part = static_cast<float*>(ws);
+  hipError_t e = moe::launch_residual_bwd(desc->dtype, q, as_stream(stream), moe::active_timer());
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_residual_norm_bwd");
 }
 
 moe_status moe_kernel_timer_enable(int32_t on) {

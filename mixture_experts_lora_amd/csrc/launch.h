@@ -144,4 +144,42 @@ hipError_t launch_router_bwd(const float* d_logits, const void* w_r, int T, int 
 hipError_t launch_accumulate(int dtype, int64_t n, const void* src, void* dst, hipStream_t s,
                              KernelTimer* tm);
 
+// ---- dropout and the residual stream
+// thr == 0: no dropout (rng is not read then).
+struct DropArgs {
+  const int64_t* rng;  // device [2]: seed, offset
+  uint64_t site;       // added to the offset
+  uint32_t thr;        // an element is dropped when its 16 bits are below it
+  float scale;         // of the kept elements
+};
+
+hipError_t launch_dropout(int dtype, int64_t n, const DropArgs& d, const void* src, void* dst,
+                          hipStream_t s, KernelTimer* tm);
+
+struct ResidualArgs {
+  int32_t T, H, post, pre, gate_kind, gate_sigmoid;
+  float alpha, eps, shift, inv_h;
+  const void *h, *y, *w_post, *b_post, *gate, *w_pre, *b_pre;
+  void *h_out, *x_out;
+  float4* stats;  // [T]: post mean and rstd, pre mean and rstd
+  DropArgs drop;
+};
+
+// f: the forward's vectors, y and statistics (h, h_out and x_out unused).
+struct ResidualBwdArgs {
+  ResidualArgs f;
+  const void *dh_out, *dx_out, *h_out;
+  void *dh, *dy, *dgate;  // dgate: token and full gates, written by the row kernel
+  void* colsum[5];        // dw_pre, db_pre, dw_post, db_post, channel dgate; null: not wanted
+  int32_t slot[5];        // each one's place in the partials, -1: not formed
+  int32_t nslots;
+  int64_t groups;
+  float* part;  // [groups][nslots][H]
+};
+
+int64_t residual_bwd_groups(int T, int H);
+hipError_t launch_residual_fwd(int dtype, const ResidualArgs& a, hipStream_t s, KernelTimer* tm);
+hipError_t launch_residual_bwd(int dtype, const ResidualBwdArgs& a, hipStream_t s,
+                               KernelTimer* tm);
+
 }  // namespace moe
