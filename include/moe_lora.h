@@ -475,6 +475,46 @@ moe_status moe_residual_norm_bwd(const moe_residual *desc, const void *dh_out, c
                                  const moe_residual_grads *grads, void *ws, size_t ws_bytes,
                                  void *stream);
 
+/* Dense product into the residual stream with its epilogue, for example the
+ * attention output projection before the block:
+ *   z = x w^T + bias            x [T, K], w [N, K], bias [N]
+ *   y = residual + dropout(act(z))      y, residual, z [T, N]
+ * Products, bias, activation and sums are float32; z and y are rounded once.
+ * Dropout's element index is t * N + n. gelu is z Phi(z); gelu_tanh its tanh
+ * form with sqrt(2/pi) and 0.044715. */
+typedef enum {
+  MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4
+} moe_act;
+
+typedef struct {
+  int32_t T, K, N, dtype;
+  int32_t act;  /* moe_act */
+  float dropout;
+} moe_linear_shape;
+
+/*   bias, residual  NULL: none; y may be residual
+ *   pre    z out, kept for the backward; NULL: not wanted
+ * moe_linear_bwd, from dy [T, N] (the residual's gradient is dy itself):
+ *   dz = act'(pre) * dropout(dy), rounded to `dtype` (it feeds the MFMA)
+ *   dx [T, K] = dz w    dw [N, K] = dz^T x    dbias [N] = sum_t dz (unrounded dz)
+ *   pre    as kept by the forward; read (and required) when act is not none
+ *   dx, dw, dbias   NULL: not wanted; x is read for dw, w for dx (else may be NULL)
+ * ws: moe_linear_workspace_bytes (either may be 0: ws may then be NULL). Results
+ * repeat bit for bit. Errors: T, K, N < 1, an unknown act or dtype, T * max(K, N)
+ * elements above 32 GiB, w of 2 GiB or more, K or N not a multiple of 8
+ * (MOE_ERR_UNSUPPORTED), a pointer off a 16-byte boundary (rng: 8), an output that
+ * overlaps an input or another output (apart from y = residual). */
+moe_status moe_linear_workspace_bytes(const moe_linear_shape *shape, size_t *fwd_ws,
+                                      size_t *bwd_ws);
+moe_status moe_linear_fwd(const moe_linear_shape *shape, const void *x, const void *w,
+                          const void *bias, const void *residual, const int64_t *rng,
+                          int64_t site, void *y, void *pre, void *ws, size_t ws_bytes,
+                          void *stream);
+moe_status moe_linear_bwd(const moe_linear_shape *shape, const void *dy, const void *x,
+                          const void *w, const void *pre, const int64_t *rng, int64_t site,
+                          void *dx, void *dw, void *dbias, void *ws, size_t ws_bytes,
+                          void *stream);
+
 const char *moe_status_str(moe_status status);
 
 /* Text of the last error raised on the calling thread ("" if none). */
@@ -493,7 +533,8 @@ typedef enum {
   MOE_K_UNPERMUTE = 12, MOE_K_BASE_WGRAD = 13, MOE_K_ROUTER_FWD = 14, MOE_K_ROUTER_BWD = 15,
   MOE_K_ACCUMULATE = 16, MOE_K_MERGE = 17, MOE_K_DY_GATHER = 18, MOE_K_DW_SUM = 19,
   MOE_K_ROW_SCALE = 20, MOE_K_DROPOUT = 21, MOE_K_RESIDUAL_NORM = 22,
-  MOE_K_RESIDUAL_NORM_BWD = 23, MOE_K_COUNT = 24
+  MOE_K_RESIDUAL_NORM_BWD = 23, MOE_K_LINEAR_FWD = 24, MOE_K_LINEAR_BWD = 25,
+  MOE_K_COUNT = 26
 } moe_kernel_id;
 moe_status moe_kernel_timer_enable(int32_t on);
 /* Time only the kernels whose bit (1u << id) is set in mask (all, by default):

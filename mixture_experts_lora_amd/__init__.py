@@ -23,8 +23,9 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (GATE_IDS, MoeBaseGrads, MoeLoraGrads, MoeResidual, MoeResidualGrads,
-                   MoeResidualParams, MoeSaved, MoeShape, MoeWeights, NORM_IDS, ROUTER_IDS, check)
+from ._lib import (ACT_IDS, GATE_IDS, MoeBaseGrads, MoeLinearShape, MoeLoraGrads, MoeResidual,
+                   MoeResidualGrads, MoeResidualParams, MoeSaved, MoeShape, MoeWeights, NORM_IDS,
+                   ROUTER_IDS, check)
 
 __all__ = [
     "Shape", "moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
@@ -35,7 +36,9 @@ __all__ = [
     "moe_grouped_lora_fwd_lean", "moe_grouped_lora_bwd_recompute", "moe_router_workspace_bytes",
     "moe_router_fwd", "moe_router_bwd", "moe_accumulate", "moe_merge_workspace_bytes",
     "moe_merge_lora", "Residual", "moe_residual_norm_workspace_bytes", "moe_residual_norm_fwd",
-    "moe_residual_norm_bwd", "moe_dropout", "kernel_timer", "ROUTER_IDS", "NORM_IDS", "GATE_IDS",
+    "moe_residual_norm_bwd", "moe_dropout", "LinearShape", "moe_linear_workspace_bytes",
+    "moe_linear_fwd", "moe_linear_bwd", "kernel_timer", "ROUTER_IDS", "NORM_IDS", "GATE_IDS",
+    "ACT_IDS",
     "library_path",
 ]
 
@@ -564,6 +567,69 @@ def moe_residual_norm_bwd(desc: Residual, dh_out, dx_out, h_out, y, params, stat
             _rng(rng, desc.dropout), int(site), _ptr(dh, rows, dt, "dh", optional=True),
             _ptr(dy, rows, dt, "dy", optional=True), ctypes.byref(g), wsp, wsb, _stream(stream)),
             "moe_residual_norm_bwd")
+
+
+@dataclass(frozen=True)
+class LinearShape:
+    """y = residual + dropout(act(x w^T + bias)): x [T, K], w [N, K], y [T, N].
+    act: "none", "relu", "silu", "gelu" or "gelu_tanh"."""
+    T: int
+    K: int
+    N: int
+    dtype: str = "bf16"       # "bf16", "f16" or "f32"
+    act: str = "none"
+    dropout: float = 0.0
+
+    @property
+    def torch_dtype(self) -> torch.dtype:
+        return _TORCH_DTYPES[self.dtype]
+
+    def c(self) -> MoeLinearShape:
+        return MoeLinearShape(self.T, self.K, self.N, _ABI_DTYPES[self.dtype], ACT_IDS[self.act],
+                              float(self.dropout))
+
+
+def moe_linear_workspace_bytes(shape: LinearShape):
+    """(forward, backward) workspace bytes for `shape`."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    check(_lib.load().moe_linear_workspace_bytes(ctypes.byref(shape.c()), ctypes.byref(f),
+                                                 ctypes.byref(b)), "moe_linear_workspace_bytes")
+    return f.value, b.value
+
+
+def moe_linear_fwd(shape: LinearShape, x, w, y, ws, bias=None, residual=None, pre=None, rng=None,
+                   site=0, stream=None):
+    """y = residual + dropout(act(z)), z = x w^T + bias. pre: z kept for the backward, or None.
+    y may be residual."""
+    T, K, N, dt = shape.T, shape.K, shape.N, shape.torch_dtype
+    _same_device(x, w, y, ws, bias, residual, pre, rng)
+    wsp, wsb = _ws(ws, moe_linear_workspace_bytes(shape)[0], "ws")
+    with _on_device(x):
+        check(_lib.load().moe_linear_fwd(
+            ctypes.byref(shape.c()), _ptr(x, (T, K), dt, "x"), _ptr(w, (N, K), dt, "w"),
+            _ptr(bias, (N,), dt, "bias", optional=True),
+            _ptr(residual, (T, N), dt, "residual", optional=True), _rng(rng, shape.dropout),
+            int(site), _ptr(y, (T, N), dt, "y"), _ptr(pre, (T, N), dt, "pre", optional=True), wsp,
+            wsb, _stream(stream)), "moe_linear_fwd")
+
+
+def moe_linear_bwd(shape: LinearShape, dy, x, w, pre, dx, dw, dbias, ws, rng=None, site=0,
+                   stream=None):
+    """Gradients of moe_linear_fwd from dy: dx, dw and dbias, any of them None (not wanted). pre is
+    the forward's, needed with an activation. The residual's gradient is dy itself."""
+    T, K, N, dt = shape.T, shape.K, shape.N, shape.torch_dtype
+    _same_device(dy, x, w, pre, dx, dw, dbias, ws, rng)
+    wsp, wsb = _ws(ws, moe_linear_workspace_bytes(shape)[1], "ws")
+    with _on_device(dy):
+        check(_lib.load().moe_linear_bwd(
+            ctypes.byref(shape.c()), _ptr(dy, (T, N), dt, "dy"),
+            _ptr(x, (T, K), dt, "x", optional=dw is None),
+            _ptr(w, (N, K), dt, "w", optional=dx is None),
+            _ptr(pre, (T, N), dt, "pre", optional=shape.act == "none"), _rng(rng, shape.dropout),
+            int(site), _ptr(dx, (T, K), dt, "dx", optional=True),
+            _ptr(dw, (N, K), dt, "dw", optional=True),
+            _ptr(dbias, (N,), dt, "dbias", optional=True), wsp, wsb, _stream(stream)),
+            "moe_linear_bwd")
 
 
 class kernel_timer:

@@ -16,8 +16,9 @@ KERNEL_IDS = {"route": 0, "permute": 1, "gather": 2, "gate_up_fwd": 3, "down_fwd
               "lora_side": 10, "lora_wgrad": 11, "unpermute": 12, "base_wgrad": 13,
               "router_fwd": 14, "router_bwd": 15, "accumulate": 16, "merge": 17,
               "dy_gather": 18, "dw_sum": 19, "row_scale": 20, "dropout": 21, "residual_norm": 22,
-              "residual_norm_bwd": 23}
+              "residual_norm_bwd": 23, "linear_fwd": 24, "linear_bwd": 25}
 NORM_IDS = {"none": 0, "rms": 1, "layer": 2}
+ACT_IDS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 GATE_IDS = {"none": 0, "channel": 1, "token": 2, "full": 3}
 
 EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
@@ -29,7 +30,8 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
            "moe_grouped_lora_combine_bwd", "moe_grouped_lora_fwd_gather",
            "moe_grouped_lora_combine_bwd_gather",
            "moe_dropout", "moe_residual_norm_workspace_bytes", "moe_residual_norm_fwd",
-           "moe_residual_norm_bwd",
+           "moe_residual_norm_bwd", "moe_linear_workspace_bytes", "moe_linear_fwd",
+           "moe_linear_bwd",
            "moe_status_str",
            "moe_last_error",
            "moe_kernel_timer_enable", "moe_kernel_timer_select", "moe_kernel_timer_reset",
@@ -70,6 +72,11 @@ class MoeResidualParams(ctypes.Structure):
 
 class MoeResidualGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dw_post", "db_post", "dgate", "dw_pre", "db_pre")]
+
+
+class MoeLinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "dtype", "act")] + \
+               [("dropout", ctypes.c_float)]
 
 
 _lib = None
@@ -155,6 +162,13 @@ def load() -> ctypes.CDLL:
                                        ctypes.POINTER(MoeResidualParams), P, P, ctypes.c_int64, P,
                                        P, ctypes.POINTER(MoeResidualGrads), P, ctypes.c_size_t,
                                        P]),
+        "moe_linear_workspace_bytes": (st, [ctypes.POINTER(MoeLinearShape),
+                                            ctypes.POINTER(ctypes.c_size_t),
+                                            ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_linear_fwd": (st, [ctypes.POINTER(MoeLinearShape), P, P, P, P, P, ctypes.c_int64, P,
+                                P, P, ctypes.c_size_t, P]),
+        "moe_linear_bwd": (st, [ctypes.POINTER(MoeLinearShape), P, P, P, P, P, ctypes.c_int64, P,
+                                P, P, P, ctypes.c_size_t, P]),
         "moe_status_str": (ctypes.c_char_p, [st]),
         "moe_last_error": (ctypes.c_char_p, []),
         "moe_kernel_timer_enable": (st, [I32]),

@@ -1030,6 +1030,126 @@ moe_status moe_residual_norm_bwd(const moe_residual* desc, const void* dh_out, c
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_residual_norm_bwd");
 }
 
+namespace {
+
+moe_status check_linear(const moe_linear_shape* s) {
+  if (!s) return fail(MOE_ERR_INVALID_ARG, "null shape");
+  if (s->T < 1 || s->K < 1 || s->N < 1)
+    return fail(MOE_ERR_INVALID_ARG, "T, K and N must be >= 1");
+  if (!known_dtype(s->dtype)) return fail(MOE_ERR_INVALID_ARG, "unknown dtype");
+  if (s->act < MOE_ACT_NONE || s->act > MOE_ACT_GELU_TANH)
+    return fail(MOE_ERR_INVALID_ARG, "unknown activation " + std::to_string(s->act));
+  if (s->K % 8 != 0 || s->N % 8 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "K and N must be multiples of 8");
+  const int64_t e = esize(s->dtype);
+  if (int64_t(s->T) * std::max(s->K, s->N) > (int64_t(1) << 35) / e)
+    return fail(MOE_ERR_INVALID_ARG, "activation tensors larger than 32 GiB");
+  if (int64_t(s->N) * s->K * e >= (int64_t(1) << 31))
+    return fail(MOE_ERR_INVALID_ARG, "w must be smaller than 2 GiB");
+  return MOE_OK;
+}
+
+moe::LinearDims linear_dims(const moe_linear_shape* s) { return {s->T, s->K, s->N, s->dtype}; }
+
+bool drops(const moe_linear_shape* s) {
+  return static_cast<double>(s->dropout) * 65536.0 + 0.5 >= 1.0;
+}
+
+}  // namespace
+
+moe_status moe_linear_workspace_bytes(const moe_linear_shape* shape, size_t* fwd_ws,
+                                      size_t* bwd_ws) {
+  moe_status st = check_linear(shape);
+  if (st != MOE_OK) return st;
+  if (fwd_ws) *fwd_ws = moe::linear_fwd_ws_bytes(linear_dims(shape));
+  if (bwd_ws)
+    *bwd_ws = moe::linear_bwd_ws_bytes(linear_dims(shape),
+                                       shape->act != MOE_ACT_NONE || drops(shape));
+  return MOE_OK;
+}
+
+moe_status moe_linear_fwd(const moe_linear_shape* shape, const void* x, const void* w,
+                          const void* bias, const void* residual, const int64_t* rng,
+                          int64_t site, void* y, void* pre, void* ws, size_t ws_bytes,
+                          void* stream) {
+  moe_status st = check_linear(shape);
+  if (st != MOE_OK) return st;
+  moe::LinearEpi epi{};
+  if ((st = make_drop(shape->dropout, rng, site, &epi.drop)) != MOE_OK) return st;
+  CHECK_PTR(x);
+  CHECK_PTR(w);
+  CHECK_PTR(y);
+  CHECK_ROWS(x);
+  CHECK_ROWS(w);
+  CHECK_ROWS(bias);
+  CHECK_ROWS(residual);
+  CHECK_ROWS(y);
+  CHECK_ROWS(pre);
+  CHECK_ROWS(ws);
+  const moe::LinearDims d = linear_dims(shape);
+  const size_t need = moe::linear_fwd_ws_bytes(d);
+  if (need > 0) CHECK_PTR(ws);
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "linear workspace needs " + std::to_string(need) + " bytes");
+  const int64_t e = esize(d.dtype), out = int64_t(d.T) * d.N * e;
+  st = check_ranges({{y, out, "y"}, {pre, out, "pre"}, {need ? ws : nullptr, int64_t(need), "ws"}},
+                    {{x, int64_t(d.T) * d.K * e, "x"}, {w, int64_t(d.N) * d.K * e, "w"},
+                     {bias, d.N * e, "bias"}, {residual, out, "residual"},
+                     {epi.drop.thr ? rng : nullptr, 16, "rng"}},
+                    y, residual);
+  if (st != MOE_OK) return st;
+  epi.bias = bias;
+  epi.residual = residual;
+  epi.pre = pre;
+  epi.y = y;
+  epi.act = shape->act;
+  hipError_t err = moe::launch_linear_fwd(d, x, w, epi, ws, as_stream(stream), moe::active_timer());
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "moe_linear_fwd");
+}
+
+moe_status moe_linear_bwd(const moe_linear_shape* shape, const void* dy, const void* x,
+                          const void* w, const void* pre, const int64_t* rng, int64_t site,
+                          void* dx, void* dw, void* dbias, void* ws, size_t ws_bytes,
+                          void* stream) {
+  moe_status st = check_linear(shape);
+  if (st != MOE_OK) return st;
+  moe::LinearEpi epi{};
+  if ((st = make_drop(shape->dropout, rng, site, &epi.drop)) != MOE_OK) return st;
+  CHECK_PTR(dy);
+  if (dw) CHECK_PTR(x);
+  if (dx) CHECK_PTR(w);
+  if (shape->act != MOE_ACT_NONE) CHECK_PTR(pre);
+  if (!dx && !dw && !dbias) return fail(MOE_ERR_INVALID_ARG, "no output");
+  CHECK_ROWS(dy);
+  CHECK_ROWS(x);
+  CHECK_ROWS(w);
+  CHECK_ROWS(pre);
+  CHECK_ROWS(dx);
+  CHECK_ROWS(dw);
+  CHECK_ROWS(dbias);
+  CHECK_ROWS(ws);
+  const moe::LinearDims d = linear_dims(shape);
+  const size_t need =
+      moe::linear_bwd_ws_bytes(d, shape->act != MOE_ACT_NONE || epi.drop.thr != 0);
+  if (need > 0) CHECK_PTR(ws);
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "linear workspace needs " + std::to_string(need) + " bytes");
+  const int64_t e = esize(d.dtype), out = int64_t(d.T) * d.N * e, in = int64_t(d.T) * d.K * e,
+                wb = int64_t(d.N) * d.K * e;
+  st = check_ranges({{dx, in, "dx"}, {dw, wb, "dw"}, {dbias, d.N * e, "dbias"},
+                     {need ? ws : nullptr, int64_t(need), "ws"}},
+                    {{dy, out, "dy"}, {dw ? x : nullptr, in, "x"}, {dx ? w : nullptr, wb, "w"},
+                     {shape->act != MOE_ACT_NONE ? pre : nullptr, out, "pre"},
+                     {epi.drop.thr ? rng : nullptr, 16, "rng"}},
+                    nullptr, nullptr);
+  if (st != MOE_OK) return st;
+  epi.pre = const_cast<void*>(pre);
+  epi.act = shape->act;
+  hipError_t err = moe::launch_linear_bwd(d, dy, x, w, epi, dx, dw, dbias, ws, as_stream(stream),
+                                          moe::active_timer());
+  return err == hipSuccess ? MOE_OK : hip_fail(err, "moe_linear_bwd");
+}
+
 moe_status moe_kernel_timer_enable(int32_t on) {
   TimerState& t = timer();
   std::lock_guard<std::mutex> lk(t.mu);

@@ -8,6 +8,7 @@
 
 #include "device_common.h"
 #include "launch.h"
+#include "linear.h"
 
 namespace moe {
 
@@ -16,8 +17,14 @@ namespace {
 enum Mode { GROUP_M = 0, GROUP_K = 1, GROUP_KV = 2 };
 // EPI_STORE_F32: float32 output (router logits); EPI_ADD: out = src + result
 // with src = aux when given (merged export: W + s B A) else out itself (an
-// accumulate); the sum formed in float32, one rounding.
-enum Epi { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_BWD = 2, EPI_STORE_F32 = 3, EPI_ADD = 4 };
+// accumulate); the sum formed in float32, one rounding. EPI_LINEAR: one dense
+// product instead of a group per expert: no tile list or offsets, E slices of
+// kchunk along the reduction, the output through linear_finish8 (GROUP_M) or
+// stored (GROUP_K), or float32 partials [E][M][N] when E > 1.
+enum Epi {
+  EPI_STORE = 0, EPI_SWIGLU = 1, EPI_SWIGLU_BWD = 2, EPI_STORE_F32 = 3, EPI_ADD = 4,
+  EPI_LINEAR = 5
+};
 
 struct Opnd {
   const void* ptr;
@@ -71,6 +78,9 @@ struct GemmArgs {
   const float* roww;
   float* dwp;
   int dwp_slots;
+  // EPI_LINEAR: M output rows, reduction length K[0] in slices of kchunk
+  int kchunk;
+  LinearEpi lin;
 };
 
 // Spread `total` logical tiles over the 8 XCDs so that each XCD works on a
@@ -93,6 +103,22 @@ __device__ __forceinline__ int group_tile(const int4* tiles, int L, int ntn, int
   const int rem = L - gs * ntn;
   n_tile = rem / gsz;
   return gs + rem % gsz;
+}
+
+// EPI_LINEAR's slice, N tile and first row of this block: the tile lists' raster (up to 8 M tiles
+// swept across the N tiles) without a list. False: a block past the last tile.
+__device__ __forceinline__ bool dense_tile(const GemmArgs& p, int bm, int& e, int& n_tile,
+                                           int& m0) {
+  const int per = p.ntm * p.ntn, total = p.E * per;
+  if (static_cast<int>(blockIdx.x) >= total) return false;
+  const int L = xcd_remap(blockIdx.x, total);
+  e = L / per;
+  const int at = L - e * per;
+  const int gs = at / (kTileGroup * p.ntn) * kTileGroup, gsz = min(kTileGroup, p.ntm - gs);
+  const int rem = at - gs * p.ntn;
+  n_tile = rem / gsz;
+  m0 = (gs + rem % gsz) * bm;
+  return true;
 }
 
 // One operand of one tile: where element (mn, k) lives and which ones exist.
@@ -641,9 +667,19 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
   // waves sit on different SIMDs (wave w runs on SIMD w % 4).
   const int wm = wave / WAVES_N, wn = (wave % WAVES_N + wm) % WAVES_N;
 
+  constexpr bool DENSE = EPI == EPI_LINEAR;
+  static_assert(!DENSE || (!PAIRED && GATH == 0 && MODE != GROUP_KV), "dense products are plain");
   int e, n_tile, rows, m0 = 0, krows = 0;
+  int kbeg = 0, K0 = p.K[0];  // GROUP_M: this block's part of the reduction
   int64_t row0;
-  if (MODE == GROUP_M) {
+  if constexpr (DENSE) {
+    if (!dense_tile(p, BM, e, n_tile, m0)) return;
+    rows = min(BM, p.M - m0);
+    kbeg = e * p.kchunk;
+    K0 = min(p.kchunk, p.K[0] - kbeg);
+    row0 = MODE == GROUP_M ? m0 : kbeg;
+    krows = K0;
+  } else if (MODE == GROUP_M) {
     const int mtot = *p.ntiles;
     const int total = mtot * p.ntn;
     if (static_cast<int>(blockIdx.x) >= total) return;
@@ -684,11 +720,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
     vb.ld = B.ld; vb.kcontig = B.kcontig; vb.vec = B.vec;
     int64_t abytes, bbytes;
     if (MODE == GROUP_M) {
-      const int K = p.K[seg];
-      va.base = static_cast<const bf16_t*>(A.ptr) + row0 * A.ld;
+      const int K = DENSE && seg == 0 ? K0 : p.K[seg];
+      va.base = static_cast<const bf16_t*>(A.ptr) + row0 * A.ld + kbeg;
       va.klim = K;
       va.mn_lim = rows;
-      abytes = static_cast<int64_t>(rows) * A.ld * 2;
+      abytes = (static_cast<int64_t>(rows) * A.ld - kbeg) * 2;
       if (A.rows) {
         va.base = static_cast<const bf16_t*>(A.ptr);
         va.grow = A.rows + row0;
@@ -706,11 +742,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
         vb.mn_lim = BN;
         bbytes = static_cast<int64_t>(2) * p.I * B.ld * 2;
       } else if (B_KC) {
-        vb.base = wb + static_cast<int64_t>(n0) * B.ld;
+        vb.base = wb + static_cast<int64_t>(n0) * B.ld + kbeg;
         vb.mn_lim = p.N - n0;
-        bbytes = static_cast<int64_t>(p.N - n0) * B.ld * 2;
+        bbytes = (static_cast<int64_t>(p.N - n0) * B.ld - kbeg) * 2;
       } else {
-        vb.base = wb + n0;
+        vb.base = wb + static_cast<int64_t>(kbeg) * B.ld + n0;
         vb.mn_lim = p.N - n0;
         bbytes = static_cast<int64_t>(K) * B.ld * 2 - static_cast<int64_t>(n0) * 2;
       }
@@ -747,7 +783,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
     pb1 = pb0;
   }
 
-  const int nk0 = MODE == GROUP_M ? (p.K[0] + BK - 1) / BK : (krows + BK - 1) / BK;
+  const int nk0 = MODE == GROUP_M ? (K0 + BK - 1) / BK : (krows + BK - 1) / BK;
   const int nk1 = MODE == GROUP_M ? (p.K[1] + BK - 1) / BK : 0;
   const int nk = nk0 + nk1;
   const bool dma0 = pa0.vec && pb0.vec, dma1 = pa1.vec && pb1.vec;
@@ -983,7 +1019,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
       read_frags(0, 0, 0);
     }
     // k-steps of the last tile holding valid k (the rest of it is zeros)
-    const int klast = MODE == GROUP_M ? (nk1 > 0 ? p.K[1] - (nk1 - 1) * BK : p.K[0] - (nk0 - 1) * BK)
+    const int klast = MODE == GROUP_M ? (nk1 > 0 ? p.K[1] - (nk1 - 1) * BK : K0 - (nk0 - 1) * BK)
                                       : krows - (nk0 - 1) * BK;
     const int ns_last = (klast + 15) / 16;
     // One k tile. PAR: the tile's LDS slot when known at compile time (-1:
@@ -1076,7 +1112,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
       const int nkf = nk - 1;  // full tiles before the last
       // Tiles 1..C are clean: the tile each stages (it + 2) is a whole tile
       // of the main segment (K tail tile excluded).
-      const int last_clean = MODE == GROUP_M ? nk0 - 1 - (p.K[0] % BK != 0 ? 1 : 0) : -1;
+      const int last_clean = MODE == GROUP_M ? nk0 - 1 - (K0 % BK != 0 ? 1 : 0) : -1;
       const int C = min(nkf - 1, last_clean - 2);
       if (nkf > 0) ktile(0, Rt(), mfmac, No(), Yes(), No());
       int it = 1;
@@ -1377,6 +1413,20 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
           continue;
         }
         if (m_local >= rows) continue;
+        if constexpr (DENSE) {
+          if (col >= p.N) continue;  // N is a multiple of 8
+          const int64_t row = m0 + m_local;
+          if (p.E > 1) {
+            Row8<float> o;
+            o.set(v);
+            o.store(static_cast<float*>(p.out) + (static_cast<int64_t>(e) * p.M + row) * p.N + col);
+          } else if (MODE == GROUP_M) {
+            linear_finish8<std::conditional_t<F16, f16_t, bf16_t>>(p.lin, row, col, p.N, v);
+          } else {
+            store8<F16>(static_cast<bf16_t*>(p.out) + row * p.N + col, v);
+          }
+          continue;
+        }
         if (EPI == EPI_STORE_F32) {
           // GROUP_M: router logits; GROUP_K: split-K partial weight gradients
           float* rp = MODE == GROUP_M

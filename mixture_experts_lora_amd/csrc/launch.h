@@ -153,6 +153,14 @@ struct DropArgs {
   float scale;         // of the kept elements
 };
 
+// What a dense product's output goes through (null or 0: left out).
+struct LinearEpi {
+  const void *bias, *residual;
+  void *pre, *y;
+  int32_t act;
+  DropArgs drop;
+};
+
 hipError_t launch_dropout(int dtype, int64_t n, const DropArgs& d, const void* src, void* dst,
                           hipStream_t s, KernelTimer* tm);
 
@@ -181,5 +189,19 @@ int64_t residual_bwd_groups(int T, int H);
 hipError_t launch_residual_fwd(int dtype, const ResidualArgs& a, hipStream_t s, KernelTimer* tm);
 hipError_t launch_residual_bwd(int dtype, const ResidualBwdArgs& a, hipStream_t s,
                                KernelTimer* tm);
+
+// ---- linear: x [T, K], w [N, K], y [T, N]
+struct LinearDims {
+  int32_t T, K, N, dtype;
+};
+size_t linear_fwd_ws_bytes(const LinearDims& d);
+// form_dz: dz differs from dy (an activation or dropout)
+size_t linear_bwd_ws_bytes(const LinearDims& d, bool form_dz);
+hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* w,
+                             const LinearEpi& epi, void* ws, hipStream_t s, KernelTimer* tm);
+// epi: act and drop of the forward; pre its kept product. dx, dw, db: null when not wanted.
+hipError_t launch_linear_bwd(const LinearDims& d, const void* dy, const void* x, const void* w,
+                             const LinearEpi& epi, void* dx, void* dw, void* db, void* ws,
+                             hipStream_t s, KernelTimer* tm);
 
 }  // namespace moe

@@ -1,0 +1,511 @@
+// Dense linear operator of the residual stream, and its backward:
+//
+//   z = x w^T + bias        x [T, K], w [N, K]
+//   y = residual + dropout(act(z))
+//   dz = act'(z) dropout(dy)   (rounded to the layer dtype, as the experts' dH is: it feeds MFMA)
+//   dx = dz w    dw = dz^T x    dbias = sum_t dz (summed before the rounding)
+//
+// Many tokens: MFMA tiles (gemm16 for the 16-bit types, linear_f32_kernel for float32) whose
+// epilogue applies bias, activation, dropout and residual to the float32 product, so z and y move
+// once. Where a product has too few tiles to fill the card, its reduction is cut into slices that
+// are summed in slice order by a second kernel with the same epilogue: no atomics, so results are
+// the same run to run. Up to 16 tokens the product is bound by reading w once, and
+// linear_few_kernel streams it.
+#include <algorithm>
+#include <type_traits>
+
+#include "gemm16.h"
+
+namespace moe {
+
+namespace {
+
+#define MOE_TRY(x)                       \
+  do {                                   \
+    hipError_t err_ = (x);               \
+    if (err_ != hipSuccess) return err_; \
+  } while (0)
+
+// ------------------------------------------------------------------ float32 product
+// 128 x 128 tiles, four waves of 64 x 64, 16 deep, two LDS slots filled through registers.
+// v_mfma_f32_32x32x2_f32 takes 64 cycles for 4 KFLOP, so the product is bound by MFMA and the
+// plain loop below keeps it fed. LDS holds both operands as [k][mn]; a row of 132 floats puts the
+// four k-quads that a k-contiguous fill writes for 16 rows on all 64 banks.
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+template <bool KC>
+__device__ __forceinline__ void f32_fetch(const float* base, int64_t ld, int mn0, int mn_lim,
+                                          int64_t k0, int64_t k_end, float4 (&r)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int idx = threadIdx.x + i * 256;
+    const int mn = mn0 + (KC ? idx / 4 : idx % 32 * 4);
+    const int64_t k = k0 + (KC ? idx % 4 * 4 : idx / 32);
+    r[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mn < mn_lim && k < k_end)
+      r[i] = *reinterpret_cast<const float4*>(base + (KC ? mn * ld + k : k * ld + mn));
+  }
+}
+
+template <bool KC>
+__device__ __forceinline__ void f32_put(float (&s)[16][132], const float4 (&r)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int idx = threadIdx.x + i * 256;
+    if (KC) {
+      const int mn = idx / 4, k = idx % 4 * 4;
+      s[k][mn] = r[i].x;
+      s[k + 1][mn] = r[i].y;
+      s[k + 2][mn] = r[i].z;
+      s[k + 3][mn] = r[i].w;
+    } else {
+      *reinterpret_cast<float4*>(&s[idx / 32][idx % 32 * 4]) = r[i];
+    }
+  }
+}
+
+// out(m, n) = sum_k a(m, k) b(n, k) over the block's slice; M, N, K[0], kchunk, E, lin and out as
+// EPI_LINEAR's. EPI: the output goes through linear_finish8, otherwise it is stored.
+template <bool A_KC, bool B_KC, bool EPI>
+__global__ __launch_bounds__(256, 2) void linear_f32_kernel(GemmArgs p) {
+  constexpr int WN = 64;
+  union Smem {
+    float tile[2][2][16][132];
+    char slab[4][32 * WN * 4];
+  };
+  __shared__ __attribute__((aligned(1024))) Smem sm;
+  int e, n_tile, m0;
+  if (!dense_tile(p, 128, e, n_tile, m0)) return;
+  const int n0 = n_tile * 128, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = wave >> 1, wn = wave & 1;
+  const int64_t kbeg = static_cast<int64_t>(e) * p.kchunk;
+  const int64_t kend = min(kbeg + p.kchunk, static_cast<int64_t>(p.K[0]));
+  const float* A = static_cast<const float*>(p.a[0].ptr);
+  const float* B = static_cast<const float*>(p.b[0].ptr);
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  float4 ra[2], rb[2];
+  f32_fetch<A_KC>(A, p.a[0].ld, m0, p.M, kbeg, kend, ra);
+  f32_fetch<B_KC>(B, p.b[0].ld, n0, p.N, kbeg, kend, rb);
+  f32_put<A_KC>(sm.tile[0][0], ra);
+  f32_put<B_KC>(sm.tile[0][1], rb);
+  __syncthreads();
+  int slot = 0;
+  for (int64_t k0 = kbeg; k0 < kend; k0 += 16) {
+    const bool more = k0 + 16 < kend;
+    if (more) {
+      f32_fetch<A_KC>(A, p.a[0].ld, m0, p.M, k0 + 16, kend, ra);
+      f32_fetch<B_KC>(B, p.b[0].ld, n0, p.N, k0 + 16, kend, rb);
+    }
+    const auto& sa = sm.tile[slot][0];
+    const auto& sb = sm.tile[slot][1];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      float fa[2], fb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        fa[i] = sa[2 * s + (lane >> 5)][wm * 64 + i * 32 + (lane & 31)];
+        fb[i] = sb[2 * s + (lane >> 5)][wn * 64 + i * 32 + (lane & 31)];
+      }
+      // b as the MFMA's A operand: a lane ends with consecutive columns of one row
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
+    slot ^= 1;
+    if (more) {
+      // the other slot was last read before the previous barrier
+      f32_put<A_KC>(sm.tile[slot][0], ra);
+      f32_put<B_KC>(sm.tile[slot][1], rb);
+    }
+    __syncthreads();
+  }
+  char* slab = sm.slab[wave];
+#pragma unroll
+  for (int mi = 0; mi < 2; ++mi) {
+    if (mi) wave_lds_sync();
+#pragma unroll
+    for (int ni = 0; ni < 2; ++ni)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        f32x4 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = acc[mi][ni][4 * q + j];
+        *reinterpret_cast<f32x4*>(slab + slab_off<WN>(lane & 31, ni * 8 + 2 * q + (lane >> 5))) = v;
+      }
+    wave_lds_sync();
+#pragma unroll
+    for (int pass = 0; pass < 4; ++pass) {
+      const int r = pass * 8 + lane / 8, s = lane % 8;
+      const int row = m0 + wm * 64 + mi * 32 + r, col = n0 + wn * 64 + 8 * s;
+      float v[8];
+      read8_interleaved<WN>(slab, r, s, v);
+      if (row >= p.M || col >= p.N) continue;
+      if (EPI && p.E == 1) {
+        linear_finish8<float>(p.lin, row, col, p.N, v);
+      } else {
+        Row8<float> o;
+        o.set(v);
+        o.store(static_cast<float*>(p.out) + (static_cast<int64_t>(e) * p.M + row) * p.N + col);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ sums over slices
+// The slices' partials [E][M][N] in slice order, then the epilogue: eight columns a thread.
+template <typename Elem>
+__global__ __launch_bounds__(256) void linear_sum_kernel(const float* __restrict__ part, int E,
+                                                         int64_t MN, int N, LinearEpi epi) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= MN) return;
+  float v[8] = {};
+  for (int e = 0; e < E; ++e) {
+    Row8<float> r;
+    float f[8];
+    r.load(part + e * MN + i);
+    r.get(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += f[j];
+  }
+  const int64_t row = i / N;
+  linear_finish8<Elem>(epi, row, static_cast<int>(i - row * N), N, v);
+}
+
+// ------------------------------------------------------------------ few tokens
+// T <= TT <= 16: bound by reading w once. A block owns eight columns (eight rows of w) and its
+// four waves split K in 16-byte pieces a lane, so a wave has eight independent streams of w in
+// flight; x is small and comes from cache. The lanes' sums meet by wave reductions, the waves' in
+// LDS, in a fixed order.
+template <typename Elem, int TT>
+__global__ __launch_bounds__(256) void linear_few_kernel(const Elem* __restrict__ x,
+                                                         const Elem* __restrict__ w, int T, int K,
+                                                         int N, LinearEpi epi) {
+  __shared__ float red[4][TT * 8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, n0 = blockIdx.x * 8;
+  float acc[8][TT];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[i][t] = 0.f;
+  for (int k = threadIdx.x * 8; k < K; k += 256 * 8) {
+    Row8<Elem> rw[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rw[i].load(w + static_cast<int64_t>(n0 + i) * K + k);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      if (t >= T) continue;  // uniform (a break would leave the loop rolled, its sums in memory)
+      Row8<Elem> rx;
+      float fx[8];
+      rx.load(x + static_cast<int64_t>(t) * K + k);
+      rx.get(fx);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float fw[8];
+        rw[i].get(fw);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][t] += fx[j] * fw[j];
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float s = wave_sum(acc[i][t]);
+      if (lane == 0) red[wave][t * 8 + i] = s;
+    }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t >= T) return;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = (red[0][t * 8 + i] + red[1][t * 8 + i]) + (red[2][t * 8 + i] + red[3][t * 8 + i]);
+  linear_finish8<Elem>(epi, t, n0, N, v);
+}
+
+// ------------------------------------------------------------------ dz and dbias
+// 512 columns a block, its four waves on different rows; rows are dealt to gridDim.y groups whose
+// column sums (float32, in row order) linear_colsum_kernel adds. dz null: only the sums.
+template <typename Elem>
+__global__ __launch_bounds__(256) void linear_dz_kernel(const Elem* __restrict__ dy, int T, int N,
+                                                        LinearEpi epi, Elem* __restrict__ dz,
+                                                        float* __restrict__ part) {
+  __shared__ float red[4][512 + 8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 512 + lane * 8;
+  const bool live = col < N;
+  const DropKey key = drop_key(epi.drop);
+  float sum[8] = {};
+  for (int64_t t = blockIdx.y * 4 + wave; live && t < T; t += gridDim.y * 4) {
+    const int64_t at = t * N + col;
+    Row8<Elem> r, rz;
+    float v[8];
+    r.load(dy + at);
+    if (epi.act != MOE_ACT_NONE) rz.load(static_cast<const Elem*>(epi.pre) + at);
+    r.get(v);
+    if (epi.drop.thr) {
+      const uint32_t bits = drop_bits(epi.drop, key, static_cast<uint64_t>(at) / 8);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (bits >> j) & 1u ? v[j] * epi.drop.scale : 0.f;
+    }
+    if (epi.act != MOE_ACT_NONE) {
+      float z[8];
+      rz.get(z);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= act_slope(z[j], epi.act);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    if (dz) {
+      r.set(v);
+      r.store(dz + at);
+    }
+  }
+  if (!part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) red[wave][lane * 8 + j] = sum[j];
+  __syncthreads();
+  for (int c = threadIdx.x; c < 512; c += 256) {
+    const int n = blockIdx.x * 512 + c;
+    if (n < N)
+      part[static_cast<int64_t>(blockIdx.y) * N + n] =
+          (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+  }
+}
+
+// 32 columns a block: 32 rows of lanes walk every 32nd group, then the 32 sums, in order.
+template <typename Elem>
+__global__ __launch_bounds__(1024) void linear_colsum_kernel(const float* __restrict__ part,
+                                                             int groups, int N,
+                                                             Elem* __restrict__ db) {
+  __shared__ float red[32][33];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, col = blockIdx.x * 32 + cx;
+  float a = 0.f;
+  if (col < N)
+    for (int g = ry; g < groups; g += 32) a += part[static_cast<int64_t>(g) * N + col];
+  red[ry][cx] = a;
+  __syncthreads();
+  if (ry != 0 || col >= N) return;
+  a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) a += red[i][cx];
+  db[col] = from_f32<Elem>(a);
+}
+
+// ------------------------------------------------------------------ host side
+constexpr int kFewTokens = 16;
+
+// One product of M x N outputs over K: tile shape, and slices of the reduction.
+enum Tile { TILE_256, TILE_128x64, TILE_128x256, TILE_F32 };
+struct Product {
+  Tile tile;
+  int bm, bn, ntm, ntn, E, kchunk;
+  size_t part_bytes;  // 0: one slice, no partials
+};
+
+Product plan(int dtype, bool reduce_rows, int64_t M, int64_t N, int64_t K) {
+  Product q{};
+  auto with = [&](Tile t, int bm, int bn) {
+    q.tile = t;
+    q.bm = bm;
+    q.bn = bn;
+    q.ntm = ceil_div(M, bm);
+    q.ntn = ceil_div(N, bn);
+  };
+  int fill = 512, least = 256;
+  if (dtype == MOE_F32) {
+    with(TILE_F32, 128, 128);
+    least = 128;
+  } else if (reduce_rows) {
+    with(TILE_128x256, 128, 256);
+  } else {
+    with(TILE_256, 256, 256);
+    if (static_cast<int64_t>(q.ntm) * q.ntn < 192) with(TILE_128x64, 128, 64);
+    else fill = 0;
+  }
+  const int64_t tiles = static_cast<int64_t>(q.ntm) * q.ntn;
+  int64_t E = std::max<int64_t>(1, std::min<int64_t>(fill / tiles, K / least));
+  q.kchunk = static_cast<int>((((K + E - 1) / E) + 63) / 64 * 64);
+  q.E = ceil_div(K, q.kchunk);
+  q.part_bytes = q.E > 1 ? static_cast<size_t>(q.E) * M * N * sizeof(float) : 0;
+  return q;
+}
+
+GemmArgs dense_args(const Product& q, int dtype, int64_t M, int64_t N, int64_t K) {
+  GemmArgs a{};
+  a.a[1] = none();
+  a.b[1] = none();
+  a.K[0] = static_cast<int>(K);
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.E = q.E;
+  a.ntm = q.ntm;
+  a.ntn = q.ntn;
+  a.kchunk = q.kchunk;
+  a.scale = 1.0f;
+  a.dtype = dtype;
+  return a;
+}
+
+// out = a b^T through epi (epi.y is the output); a is [M, K]; b is [N, K], or [K, N] when !B_KC.
+template <bool B_KC>
+hipError_t product(const Product& q, GemmArgs& a, const LinearEpi& epi, void* part, hipStream_t s) {
+  a.lin = epi;
+  a.out = part;
+  const int grid = q.E * q.ntm * q.ntn;
+  switch (q.tile) {
+    case TILE_256:
+      MOE_TRY(launch(GEMM16(a.dtype, 256, 256, 128, 64, 64, 2, 1, GROUP_M, EPI_LINEAR, false, true, B_KC, 1),
+                     grid, a, s, 512));
+      break;
+    case TILE_128x64:
+      MOE_TRY(launch(GEMM16(a.dtype, 128, 64, 32, 64, 64, 3, 2, GROUP_M, EPI_LINEAR, false, true, B_KC, 0),
+                     grid, a, s));
+      break;
+    case TILE_F32:
+      MOE_TRY(launch(linear_f32_kernel<true, B_KC, true>, grid, a, s));
+      break;
+    default: return hipErrorInvalidValue;
+  }
+  if (q.E == 1) return hipSuccess;
+  return by_type(a.dtype, [&](auto tag) {
+    const int64_t MN = static_cast<int64_t>(a.M) * a.N;
+    hipLaunchKernelGGL(linear_sum_kernel<decltype(tag)>,
+                       dim3(static_cast<unsigned>((MN / 8 + 255) / 256)), dim3(256), 0, s,
+                       static_cast<const float*>(part), q.E, MN, a.N, epi);
+    return hipGetLastError();
+  });
+}
+
+// dw [N, K] = dz^T x: the reduction runs over the rows of both.
+hipError_t product_rows(const Product& q, GemmArgs& a, void* out, void* part, hipStream_t s) {
+  a.out = q.E > 1 ? part : out;
+  const int grid = q.E * q.ntm * q.ntn;
+  if (a.dtype == MOE_F32)
+    MOE_TRY(launch(linear_f32_kernel<false, false, false>, grid, a, s));
+  else
+    MOE_TRY(launch(GEMM16(a.dtype, 128, 256, 64, 128, 32, 3, 2, GROUP_K, EPI_LINEAR, false, false, false, 0),
+                   grid, a, s));
+  if (q.E == 1) return hipSuccess;
+  LinearEpi epi{};
+  epi.y = out;
+  return by_type(a.dtype, [&](auto tag) {
+    const int64_t MN = static_cast<int64_t>(a.M) * a.N;
+    hipLaunchKernelGGL(linear_sum_kernel<decltype(tag)>,
+                       dim3(static_cast<unsigned>((MN / 8 + 255) / 256)), dim3(256), 0, s,
+                       static_cast<const float*>(part), q.E, MN, a.N, epi);
+    return hipGetLastError();
+  });
+}
+
+template <typename Elem>
+hipError_t few_tokens(const LinearDims& d, const void* x, const void* w, const LinearEpi& epi,
+                      hipStream_t s) {
+  auto go = [&](auto tt) {
+    hipLaunchKernelGGL((linear_few_kernel<Elem, decltype(tt)::value>), dim3(d.N / 8), dim3(256), 0,
+                       s, static_cast<const Elem*>(x), static_cast<const Elem*>(w), d.T, d.K, d.N,
+                       epi);
+    return hipGetLastError();
+  };
+  if (d.T == 1) return go(std::integral_constant<int, 1>());
+  if (d.T <= 2) return go(std::integral_constant<int, 2>());
+  if (d.T <= 4) return go(std::integral_constant<int, 4>());
+  if (d.T <= 8) return go(std::integral_constant<int, 8>());
+  return go(std::integral_constant<int, 16>());
+}
+
+inline int dz_groups(const LinearDims& d) {
+  return std::min<int>(ceil_div(d.T, 4), std::max<int>(1, 768 / ceil_div(d.N, 512)));
+}
+
+struct BwdPlan {
+  Product dx, dw;
+  size_t dz_bytes, part_bytes;
+};
+
+BwdPlan bwd_plan(const LinearDims& d, bool form_dz) {
+  BwdPlan b{};
+  b.dx = plan(d.dtype, false, d.T, d.K, d.N);
+  b.dw = plan(d.dtype, true, d.N, d.K, d.T);
+  const size_t es = d.dtype == MOE_F32 ? 4 : 2;
+  b.dz_bytes = form_dz ? align_up(static_cast<size_t>(d.T) * d.N * es) : 0;
+  // dbias's, dx's and dw's partials are used one after the other
+  b.part_bytes = std::max({b.dx.part_bytes, b.dw.part_bytes,
+                           static_cast<size_t>(dz_groups(d)) * d.N * sizeof(float)});
+  return b;
+}
+
+}  // namespace
+
+size_t linear_fwd_ws_bytes(const LinearDims& d) {
+  if (d.T <= kFewTokens) return 0;
+  return plan(d.dtype, false, d.T, d.N, d.K).part_bytes;
+}
+
+size_t linear_bwd_ws_bytes(const LinearDims& d, bool form_dz) {
+  const BwdPlan b = bwd_plan(d, form_dz);
+  return b.dz_bytes + b.part_bytes;
+}
+
+hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* w,
+                             const LinearEpi& epi, void* ws, hipStream_t s, KernelTimer* tm) {
+  TimedScope ts(tm, MOE_K_LINEAR_FWD, s);
+  if (d.T <= kFewTokens)
+    return by_type(d.dtype, [&](auto tag) { return few_tokens<decltype(tag)>(d, x, w, epi, s); });
+  const Product q = plan(d.dtype, false, d.T, d.N, d.K);
+  GemmArgs a = dense_args(q, d.dtype, d.T, d.N, d.K);
+  a.a[0] = opnd(x, 0, d.K, 1, true);
+  a.b[0] = opnd(w, 0, d.K, 1, true);
+  return product<true>(q, a, epi, ws, s);
+}
+
+hipError_t launch_linear_bwd(const LinearDims& d, const void* dy, const void* x, const void* w,
+                             const LinearEpi& epi, void* dx, void* dw, void* db, void* ws,
+                             hipStream_t s, KernelTimer* tm) {
+  TimedScope ts(tm, MOE_K_LINEAR_BWD, s);
+  const bool form_dz = epi.act != MOE_ACT_NONE || epi.drop.thr != 0;
+  const BwdPlan b = bwd_plan(d, form_dz);
+  void* part = static_cast<char*>(ws) + b.dz_bytes;
+  const void* dz = form_dz ? ws : dy;
+  if (form_dz || db) {
+    MOE_TRY(by_type(d.dtype, [&](auto tag) {
+      using Elem = decltype(tag);
+      const int groups = dz_groups(d);
+      hipLaunchKernelGGL(linear_dz_kernel<Elem>, dim3(ceil_div(d.N, 512), groups), dim3(256), 0, s,
+                         static_cast<const Elem*>(dy), d.T, d.N, epi,
+                         form_dz && (dx || dw) ? static_cast<Elem*>(ws) : nullptr,
+                         db ? static_cast<float*>(part) : nullptr);
+      MOE_TRY(hipGetLastError());
+      if (!db) return hipSuccess;
+      hipLaunchKernelGGL(linear_colsum_kernel<Elem>, dim3(ceil_div(d.N, 32)), dim3(1024), 0, s,
+                         static_cast<const float*>(part), groups, d.N, static_cast<Elem*>(db));
+      return hipGetLastError();
+    }));
+  }
+  if (dx) {
+    GemmArgs a = dense_args(b.dx, d.dtype, d.T, d.K, d.N);
+    a.a[0] = opnd(dz, 0, d.N, 1, true);
+    a.b[0] = opnd(w, 0, d.K, 0, true);
+    LinearEpi out{};
+    out.y = dx;
+    MOE_TRY(product<false>(b.dx, a, out, part, s));
+  }
+  if (dw) {
+    GemmArgs a = dense_args(b.dw, d.dtype, d.N, d.K, d.T);
+    a.a[0] = opnd(dz, 0, d.N, 0, true);
+    a.b[0] = opnd(x, 0, d.K, 0, true);
+    MOE_TRY(product_rows(b.dw, a, dw, part, s));
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

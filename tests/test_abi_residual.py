@@ -179,3 +179,59 @@ def test_python_refusals():
         "w_post": (8,), "b_post": (8,), "w_pre": (8,), "gate": (4,)}
     with pytest.raises(KeyError):
         mel.Residual(4, 8, pre="batch").c()
+
+
+def lin(T=64, K=128, N=256, dtype=1, act=0, p=0.0):
+    from mixture_experts_lora_amd._lib import MoeLinearShape
+    return MoeLinearShape(T, K, N, dtype, act, p)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=0), 1), (dict(K=0), 1), (dict(N=-8), 1), (dict(dtype=4), 1), (dict(act=5), 1),
+    (dict(act=-1), 1), (dict(K=100), 2), (dict(N=12), 2),
+    (dict(T=1 << 24, K=1032), 1),                        # x above 32 GiB
+    (dict(K=32768, N=32768), 1),                         # w of 2 GiB
+    (dict(K=16384, N=32768, dtype=0), 1),
+])
+def test_linear_shape(lib, kw, status):
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.moe_linear_workspace_bytes(ctypes.byref(lin(**kw)), ctypes.byref(f),
+                                          ctypes.byref(b)) == status
+    assert err(lib)
+
+
+def test_linear_refusals(lib):
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    sh = lin(act=2, p=0.1)
+    assert lib.moe_linear_workspace_bytes(ctypes.byref(sh), ctypes.byref(f), ctypes.byref(b)) == 0
+    assert lib.moe_linear_workspace_bytes(None, ctypes.byref(f), ctypes.byref(b)) == 1
+    f, b = f.value, b.value
+    assert b >= 64 * 256 * 2                              # dz
+
+    def fwd(sh=sh, x=at(0), w=at(1), bias=at(2), res=at(3), rng=at(4), y=at(5), pre=at(6),
+            ws=at(7), n=f):
+        return lib.moe_linear_fwd(ctypes.byref(sh), x, w, bias, res, rng, 0, y, pre, ws, n, None)
+
+    def bwd(sh=sh, dy=at(0), x=at(1), w=at(2), pre=at(3), rng=at(4), dx=at(5), dw=at(6), db=at(7),
+            ws=at(8), n=b):
+        return lib.moe_linear_bwd(ctypes.byref(sh), dy, x, w, pre, rng, 0, dx, dw, db, ws, n, None)
+
+    for n in ("x", "w", "y", "rng"):
+        assert fwd(**{n: None}) == 1, n
+    for n in ("dy", "x", "w", "pre", "rng"):
+        assert bwd(**{n: None}) == 1, n
+    assert bwd(dx=None, dw=None, db=None) == 1
+    assert bwd(n=b - 1) == 3 and bwd(ws=None) == 1
+    if f:
+        assert fwd(n=f - 1) == 3 and fwd(ws=None) == 1
+    assert fwd(sh=lin(p=1.0)) == 1 and bwd(sh=lin(p=-0.5)) == 1
+    for n in ("x", "w", "bias", "res", "y", "pre"):
+        assert fwd(**{n: P(0x70000008)}) == 1 and "16-byte" in err(lib), n
+    for n in ("dy", "x", "w", "pre", "dx", "dw", "db", "ws"):
+        assert bwd(**{n: P(0x70000008)}) == 1 and "16-byte" in err(lib), n
+    for kw in (dict(y=at(0)), dict(y=at(1)), dict(y=at(2)), dict(pre=at(3)), dict(pre=at(5)),
+               dict(y=P(at(3).value + 16))):
+        assert fwd(**kw) == 1 and "overlaps" in err(lib), kw
+    for kw in (dict(dx=at(0)), dict(dx=at(6)), dict(dw=at(1)), dict(db=at(3)), dict(ws=at(5)),
+               dict(dx=P(at(2).value + 16))):
+        assert bwd(**kw) == 1 and "overlaps" in err(lib), kw

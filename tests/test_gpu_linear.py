@@ -1,0 +1,203 @@
+"""GPU parity of the linear operator against the float64 oracle.
+
+Tolerances. u = eps / 2 of the storage type, e = 2^-24. A float32 dot product of n terms is off by a
+random walk of n roundings, each at most e of a partial sum, so by 4 sqrt(n) e sum |terms| at far
+more than the walk's deviation; the epilogue adds at most 32 e of its terms (an activation's slope
+is below 1.13), and the output one rounding of u. dz feeds the products rounded to the storage
+type: the oracle rounds its float64 dz the same way, and where float32 and float64 fall on two
+sides of a rounding border (a share of about 8 e / 2u of the elements, below one in a row of these
+widths) a term differs by 2u |dz w|; eight such are allowed for.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import residual as R
+
+from gpu_util import say
+from test_gpu_residual import DT, E, _np, _rng, within
+
+pytestmark = pytest.mark.gpu
+
+# every path: up to 1, 2, 4, 8 and 16 tokens, small tiles with slices, one slice, 256-wide tiles
+SHAPES = [(1, 264, 584), (1, 8, 8), (2, 584, 264), (3, 4096, 136), (7, 1032, 264), (8, 2880, 72),
+          (13, 136, 1032), (16, 264, 264), (17, 584, 264), (64, 8, 264), (129, 1032, 8),
+          (300, 584, 1032), (700, 2880, 200), (1500, 72, 1032)]
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh"]
+
+
+def _mel():
+    import mixture_experts_lora_amd as mel
+    return mel
+
+
+def _inputs(T, K, N, dtype, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T * 131 + K * 7 + N + seed)
+    new = lambda *s: torch.randn(s, device="cuda", generator=g)  # noqa: E731
+    dt = DT[dtype]
+    return (new(T, K).to(dt), (new(N, K) * K ** -0.5).to(dt), (0.3 * new(N)).to(dt),
+            new(T, N).to(dt), new(T, N).to(dt))
+
+
+def _ws(n):
+    return torch.full((max(1, n),), 255, device="cuda", dtype=torch.uint8)  # NaN as float32
+
+
+def _nan(*s, dtype):
+    return torch.full(s, float("nan"), device="cuda", dtype=DT[dtype])
+
+
+def check_fwd(mel, T, K, N, dtype, act, p, use_bias=True, use_res=True, keep_pre=True):
+    x, w, b, res, _ = _inputs(T, K, N, dtype)
+    b, res = b if use_bias else None, res if use_res else None
+    sh = mel.LinearShape(T, K, N, dtype, act=act, dropout=p)
+    y = _nan(T, N, dtype=dtype)
+    pre = _nan(T, N, dtype=dtype) if keep_pre else None
+    mel.moe_linear_fwd(sh, x, w, y, _ws(mel.moe_linear_workspace_bytes(sh)[0]), bias=b,
+                       residual=res, pre=pre, rng=_rng(), site=4)
+    drop = (p, 77, 123, 4)
+    xs, ws, bs = _np(x), _np(w), _np(b) if use_bias else 0.0
+    ref, z = R.linear(xs, ws, bs, _np(res) if use_res else None, act, drop)
+    zerr = 4 * np.sqrt(K) * E * (np.abs(xs) @ np.abs(ws).T) + E * (np.abs(bs) + np.abs(z))
+    if keep_pre:
+        within("pre", pre, z, dtype, zerr)
+    keep = R.dropout(np.ones((T, N)), *drop)
+    extra = keep * (1.13 * zerr + 32 * E * (np.abs(z) + 1)) + 2 * E * np.abs(ref)
+    within("y", y, ref, dtype, extra + (E * np.abs(_np(res)) if use_res else 0.0))
+    return y
+
+
+def check_bwd(mel, T, K, N, dtype, act, p):
+    x, w, b, _, dy = _inputs(T, K, N, dtype)
+    sh = mel.LinearShape(T, K, N, dtype, act=act, dropout=p)
+    xs, ws = _np(x), _np(w)
+    pre = torch.from_numpy(xs @ ws.T + _np(b)).to(DT[dtype]).cuda()
+    out = {"dx": _nan(T, K, dtype=dtype), "dw": _nan(N, K, dtype=dtype), "db": _nan(N, dtype=dtype)}
+    mel.moe_linear_bwd(sh, dy, x, w, pre if act != "none" else None, out["dx"], out["dw"],
+                       out["db"], _ws(mel.moe_linear_workspace_bytes(sh)[1]), rng=_rng(), site=4)
+    dz = R.linear_bwd(_np(dy), xs, ws, _np(pre), act, (p, 77, 123, 4))[0]
+    db = dz.sum(0)
+    u = torch.finfo(DT[dtype]).eps / 2
+    form = act != "none" or p > 0
+    dzr = _np(torch.from_numpy(dz).to(DT[dtype])) if form else dz
+    # dz itself: its slope, mask and product in float32 (48 e of |dy| times the scale of the kept)
+    dzerr = 48 * E * np.abs(R.dropout(_np(dy), p, 77, 123, 4)) if form else 0 * dz
+    flips = 16 * u if form and dtype != "f32" else 0.0
+    a, c = np.abs(dzr), dzerr.max()
+    within("dx", out["dx"], dzr @ ws, dtype,
+           4 * np.sqrt(N) * E * (a @ np.abs(ws)) + flips * a.max() * np.abs(ws).max() +
+           (4 * np.sqrt(N) * c * np.abs(ws).max() if form else 0))
+    within("dw", out["dw"], dzr.T @ xs, dtype,
+           4 * np.sqrt(T) * E * (a.T @ np.abs(xs)) + flips * a.max() * np.abs(xs).max() +
+           (4 * np.sqrt(T) * c * np.abs(xs).max() if form else 0))
+    within("db", out["db"], db, dtype, (4 * np.sqrt(T) + 32) * E * np.abs(dz).sum(0) + T * c)
+    return out
+
+
+@pytest.mark.parametrize("T,K,N", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_linear_forward(dtype, T, K, N):
+    mel = _mel()
+    say(f"[linear fwd] {dtype} T={T} K={K} N={N}")
+    for i, act in enumerate(ACTS):
+        check_fwd(mel, T, K, N, dtype, act, 0.25 if i % 2 else 0.0)
+    check_fwd(mel, T, K, N, dtype, "none", 0.5, use_bias=False, keep_pre=False)
+    check_fwd(mel, T, K, N, dtype, "silu", 0.0, use_bias=False, use_res=False, keep_pre=False)
+
+
+@pytest.mark.parametrize("T,K,N", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_linear_backward(dtype, T, K, N):
+    mel = _mel()
+    say(f"[linear bwd] {dtype} T={T} K={K} N={N}")
+    for i, act in enumerate(ACTS):
+        check_bwd(mel, T, K, N, dtype, act, 0.0 if i % 2 else 0.25)
+    check_bwd(mel, T, K, N, dtype, "none", 0.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,K,N", [(4000, 264, 3400), (4111, 1160, 520)])
+def test_linear_large_tiles(dtype, T, K, N):
+    """Enough tiles for the widest ones in the forward (first) and the input gradient (second)."""
+    mel = _mel()
+    say(f"[linear large] {dtype} T={T} K={K} N={N}")
+    check_fwd(mel, T, K, N, dtype, "gelu_tanh", 0.1)
+    check_bwd(mel, T, K, N, dtype, "none", 0.0)
+
+
+def test_linear_optional_outputs_and_in_place():
+    mel = _mel()
+    for T in (5, 300):
+        say(f"[linear optional] T={T}")
+        K, N = 264, 520
+        x, w, b, res, dy = _inputs(T, K, N, "bf16")
+        sh = mel.LinearShape(T, K, N, "bf16", act="gelu", dropout=0.1)
+        f, bw = mel.moe_linear_workspace_bytes(sh)
+        y, pre = torch.empty_like(res), torch.empty_like(res)
+        mel.moe_linear_fwd(sh, x, w, y, _ws(f), bias=b, residual=res, pre=pre, rng=_rng())
+        io = res.clone()
+        mel.moe_linear_fwd(sh, x, w, io, _ws(f), bias=b, residual=io, rng=_rng())
+        assert torch.equal(io, y)
+        full = [torch.empty_like(t) for t in (x, w, b)]
+        mel.moe_linear_bwd(sh, dy, x, w, pre, *full, _ws(bw), rng=_rng())
+        for i in range(3):
+            one = [None] * 3
+            one[i] = torch.empty_like(full[i])
+            mel.moe_linear_bwd(sh, dy, x if i == 1 else None, w if i == 0 else None, pre, *one,
+                               _ws(bw), rng=_rng())
+            assert torch.equal(one[i], full[i]), i
+
+
+@pytest.mark.parametrize("T", [4, 333, 4000])
+def test_linear_repeats_and_replays_bit_for_bit(T):
+    mel = _mel()
+    say(f"[linear graph] T={T}")
+    K, N = 520, 3400 if T == 4000 else 264
+    x, w, b, res, dy = _inputs(T, K, N, "bf16")
+    sh = mel.LinearShape(T, K, N, "bf16", act="silu", dropout=0.2)
+    f, bw = (_ws(n) for n in mel.moe_linear_workspace_bytes(sh))
+    y, pre = torch.empty_like(res), torch.empty_like(res)
+    out = [torch.empty_like(t) for t in (x, w, b)]
+    rng = _rng()
+
+    def step():
+        mel.moe_linear_fwd(sh, x, w, y, f, bias=b, residual=res, pre=pre, rng=rng)
+        mel.moe_linear_bwd(sh, dy, x, w, pre, *out, bw, rng=rng)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for offset in (1, 2, 3):
+        rng[1] = offset
+        for t in (y, pre, *out):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (y, pre, *out)]
+        step()
+        torch.cuda.synchronize()
+        for a, c in zip(got, (y, pre, *out)):
+            assert torch.equal(a, c)
+
+
+def test_linear_nonfinite_inputs_stay_in_their_rows():
+    mel = _mel()
+    say("[linear nan]")
+    for T in (6, 200):
+        x, w, b, res, _ = _inputs(T, 264, 136, "bf16")
+        sh = mel.LinearShape(T, 264, 136, "bf16", act="gelu")
+        ws = _ws(mel.moe_linear_workspace_bytes(sh)[0])
+        y0, y1 = torch.empty_like(res), torch.empty_like(res)
+        mel.moe_linear_fwd(sh, x, w, y0, ws, bias=b, residual=res)
+        x[2, 5] = float("nan")
+        x[4, 7] = float("inf")
+        mel.moe_linear_fwd(sh, x, w, y1, ws, bias=b, residual=res)
+        rows = [r for r in range(T) if r not in (2, 4)]
+        assert torch.equal(y0[rows], y1[rows])
+        assert torch.isnan(y1[2]).all() and not torch.isfinite(y1[4]).all()
