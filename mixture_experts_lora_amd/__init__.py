@@ -679,7 +679,7 @@ except RuntimeError:
     pass
 
 from .layer import (LayerScratch, MoELoRABlock, MoELoRAChunkedLayer, MoELoRAFunction,  # noqa: E402
-                    MoELoRALayer)
+                    MoELoRALayer, MoELoRASublayer)
 
 __all__ += ["LayerScratch", "MoELoRABlock", "MoELoRAChunkedLayer", "MoELoRALayer",
-            "MoELoRAFunction"]
+            "MoELoRAFunction", "MoELoRASublayer"]

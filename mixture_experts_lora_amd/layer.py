@@ -29,12 +29,20 @@ layer, and adds an optional always-on shared expert (a dense LoRA SwiGLU MLP
 over every token: the grouped calls with one expert, k = 1 and the tokens in
 their own order); its backward adds the router's and the shared expert's input
 gradients to dX (moe_router_bwd, moe_accumulate).
+
+MoELoRASublayer is the block on the residual stream, the rest of a decoder
+layer once attention has run: attention's heads projected into the stream
+(moe_linear_fwd), the norm before the block, the block, and its output through
+a norm, a gate, a residual scale and dropout added to the stream
+(moe_residual_norm_fwd); and the backward of all of it.
 """
 from __future__ import annotations
 
 import torch
 
-from . import (Shape, moe_accumulate, moe_grouped_full_bwd, moe_grouped_lora_bwd,
+from . import (LinearShape, Residual, Shape, moe_accumulate, moe_grouped_full_bwd,
+               moe_grouped_lora_bwd, moe_linear_bwd, moe_linear_fwd, moe_linear_workspace_bytes,
+               moe_residual_norm_bwd, moe_residual_norm_fwd, moe_residual_norm_workspace_bytes,
                moe_grouped_lora_combine_bwd, moe_grouped_lora_combine_bwd_gather,
                moe_grouped_lora_fwd_gather,
                moe_grouped_lora_bwd_recompute, moe_grouped_lora_fwd, moe_grouped_lora_fwd_lean,
@@ -395,6 +403,107 @@ class MoELoRABlock:
     def step(self, x, w_r, dy, weights: dict, shared_weights: dict | None = None, stream=None):
         self.forward(x, w_r, weights, shared_weights, stream)
         return self.backward(dy, x, w_r, weights, shared_weights, stream)
+
+
+class MoELoRASublayer:
+    """A MoE block on the residual stream h [T, H]:
+
+        h1 = h + dropout(attn w_o^T + b_o)        (attn_width: columns of attn; None: h1 = h)
+        h2 = h1 + alpha * g * dropout(post(block(norm(h1))))
+
+    norm, post, gate, gate_sigmoid, alpha, eps, weight_shift as in Residual (norm is its pre,
+    "rms" or "layer"); shared_I, full_ft and recompute as in MoELoRABlock. attn_bias: b_o exists.
+    The norms', gate's and projection's vectors come in `params` (param_shapes() names them) and
+    their gradients are written to self.grads; those of a frozen vector can be left out with
+    `train`, the names to differentiate (None: all). The two dropouts draw the masks of
+    offset + site and offset + site + 1, so a step's sublayers take every second site."""
+
+    def __init__(self, shape: Shape, router: str, shared_I: int | None = None,
+                 attn_width: int | None = None, attn_bias: bool = False, norm: str = "rms",
+                 post: str = "none", gate: str = "none", gate_sigmoid: bool = False,
+                 alpha: float = 1.0, eps: float = 1e-5, weight_shift: float = 0.0,
+                 dropout: float = 0.0, train=None, device="cuda", full_ft: bool = False,
+                 recompute: bool = False):
+        if norm == "none":
+            raise ValueError("the block's input needs a norm: \"rms\" or \"layer\"")
+        T, H, dt = shape.T, shape.H, shape.torch_dtype
+        self.shape, self.attn_bias = shape, attn_bias
+        self.block = MoELoRABlock(shape, router, shared_I, device, full_ft, recompute)
+        common = dict(eps=eps, weight_shift=weight_shift)
+        self.before = Residual(T, H, shape.dtype, pre=norm, **common)
+        self.after = Residual(T, H, shape.dtype, post=post, pre="none", gate=gate,
+                              gate_sigmoid=gate_sigmoid, alpha=alpha, dropout=dropout, **common)
+        z = lambda *s, dtype=dt: torch.empty(s, device=device, dtype=dtype)  # noqa: E731
+        self.x, self.h2 = z(T, H), z(T, H)
+        self.stats_before, self.stats_after = (z(T, 4, dtype=torch.float32) for _ in range(2))
+        self.dy, self.dh = z(T, H), z(T, H)
+        ws = max(moe_residual_norm_workspace_bytes(d) for d in (self.before, self.after))
+        self.proj = None
+        if attn_width is not None:
+            self.proj = LinearShape(T, attn_width, H, shape.dtype, dropout=dropout)
+            self.h1, self.dattn = z(T, H), z(T, attn_width)
+            ws = max(ws, *moe_linear_workspace_bytes(self.proj))
+        self.ws = z(max(ws, 1), dtype=torch.uint8)
+        self.grads = {"d" + n: z(*s) for n, s in self.param_shapes().items()
+                      if train is None or n in train}
+
+    def param_shapes(self) -> dict:
+        s = {**self.before.param_shapes(), **self.after.param_shapes()}
+        if self.proj is not None:
+            s["w_o"] = (self.proj.N, self.proj.K)
+            if self.attn_bias:
+                s["b_o"] = (self.proj.N,)
+        return s
+
+    def _sub(self, d: dict, desc: Residual, prefix="") -> dict:
+        """The entries of d (vectors, or with prefix "d" gradients) that desc's call takes."""
+        return {prefix + n: d[prefix + n] for n in desc.param_shapes() if prefix + n in d}
+
+    def forward(self, h, params: dict, w_r, weights: dict, shared_weights: dict | None = None,
+                attn=None, rng=None, site: int = 0, stream=None):
+        """h2; h and attn are kept by the caller for the backward."""
+        self.stream_in = h
+        if self.proj is not None:
+            if attn is None:
+                raise ValueError("the attention projection reads attn: pass it")
+            moe_linear_fwd(self.proj, attn, params["w_o"], self.h1, self.ws,
+                           bias=params["b_o"] if self.attn_bias else None, residual=h, rng=rng,
+                           site=site, stream=stream)
+            self.stream_in = self.h1
+        moe_residual_norm_fwd(self.before, self.stream_in, None, self._sub(params, self.before),
+                              None, self.x, self.stats_before, stream=stream)
+        self.y = self.block.forward(self.x, w_r, weights, shared_weights, stream)
+        moe_residual_norm_fwd(self.after, self.stream_in, self.y, self._sub(params, self.after),
+                              self.h2, None, self.stats_after, rng=rng, site=site + 1,
+                              stream=stream)
+        return self.h2
+
+    def backward(self, dh2, params: dict, w_r, weights: dict, shared_weights: dict | None = None,
+                 attn=None, rng=None, site: int = 0, stream=None):
+        """From the gradient at h2: returns (dh, dattn or None, routed LoRA grads, shared LoRA
+        grads or None); the gradients of `params` are in self.grads. rng must hold the forward's
+        values."""
+        g = self.grads
+        moe_residual_norm_bwd(self.after, dh2, None, None, self.y, self._sub(params, self.after),
+                              self.stats_after, None, self.dy, self._sub(g, self.after, "d"),
+                              self.ws, rng=rng, site=site + 1, stream=stream)
+        dx, _, lora, shared = self.block.backward(self.dy, self.x, w_r, weights, shared_weights,
+                                                  stream)
+        moe_residual_norm_bwd(self.before, dh2, dx, self.stream_in, None,
+                              self._sub(params, self.before), self.stats_before, self.dh, None,
+                              self._sub(g, self.before, "d"), self.ws, stream=stream)
+        dattn = None
+        if self.proj is not None:
+            moe_linear_bwd(self.proj, self.dh, attn, params["w_o"], None, self.dattn,
+                           g.get("dw_o"), g.get("db_o"), self.ws, rng=rng, site=site,
+                           stream=stream)
+            dattn = self.dattn
+        return self.dh, dattn, lora, shared
+
+    def step(self, h, dh2, params: dict, w_r, weights: dict, shared_weights: dict | None = None,
+             attn=None, rng=None, site: int = 0, stream=None):
+        self.forward(h, params, w_r, weights, shared_weights, attn, rng, site, stream)
+        return self.backward(dh2, params, w_r, weights, shared_weights, attn, rng, site, stream)
 
 
 class MoELoRAFunction(torch.autograd.Function):
