@@ -16,8 +16,8 @@ sections "What is torch._grouped_mm?", "Faster LoRA MoE training" and
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -471,28 +471,61 @@ class Residual:
             s["gate"] = {"channel": (self.H,), "token": (self.T,), "full": (self.T, self.H)}[self.gate]
         return s
 
+    @functools.cached_property
+    def _c(self) -> MoeResidual:
+        return self.c()
 
-def _on_device(t):
-    """The launches of a call run on its tensors' device, whichever device is current."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.device.index != torch.cuda.current_device():
-        return torch.cuda.device(t.device)
-    return contextlib.nullcontext()
+    @functools.cached_property
+    def _shapes(self) -> dict:
+        return self.param_shapes()
+
+    @functools.cached_property
+    def _ws(self) -> int:
+        n = ctypes.c_size_t()
+        check(_lib.load().moe_residual_norm_workspace_bytes(ctypes.byref(self._c),
+                                                            ctypes.byref(n)),
+              "moe_residual_norm_workspace_bytes")
+        return n.value
 
 
-def _same_device(*tensors):
+# The calls around the residual stream are often a few microseconds of work (single tokens), so
+# their marshalling takes the short way when everything is in order, and the descriptors keep their
+# C structs and workspace sizes.
+def _device(*tensors):
+    """Index of the GPU that a call's tensors are on; the launches run there, whichever device is
+    current. Refuses tensors of two devices."""
     first = None
     for t in tensors:
-        if isinstance(t, torch.Tensor):
-            if first is None:
-                first = t.device
-            elif t.device != first:
-                raise ValueError(f"tensors on {first} and {t.device}")
+        if t is None or not isinstance(t, torch.Tensor):
+            continue
+        if first is None:
+            first = t
+        elif t.get_device() != first.get_device():
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    return -1 if first is None else first.get_device()
+
+
+def _addr(t, shape, dtype, name, optional=False):
+    """_ptr's checks; the address as a number."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()
+            and t.is_cuda):
+        return t.data_ptr()
+    p = _ptr(t, shape, dtype, name, optional)
+    return None if p is None else p.value
 
 
 def _rng(rng, p):
-    if p == 0.0:
-        return None
-    return _ptr(rng, (2,), torch.int64, "rng")
+    return None if p == 0.0 else _addr(rng, (2,), torch.int64, "rng")
+
+
+def _call(fn, name, device, stream, *args):
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            check(fn(*args, _stream(stream)), name)
+    elif stream is None:
+        check(fn(*args, torch._C._cuda_getCurrentRawStream(device)), name)
+    else:
+        check(fn(*args, _stream(stream)), name)
 
 
 def moe_dropout(src, dst, p, rng, site=0, stream=None):
@@ -500,27 +533,21 @@ def moe_dropout(src, dst, p, rng, site=0, stream=None):
     rng: int64 [2] on the GPU, {seed, offset}; the mask depends on (seed, offset + site, element
     index) alone, so the same call on a gradient is the backward. dst may be src."""
     key, dt = _dtype_of(src, "src")
-    _same_device(src, dst, rng)
-    with _on_device(src):
-        check(_lib.load().moe_dropout(
-            _ABI_DTYPES[key], src.numel(), float(p), _rng(rng, p), int(site),
-            _ptr(src, tuple(src.shape), dt, "src"), _ptr(dst, tuple(src.shape), dt, "dst"),
-            _stream(stream)), "moe_dropout")
+    dev, shape = _device(src, dst, rng), src.shape
+    args = (_ABI_DTYPES[key], src.numel(), p, _rng(rng, p), site, _addr(src, shape, dt, "src"),
+            _addr(dst, shape, dt, "dst"))
+    _call(_lib.load().moe_dropout, "moe_dropout", dev, stream, *args)
 
 
 def moe_residual_norm_workspace_bytes(desc: Residual) -> int:
     """Workspace bytes of moe_residual_norm_bwd (the forward needs none)."""
-    n = ctypes.c_size_t()
-    check(_lib.load().moe_residual_norm_workspace_bytes(ctypes.byref(desc.c()), ctypes.byref(n)),
-          "moe_residual_norm_workspace_bytes")
-    return n.value
+    return desc._ws
 
 
 def _residual_params(desc: Residual, params):
-    shapes, params = desc.param_shapes(), params or {}
-    return MoeResidualParams(**{n: _ptr(params.get(n), s, desc.torch_dtype, n,
-                                        optional=n.startswith("b_"))
-                                for n, s in shapes.items()})
+    params = params or {}
+    return MoeResidualParams(**{n: _addr(params.get(n), s, desc.torch_dtype, n, n[0] == "b")
+                                for n, s in desc._shapes.items()})
 
 
 def moe_residual_norm_fwd(desc: Residual, h, y, params, h_out, x_out, stats, rng=None, site=0,
@@ -529,16 +556,13 @@ def moe_residual_norm_fwd(desc: Residual, h, y, params, h_out, x_out, stats, rng
     y None: no block output (x_out = pre(h), h_out optional). params: dict of desc.param_shapes().
     stats: float32 [T, 4] for the backward, or None. h_out may be h."""
     rows, dt = (desc.T, desc.H), desc.torch_dtype
-    _same_device(h, y, h_out, x_out, stats, rng, *(params or {}).values())
     q = _residual_params(desc, params)
-    with _on_device(h if h is not None else y):
-        check(_lib.load().moe_residual_norm_fwd(
-            ctypes.byref(desc.c()), _ptr(h, rows, dt, "h", optional=True),
-            _ptr(y, rows, dt, "y", optional=True), ctypes.byref(q), _rng(rng, desc.dropout),
-            int(site), _ptr(h_out, rows, dt, "h_out", optional=y is None),
-            _ptr(x_out, rows, dt, "x_out", optional=True),
-            _ptr(stats, (desc.T, 4), torch.float32, "stats", optional=True), _stream(stream)),
-            "moe_residual_norm_fwd")
+    args = (ctypes.byref(desc._c), _addr(h, rows, dt, "h", True), _addr(y, rows, dt, "y", True),
+            ctypes.byref(q), _rng(rng, desc.dropout), site,
+            _addr(h_out, rows, dt, "h_out", y is None), _addr(x_out, rows, dt, "x_out", True),
+            _addr(stats, (desc.T, 4), torch.float32, "stats", True))
+    dev = _device(h, y, h_out, x_out, stats, rng, *(params or {}).values())
+    _call(_lib.load().moe_residual_norm_fwd, "moe_residual_norm_fwd", dev, stream, *args)
 
 
 def moe_residual_norm_bwd(desc: Residual, dh_out, dx_out, h_out, y, params, stats, dh, dy, grads,
@@ -546,27 +570,25 @@ def moe_residual_norm_bwd(desc: Residual, dh_out, dx_out, h_out, y, params, stat
     """Backward of moe_residual_norm_fwd from the gradients at h_out (None: 0) and x_out (None
     exactly when there is no pre norm): writes dh, dy and the vectors of grads (keys dw_post,
     db_post, dgate, dw_pre, db_pre); any of them may be None or left out. dh may be dh_out."""
-    rows, dt = (desc.T, desc.H), desc.torch_dtype
+    rows, dt, shapes = (desc.T, desc.H), desc.torch_dtype, desc._shapes
     grads = grads or {}
-    _same_device(dh_out, dx_out, h_out, y, stats, dh, dy, ws, rng, *(params or {}).values(),
-                 *grads.values())
+    for n in grads:
+        if n[:1] != "d" or n[1:] not in shapes:
+            raise ValueError(f"no such gradient here: {n}")
     q = _residual_params(desc, params)
-    unknown = set(grads) - {"d" + n for n in desc.param_shapes()}
-    if unknown:
-        raise ValueError(f"no such gradient here: {sorted(unknown)}")
-    g = MoeResidualGrads(**{"d" + n: _ptr(grads.get("d" + n), s, dt, "d" + n, optional=True)
-                            for n, s in desc.param_shapes().items()})
-    need = moe_residual_norm_workspace_bytes(desc) if any(v is not None for v in grads.values()) else 0
+    g = MoeResidualGrads(**{"d" + n: _addr(grads.get("d" + n), s, dt, "d" + n, True)
+                            for n, s in shapes.items()})
+    need = desc._ws if any(v is not None for v in grads.values()) else 0
     wsp, wsb = _ws(ws, need, "ws")
-    with _on_device(dh_out if dh_out is not None else dx_out):
-        check(_lib.load().moe_residual_norm_bwd(
-            ctypes.byref(desc.c()), _ptr(dh_out, rows, dt, "dh_out", optional=True),
-            _ptr(dx_out, rows, dt, "dx_out", optional=True),
-            _ptr(h_out, rows, dt, "h_out", optional=True), _ptr(y, rows, dt, "y", optional=True),
-            ctypes.byref(q), _ptr(stats, (desc.T, 4), torch.float32, "stats", optional=True),
-            _rng(rng, desc.dropout), int(site), _ptr(dh, rows, dt, "dh", optional=True),
-            _ptr(dy, rows, dt, "dy", optional=True), ctypes.byref(g), wsp, wsb, _stream(stream)),
-            "moe_residual_norm_bwd")
+    args = (ctypes.byref(desc._c), _addr(dh_out, rows, dt, "dh_out", True),
+            _addr(dx_out, rows, dt, "dx_out", True), _addr(h_out, rows, dt, "h_out", True),
+            _addr(y, rows, dt, "y", True), ctypes.byref(q),
+            _addr(stats, (desc.T, 4), torch.float32, "stats", True), _rng(rng, desc.dropout), site,
+            _addr(dh, rows, dt, "dh", True), _addr(dy, rows, dt, "dy", True), ctypes.byref(g), wsp,
+            wsb)
+    dev = _device(dh_out, dx_out, h_out, y, stats, dh, dy, ws, rng, *(params or {}).values(),
+                  *grads.values())
+    _call(_lib.load().moe_residual_norm_bwd, "moe_residual_norm_bwd", dev, stream, *args)
 
 
 @dataclass(frozen=True)
@@ -588,48 +610,52 @@ class LinearShape:
         return MoeLinearShape(self.T, self.K, self.N, _ABI_DTYPES[self.dtype], ACT_IDS[self.act],
                               float(self.dropout))
 
+    @functools.cached_property
+    def _c(self) -> MoeLinearShape:
+        return self.c()
+
+    @functools.cached_property
+    def _ws(self) -> tuple:
+        f, b = ctypes.c_size_t(), ctypes.c_size_t()
+        check(_lib.load().moe_linear_workspace_bytes(ctypes.byref(self._c), ctypes.byref(f),
+                                                     ctypes.byref(b)),
+              "moe_linear_workspace_bytes")
+        return f.value, b.value
+
 
 def moe_linear_workspace_bytes(shape: LinearShape):
     """(forward, backward) workspace bytes for `shape`."""
-    f, b = ctypes.c_size_t(), ctypes.c_size_t()
-    check(_lib.load().moe_linear_workspace_bytes(ctypes.byref(shape.c()), ctypes.byref(f),
-                                                 ctypes.byref(b)), "moe_linear_workspace_bytes")
-    return f.value, b.value
+    return shape._ws
 
 
 def moe_linear_fwd(shape: LinearShape, x, w, y, ws, bias=None, residual=None, pre=None, rng=None,
                    site=0, stream=None):
     """y = residual + dropout(act(z)), z = x w^T + bias. pre: z kept for the backward, or None.
     y may be residual."""
-    T, K, N, dt = shape.T, shape.K, shape.N, shape.torch_dtype
-    _same_device(x, w, y, ws, bias, residual, pre, rng)
-    wsp, wsb = _ws(ws, moe_linear_workspace_bytes(shape)[0], "ws")
-    with _on_device(x):
-        check(_lib.load().moe_linear_fwd(
-            ctypes.byref(shape.c()), _ptr(x, (T, K), dt, "x"), _ptr(w, (N, K), dt, "w"),
-            _ptr(bias, (N,), dt, "bias", optional=True),
-            _ptr(residual, (T, N), dt, "residual", optional=True), _rng(rng, shape.dropout),
-            int(site), _ptr(y, (T, N), dt, "y"), _ptr(pre, (T, N), dt, "pre", optional=True), wsp,
-            wsb, _stream(stream)), "moe_linear_fwd")
+    K, N, rows, dt = shape.K, shape.N, (shape.T, shape.N), shape.torch_dtype
+    wsp, wsb = _ws(ws, shape._ws[0], "ws")
+    args = (ctypes.byref(shape._c), _addr(x, (shape.T, K), dt, "x"), _addr(w, (N, K), dt, "w"),
+            _addr(bias, (N,), dt, "bias", True), _addr(residual, rows, dt, "residual", True),
+            _rng(rng, shape.dropout), site, _addr(y, rows, dt, "y"),
+            _addr(pre, rows, dt, "pre", True), wsp, wsb)
+    dev = _device(x, w, y, ws, bias, residual, pre, rng)
+    _call(_lib.load().moe_linear_fwd, "moe_linear_fwd", dev, stream, *args)
 
 
 def moe_linear_bwd(shape: LinearShape, dy, x, w, pre, dx, dw, dbias, ws, rng=None, site=0,
                    stream=None):
     """Gradients of moe_linear_fwd from dy: dx, dw and dbias, any of them None (not wanted). pre is
-    the forward's, needed with an activation. The residual's gradient is dy itself."""
-    T, K, N, dt = shape.T, shape.K, shape.N, shape.torch_dtype
-    _same_device(dy, x, w, pre, dx, dw, dbias, ws, rng)
-    wsp, wsb = _ws(ws, moe_linear_workspace_bytes(shape)[1], "ws")
-    with _on_device(dy):
-        check(_lib.load().moe_linear_bwd(
-            ctypes.byref(shape.c()), _ptr(dy, (T, N), dt, "dy"),
-            _ptr(x, (T, K), dt, "x", optional=dw is None),
-            _ptr(w, (N, K), dt, "w", optional=dx is None),
-            _ptr(pre, (T, N), dt, "pre", optional=shape.act == "none"), _rng(rng, shape.dropout),
-            int(site), _ptr(dx, (T, K), dt, "dx", optional=True),
-            _ptr(dw, (N, K), dt, "dw", optional=True),
-            _ptr(dbias, (N,), dt, "dbias", optional=True), wsp, wsb, _stream(stream)),
-            "moe_linear_bwd")
+    the forward's, needed with an activation; x is needed for dw, w for dx. The residual's gradient
+    is dy itself."""
+    K, N, rows, dt = shape.K, shape.N, (shape.T, shape.N), shape.torch_dtype
+    wsp, wsb = _ws(ws, shape._ws[1], "ws")
+    args = (ctypes.byref(shape._c), _addr(dy, rows, dt, "dy"),
+            _addr(x, (shape.T, K), dt, "x", dw is None), _addr(w, (N, K), dt, "w", dx is None),
+            _addr(pre, rows, dt, "pre", shape.act == "none"), _rng(rng, shape.dropout), site,
+            _addr(dx, (shape.T, K), dt, "dx", True), _addr(dw, (N, K), dt, "dw", True),
+            _addr(dbias, (N,), dt, "dbias", True), wsp, wsb)
+    dev = _device(dy, x, w, pre, dx, dw, dbias, ws, rng)
+    _call(_lib.load().moe_linear_bwd, "moe_linear_bwd", dev, stream, *args)
 
 
 class kernel_timer:

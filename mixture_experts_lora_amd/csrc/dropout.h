@@ -40,8 +40,9 @@ __device__ __forceinline__ uint4 philox(const DropKey& k, uint64_t ctr) {
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = static_cast<uint64_t>(0xD2511F53u) * x0;
     const uint64_t b = static_cast<uint64_t>(0xCD9E8D57u) * x2;
-    x0 = static_cast<uint32_t>(b >> 32) ^ x1 ^ k0;
-    x2 = static_cast<uint32_t>(a >> 32) ^ x3 ^ k1;
+    // three-operand exclusive or (v_bitop3_b32)
+    x0 = __builtin_amdgcn_bitop3_b32(static_cast<uint32_t>(b >> 32), x1, k0, 0x96);
+    x2 = __builtin_amdgcn_bitop3_b32(static_cast<uint32_t>(a >> 32), x3, k1, 0x96);
     x1 = static_cast<uint32_t>(b);
     x3 = static_cast<uint32_t>(a);
     k0 += 0x9E3779B9u;
@@ -50,18 +51,20 @@ __device__ __forceinline__ uint4 philox(const DropKey& k, uint64_t ctr) {
   return make_uint4(x0, x1, x2, x3);
 }
 
-// Bit i is set where element 8 ctr + i is kept. Callers select by it (v * scale or 0) rather than
-// multiply by it, so that a dropped infinity or NaN gives 0.
-__device__ __forceinline__ uint32_t drop_bits(const DropArgs& d, const DropKey& k, uint64_t ctr) {
-  const uint4 r = philox(k, ctr);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  uint32_t bits = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bits |= (w[i] & 0xffffu) >= d.thr ? 1u << (2 * i) : 0u;
-    bits |= (w[i] >> 16) >= d.thr ? 2u << (2 * i) : 0u;
-  }
-  return bits;
+// The 128 bits of elements 8 ctr .. 8 ctr + 7; zeros, which keep all, without dropout.
+__device__ __forceinline__ uint4 drop_words(const DropArgs& d, const DropKey& k, uint64_t ctr) {
+  return d.thr ? philox(k, ctr) : make_uint4(0, 0, 0, 0);
+}
+
+// Whether element i (0..7) of the words is kept. (The high half is >= t where the word is >=
+// t 2^16.) Callers select by it rather than multiply, so that a dropped infinity or NaN gives 0.
+__device__ __forceinline__ bool kept(const DropArgs& d, const uint4& r, int i) {
+  const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
+  return i & 1 ? w >= d.thr << 16 : (w & 0xffffu) >= d.thr;
+}
+
+__device__ __forceinline__ float drop(const DropArgs& d, const uint4& r, int i, float v) {
+  return kept(d, r, i) ? v * d.scale : 0.f;
 }
 
 }  // namespace moe

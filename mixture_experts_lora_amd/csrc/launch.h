@@ -189,6 +189,9 @@ int64_t residual_bwd_groups(int T, int H);
 hipError_t launch_residual_fwd(int dtype, const ResidualArgs& a, hipStream_t s, KernelTimer* tm);
 hipError_t launch_residual_bwd(int dtype, const ResidualBwdArgs& a, hipStream_t s,
                                KernelTimer* tm);
+hipError_t launch_residual_bwd_bf16(const ResidualBwdArgs& a, hipStream_t s);
+hipError_t launch_residual_bwd_f16(const ResidualBwdArgs& a, hipStream_t s);
+hipError_t launch_residual_bwd_f32(const ResidualBwdArgs& a, hipStream_t s);
 
 // ---- linear: x [T, K], w [N, K], y [T, N]
 struct LinearDims {

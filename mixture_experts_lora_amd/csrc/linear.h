@@ -62,10 +62,9 @@ __device__ __forceinline__ void linear_finish8(const LinearEpi& q, int64_t row, 
     for (int j = 0; j < 8; ++j) v[j] = act_value(v[j], q.act);
   }
   if (q.drop.thr) {
-    const uint32_t bits =
-        drop_bits(q.drop, drop_key(q.drop), static_cast<uint64_t>(at) / 8);
+    const uint4 rnd = drop_words(q.drop, drop_key(q.drop), static_cast<uint64_t>(at) / 8);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (bits >> j) & 1u ? v[j] * q.drop.scale : 0.f;
+    for (int j = 0; j < 8; ++j) v[j] = drop(q.drop, rnd, j, v[j]);
   }
   if (q.residual) {
     r.load(static_cast<const Elem*>(q.residual) + at);

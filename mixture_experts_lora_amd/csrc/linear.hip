@@ -253,9 +253,9 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const Elem* __restrict__
     if (epi.act != MOE_ACT_NONE) rz.load(static_cast<const Elem*>(epi.pre) + at);
     r.get(v);
     if (epi.drop.thr) {
-      const uint32_t bits = drop_bits(epi.drop, key, static_cast<uint64_t>(at) / 8);
+      const uint4 rnd = drop_words(epi.drop, key, static_cast<uint64_t>(at) / 8);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (bits >> j) & 1u ? v[j] * epi.drop.scale : 0.f;
+      for (int j = 0; j < 8; ++j) v[j] = drop(epi.drop, rnd, j, v[j]);
     }
     if (epi.act != MOE_ACT_NONE) {
       float z[8];
