@@ -1,6 +1,8 @@
 // What the residual operator's forward and backward kernels share: sums over a row, and the gate.
 #pragma once
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 
@@ -29,19 +31,24 @@ struct RowSum {
         s[2 * wave + 1] = b;
       }
       __syncthreads();
-      // lane l takes wave l % W's sums; a butterfly over W lanes then gives every lane the total
-      a = s[2 * (lane & (W - 1))];
-      b = s[2 * (lane & (W - 1)) + 1];
-      static_assert(W == 4 || W == 8 || W == 16, "steps below");
+      // lane l takes wave l % P's sums (P: W's next power of two); a butterfly over P lanes then
+      // gives every lane the total
+      constexpr int P = W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : 16;
+      static_assert(W <= 16, "steps below");
+      const int from = lane & (P - 1);
+      a = from < W ? s[2 * from] : 0.f;
+      b = from < W ? s[2 * from + 1] : 0.f;
       a += dpp_f32<kDppSwap1>(a);
       b += dpp_f32<kDppSwap1>(b);
-      a += dpp_f32<kDppSwap2>(a);
-      b += dpp_f32<kDppSwap2>(b);
-      if (W >= 8) {
+      if (P >= 4) {
+        a += dpp_f32<kDppSwap2>(a);
+        b += dpp_f32<kDppSwap2>(b);
+      }
+      if (P >= 8) {
         a += dpp_f32<kDppHalfMirror>(a);
         b += dpp_f32<kDppHalfMirror>(b);
       }
-      if (W >= 16) {
+      if (P >= 16) {
         a += dpp_f32<kDppMirror>(a);
         b += dpp_f32<kDppMirror>(b);
       }
@@ -63,6 +70,29 @@ __device__ __forceinline__ int row_in_block() {
 
 __device__ __forceinline__ float gate_value(float g, int sigmoid) {
   return sigmoid ? sigmoidf_(g) : g;
+}
+
+// Threads of a block whose rows take TPR threads each: four rows of a wave, or one row.
+template <int TPR>
+constexpr int row_block() {
+  return TPR == kWave ? 4 * kWave : TPR;
+}
+
+// Calls go with the threads a row takes and the chunks of 8 elements each of them takes: one chunk
+// while a block can hold the row (registers decide how many rows are in flight), with a width of
+// block every few waves so that few lanes idle.
+template <typename F>
+hipError_t by_row_width(int H, F&& go) {
+  using std::integral_constant;
+  using One = integral_constant<int, 1>;
+  if (H <= 512) return go(integral_constant<int, 64>(), One());
+  if (H <= 1024) return go(integral_constant<int, 128>(), One());
+  if (H <= 2048) return go(integral_constant<int, 256>(), One());
+  if (H <= 3584) return go(integral_constant<int, 448>(), One());
+  if (H <= 4096) return go(integral_constant<int, 512>(), One());
+  if (H <= 7168) return go(integral_constant<int, 896>(), One());
+  if (H <= 8192) return go(integral_constant<int, 1024>(), One());
+  return go(integral_constant<int, 1024>(), integral_constant<int, 2>());
 }
 
 }  // namespace moe

@@ -55,163 +55,166 @@ __global__ __launch_bounds__(256) void dropout_kernel(const Elem* src, Elem* dst
   }
 }
 
-// Statistics of a row held as CH chunks of 8 elements: chunk i of a thread is chunk
-// lane + i TPR of the row (chunks past the row are skipped).
-template <typename Elem, int TPR, int CH>
-__device__ __forceinline__ void row_stats(const Row8<Elem> (&r)[CH], int lane, int cpr, int kind,
-                                          float inv_h, float eps, RowSum<TPR>& sum, float& mean,
-                                          float& rstd) {
+// ------------------------------------------------------------------ forward
+// Mean and 1 / deviation of a row held as float32 (zeros past its end, which `live` keeps out of a
+// layer norm's squares).
+template <int TPR, int CH>
+__device__ __forceinline__ void row_stats(const float (&u)[CH][8], const bool (&live)[CH],
+                                          bool layer, float inv_h, float eps, RowSum<TPR>& sum,
+                                          float& mean, float& rstd) {
   mean = 0.f;
-  if (kind == MOE_NORM_LAYER) {
+  if (layer) {
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      if (lane + i * TPR >= cpr) continue;
-      float v[8];
-      r[i].get(v);
+    for (int i = 0; i < CH; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += v[j];
-    }
+      for (int j = 0; j < 8; ++j) s += u[i][j];
     mean = sum(s, 0.f).x * inv_h;
   }
   float q = 0.f;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    if (lane + i * TPR >= cpr) continue;
-    float v[8];
-    r[i].get(v);
+    const float m = live[i] ? mean : 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q += (v[j] - mean) * (v[j] - mean);
+    for (int j = 0; j < 8; ++j) {
+      const float c = u[i][j] - m;
+      q = fmaf(c, c, q);
+    }
   }
   rstd = 1.0f / sqrtf(sum(q, 0.f).x * inv_h + eps);
 }
 
-// (shift + w) u + b of one chunk; b may be null.
-template <typename Elem>
-__device__ __forceinline__ void affine(float (&u)[8], const Elem* w, const Elem* b, int col,
-                                       float shift) {
-  Row8<Elem> r;
-  float f[8];
-  r.load(w + col);
-  r.get(f);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) u[j] *= shift + f[j];
-  if (b) {
-    r.load(b + col);
-    r.get(f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) u[j] += f[j];
-  }
-}
-
-// ------------------------------------------------------------------ forward
-// TPR threads a row, the row in CH chunks of 8 elements a thread. Reads h and y, writes h' and
-// x' once; the norms' vectors come from cache. A thread reads all of its h and y before it writes
-// anything, so h' may be h.
-template <typename Elem, int TPR, int CH>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void residual_fwd_kernel(ResidualArgs p) {
-  constexpr int BLOCK = TPR < 256 ? 256 : TPR;
-  static_assert(TPR == kWave || TPR == BLOCK, "a row belongs to a wave or to a block");
+// TPR threads a row, in CH chunks of 8 elements a thread; each takes every so many-th row, with
+// the vectors along H in registers over the rows and the next row in flight while one is reduced.
+// A row is read once and h', x' are written once. A thread reads all of its h and y before it
+// writes anything of that row, so h' may be h.
+template <typename Elem, int TPR, int CH, int GATE>
+__global__ __launch_bounds__(row_block<TPR>()) void residual_fwd_kernel(ResidualArgs p) {
+  constexpr int BLOCK = row_block<TPR>(), R = BLOCK / TPR;
   __shared__ float slots[2][2 * (TPR / kWave)];
   const int lane = row_lane<TPR>();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (BLOCK / TPR) + row_in_block<TPR>();
-  if (row >= p.T) return;  // whole waves; a block that owns one row never leaves early
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * R + row_in_block<TPR>();
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * R;
   RowSum<TPR> sum{slots, 0};
-  const int cpr = p.H / 8;
-  const int64_t base = row * p.H;
-  const Elem* h = static_cast<const Elem*>(p.h);
-  const Elem* y = static_cast<const Elem*>(p.y);
-  Row8<Elem> rh[CH], ry[CH];
+  const int cpr = p.H / 8, rb = p.H * static_cast<int>(sizeof(Elem));
+  const bool post = p.post != MOE_NORM_NONE, pre = p.pre != MOE_NORM_NONE;
+  const bool dropout = p.drop.thr != 0;
+  const DropKey key = drop_key(p.drop);
+
+  Row8<Elem> nh[CH], ny[CH];
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    const auto bh = row_buf(p.h, row, rb, row < p.T), by = row_buf(p.y, row, rb, row < p.T);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      ny[i].load(by, lane + i * TPR);
+      nh[i].load(bh, lane + i * TPR);
+    }
+  };
+  fetch(first);
+  // as they are applied: shift + w, and the gate's value; 0 past the row
+  bool live[CH];
+  float wpost[CH][8], bpost[CH][8], wpre[CH][8], bpre[CH][8], gch[CH][8];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
-    const int c = lane + i * TPR;
-    rh[i].zero();
-    ry[i].zero();
-    if (c < cpr) {
-      if (y) ry[i].load(y + base + 8 * c);
-      if (h) rh[i].load(h + base + 8 * c);
+    live[i] = lane + i * TPR < cpr;
+    auto vector = [&](const void* v, float add, float (&out)[8]) {
+      Row8<Elem> r;
+      r.load(row_buf(v, 0, rb), lane + i * TPR);
+      r.get(out);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[j] = live[i] ? out[j] + add : 0.f;
+    };
+    vector(p.w_post, p.shift, wpost[i]);
+    vector(p.b_post, 0.f, bpost[i]);
+    vector(p.w_pre, p.shift, wpre[i]);
+    vector(p.b_pre, 0.f, bpre[i]);
+    if (GATE == MOE_GATE_CHANNEL) {
+      vector(p.gate, 0.f, gch[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) gch[i][j] = gate_value(gch[i][j], p.gate_sigmoid);
     }
   }
-  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (y) {
-    if (p.post != MOE_NORM_NONE)
-      row_stats<Elem, TPR, CH>(ry, lane, cpr, p.post, p.inv_h, p.eps, sum, st.x, st.y);
-    const DropKey key = drop_key(p.drop);
-    const Elem* gate = static_cast<const Elem*>(p.gate);
-    float g = 1.f;
-    if (p.gate_kind == MOE_GATE_TOKEN) g = gate_value(to_f32<Elem>(gate[row]), p.gate_sigmoid);
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = lane + i * TPR;
-      if (c >= cpr) continue;
-      float v[8], u[8];
-      ry[i].get(v);
-      if (p.post != MOE_NORM_NONE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (v[j] - st.x) * st.y;
-        affine<Elem>(v, static_cast<const Elem*>(p.w_post), static_cast<const Elem*>(p.b_post),
-                     8 * c, p.shift);
-      }
-      if (p.drop.thr) {
-        const uint4 rnd = drop_words(p.drop, key, static_cast<uint64_t>(row * cpr + c));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = drop(p.drop, rnd, j, v[j]);
-      }
-      if (p.gate_kind == MOE_GATE_CHANNEL || p.gate_kind == MOE_GATE_FULL) {
-        Row8<Elem> rg;
-        float f[8];
-        rg.load(gate + (p.gate_kind == MOE_GATE_FULL ? base : 0) + 8 * c);
-        rg.get(f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= gate_value(f[j], p.gate_sigmoid);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= g;
-      }
-      rh[i].get(u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] += p.alpha * v[j];
-      rh[i].set(u);
-    }
-  }
-  if (p.h_out) {
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = lane + i * TPR;
-      if (c < cpr) rh[i].store(static_cast<Elem*>(p.h_out) + base + 8 * c);
-    }
-  }
-  if (p.pre != MOE_NORM_NONE) {
-    row_stats<Elem, TPR, CH>(rh, lane, cpr, p.pre, p.inv_h, p.eps, sum, st.z, st.w);
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int c = lane + i * TPR;
-      if (c >= cpr) continue;
-      float u[8];
-      rh[i].get(u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = (u[j] - st.z) * st.w;
-      affine<Elem>(u, static_cast<const Elem*>(p.w_pre), static_cast<const Elem*>(p.b_pre), 8 * c,
-                   p.shift);
-      Row8<Elem> o;
-      o.set(u);
-      o.store(static_cast<Elem*>(p.x_out) + base + 8 * c);
-    }
-  }
-  if (lane == 0 && p.stats) p.stats[row] = st;
-}
 
-// Threads a row and chunks a thread. Forward: a wave holds rows up to 2048 wide, wider ones take a
-// block (16384 x 2048: 59.7 us by waves, 63.1 by blocks; 16384 x 4096: 128 and 110.5 us).
-template <typename F>
-hipError_t by_width_fwd(int H, F&& go) {
-  using std::integral_constant;
-  if (H <= 512) return go(integral_constant<int, 64>(), integral_constant<int, 1>());
-  if (H <= 1024) return go(integral_constant<int, 64>(), integral_constant<int, 2>());
-  if (H <= 2048) return go(integral_constant<int, 64>(), integral_constant<int, 4>());
-  if (H <= 4096) return go(integral_constant<int, 256>(), integral_constant<int, 2>());
-  if (H <= 8192) return go(integral_constant<int, 512>(), integral_constant<int, 2>());
-  return go(integral_constant<int, 512>(), integral_constant<int, 4>());
+  for (int64_t row = first; row < p.T; row += stride) {
+    Row8<Elem> rh[CH], ry[CH], rg[CH];
+    if (GATE == MOE_GATE_FULL) {
+      const auto bg = row_buf(p.gate, row, rb);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) rg[i].load(bg, lane + i * TPR);
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      rh[i] = nh[i];
+      ry[i] = ny[i];
+    }
+    fetch(row + stride);
+    // the mask needs nothing from memory: drawn while the row arrives
+    uint4 rnd[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      rnd[i] = make_uint4(0, 0, 0, 0);
+      if (dropout) rnd[i] = philox(key, static_cast<uint64_t>(row * cpr + lane + i * TPR));
+    }
+    float gt = 1.f;
+    if (GATE == MOE_GATE_TOKEN)
+      gt = gate_value(to_f32<Elem>(static_cast<const Elem*>(p.gate)[row]), p.gate_sigmoid);
+    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+    float u[CH][8];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) ry[i].get(u[i]);
+    if (post) {
+      row_stats<TPR, CH>(u, live, p.post == MOE_NORM_LAYER, p.inv_h, p.eps, sum, st.x, st.y);
+      const float off = -st.x * st.y;
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          u[i][j] = fmaf(fmaf(u[i][j], st.y, off), wpost[i][j], bpost[i][j]);
+    }
+    const auto bho = row_buf(p.h_out, row, rb);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      float h[8];
+      if (GATE == MOE_GATE_FULL) {
+        float g[8];
+        rg[i].get(g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[i][j] *= gate_value(g[j], p.gate_sigmoid);
+      }
+      if (GATE == MOE_GATE_CHANNEL) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[i][j] *= gch[i][j];
+      }
+      const float k = GATE == MOE_GATE_TOKEN ? p.alpha * gt : p.alpha;
+      // scaled before the sum rather than through k: the result is the one of moe_dropout and an
+      // add, bit for bit
+      if (dropout) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[i][j] = drop(p.drop, rnd[i], j, u[i][j]);
+      }
+      rh[i].get(h);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = fmaf(k, u[i][j], h[j]);
+      rh[i].set(h);
+      rh[i].store(bho, lane + i * TPR);
+      rh[i].get(u[i]);  // h' as it is stored
+    }
+    if (pre) {
+      row_stats<TPR, CH>(u, live, p.pre == MOE_NORM_LAYER, p.inv_h, p.eps, sum, st.z, st.w);
+      const float off = -st.z * st.w;
+      const auto bxo = row_buf(p.x_out, row, rb);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          u[i][j] = fmaf(fmaf(u[i][j], st.w, off), wpre[i][j], bpre[i][j]);
+        Row8<Elem> o;
+        o.set(u[i]);
+        o.store(bxo, lane + i * TPR);
+      }
+    }
+    if (lane == 0 && p.stats) p.stats[row] = st;
+  }
 }
 
 }  // namespace
@@ -233,23 +236,36 @@ hipError_t launch_dropout(int dtype, int64_t n, const DropArgs& d, const void* s
 hipError_t launch_residual_fwd(int dtype, const ResidualArgs& a, hipStream_t s, KernelTimer* tm) {
   TimedScope ts(tm, MOE_K_RESIDUAL_NORM, s);
   return by_type(dtype, [&](auto tag) {
-    return by_width_fwd(a.H, [&](auto tpr, auto ch) {
-      constexpr int TPR = decltype(tpr)::value, BLOCK = TPR < 256 ? 256 : TPR, R = BLOCK / TPR;
-      hipLaunchKernelGGL((residual_fwd_kernel<decltype(tag), TPR, decltype(ch)::value>),
-                         dim3(static_cast<unsigned>((static_cast<int64_t>(a.T) + R - 1) / R)),
+    return by_row_width(a.H, [&](auto tpr, auto ch) {
+      typedef decltype(tag) Elem;
+      constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
+      constexpr int BLOCK = row_block<TPR>(), R = BLOCK / TPR;
+      // as many blocks as a CU holds by registers, over 256 CUs: one round, no tail
+      const int64_t rows = (static_cast<int64_t>(a.T) + R - 1) / R;
+      const int64_t blocks = 256 * std::max(1, 1024 / BLOCK);
+      auto* kern = a.gate_kind == MOE_GATE_CHANNEL ? residual_fwd_kernel<Elem, TPR, CH, MOE_GATE_CHANNEL>
+                   : a.gate_kind == MOE_GATE_TOKEN ? residual_fwd_kernel<Elem, TPR, CH, MOE_GATE_TOKEN>
+                   : a.gate_kind == MOE_GATE_FULL  ? residual_fwd_kernel<Elem, TPR, CH, MOE_GATE_FULL>
+                                                   : residual_fwd_kernel<Elem, TPR, CH, MOE_GATE_NONE>;
+      hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(std::min(rows, blocks))),
                          dim3(BLOCK), 0, s, a);
       return hipGetLastError();
     });
   });
 }
 
-// Blocks of the backward: 1024 threads a CU over 256 CUs keep enough rows in flight, and each
-// block adds a row of partials.
+// Blocks of the backward, over 256 CUs: what a CU holds of the wider ones, and 512 threads a CU of
+// the narrow ones, whose partials (a row a block) cost more than the rows in flight gain
+// (16384 x 2048, both norms and a gate: 86.1 us with two blocks a CU, 96.3 with four).
 int64_t residual_bwd_groups(int T, int H) {
-  const int threads = H <= 512 ? 64 : H <= 2048 ? 256 : H <= 4096 ? 512 : 1024;
-  const int rows = threads < 256 ? 256 / threads : 1;
-  return std::min<int64_t>((static_cast<int64_t>(T) + rows - 1) / rows,
-                           256 * 1024 / std::max(threads, 256));
+  int64_t groups = 0;
+  (void)by_row_width(H, [&](auto tpr, auto) {
+    constexpr int BLOCK = row_block<decltype(tpr)::value>(), R = BLOCK / decltype(tpr)::value;
+    groups = std::min<int64_t>((static_cast<int64_t>(T) + R - 1) / R,
+                               256 * std::max(1, (BLOCK <= 256 ? 512 : 1024) / BLOCK));
+    return hipSuccess;
+  });
+  return groups;
 }
 
 hipError_t launch_residual_bwd(int dtype, const ResidualBwdArgs& a, hipStream_t s,

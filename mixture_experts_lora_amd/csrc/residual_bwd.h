@@ -29,10 +29,9 @@ enum ColSum { CS_W_PRE = 0, CS_B_PRE = 1, CS_W_POST = 2, CS_B_POST = 3, CS_GATE 
 // element (uhat = u rstd - mean rstd), constants along a row are folded, and what a row's second
 // pass needs is kept from the first.
 template <typename Elem, int TPR, int CH, bool YPATH, bool LAYER, int GATE>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void residual_bwd_kernel(ResidualBwdArgs q) {
+__global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(ResidualBwdArgs q) {
   const ResidualArgs& p = q.f;
-  constexpr int BLOCK = TPR < 256 ? 256 : TPR;
-  static_assert(TPR == kWave || TPR == BLOCK, "a row belongs to a wave or to a block");
+  constexpr int BLOCK = row_block<TPR>();
   __shared__ float slots[2][2 * (TPR / kWave)];
   const int lane = row_lane<TPR>();
   constexpr int R = BLOCK / TPR;
@@ -73,10 +72,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void residual_bwd_kernel(Res
       a_wpre[i][j] = a_bpre[i][j] = a_wpost[i][j] = a_bpost[i][j] = a_gate[i][j] = 0.f;
   }
 
-  // The next row is loaded while this one is reduced. Blocks of 512 and 1024 threads have registers
+  // The next row is loaded while this one is reduced. Blocks of over 256 threads have registers
   // left for only what a row needs first, dx' and h' (the rest arrives during the first reduction),
   // and rows of two chunks a thread for nothing.
-  constexpr bool AHEAD = CH == 1, AHEAD_ALL = AHEAD && TPR < 512;
+  constexpr bool AHEAD = CH == 1, AHEAD_ALL = AHEAD && TPR <= 256;
   const int rb = p.H * static_cast<int>(sizeof(Elem));
   Row8<Elem> nd[CH], nx[CH], nh[CH], ny[CH];
   float4 nst = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -347,25 +346,13 @@ __global__ __launch_bounds__(1024) void residual_colsum_kernel(ResidualBwdArgs q
   static_cast<Elem*>(out)[col] = from_f32<Elem>(s);
 }
 
-// Threads a row and chunks a thread: one chunk while a block can hold the row, since the column
-// sums, the vectors along H and the row in flight take up to 80 registers a chunk.
-template <typename F>
-hipError_t by_width_bwd(int H, F&& go) {
-  using std::integral_constant;
-  if (H <= 512) return go(integral_constant<int, 64>(), integral_constant<int, 1>());
-  if (H <= 2048) return go(integral_constant<int, 256>(), integral_constant<int, 1>());
-  if (H <= 4096) return go(integral_constant<int, 512>(), integral_constant<int, 1>());
-  if (H <= 8192) return go(integral_constant<int, 1024>(), integral_constant<int, 1>());
-  return go(integral_constant<int, 1024>(), integral_constant<int, 2>());
-}
-
 template <typename Elem>
 hipError_t launch_bwd(ResidualBwdArgs a, hipStream_t s) {
   const bool layer = a.f.post == MOE_NORM_LAYER || a.f.pre == MOE_NORM_LAYER;
   auto go = [&](auto ypath, auto gate) {
-    return by_width_bwd(a.f.H, [&](auto tpr, auto ch) {
+    return by_row_width(a.f.H, [&](auto tpr, auto ch) {
       constexpr int TPR = decltype(tpr)::value, CH = decltype(ch)::value;
-      constexpr int BLOCK = TPR < 256 ? 256 : TPR;
+      constexpr int BLOCK = row_block<TPR>();
       constexpr bool Y = decltype(ypath)::value;
       constexpr int G = decltype(gate)::value;
       auto* kern = layer ? residual_bwd_kernel<Elem, TPR, CH, Y, true, G>
