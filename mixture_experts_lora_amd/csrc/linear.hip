@@ -180,12 +180,14 @@ __global__ __launch_bounds__(256) void linear_sum_kernel(const float* __restrict
 }
 
 // ------------------------------------------------------------------ few tokens
-// T <= TT <= 16: bound by reading w once. A block owns eight columns (eight rows of w) and its
-// four waves split K in 16-byte pieces a lane, so a wave has eight independent streams of w in
-// flight; x is small and comes from cache. The lanes' sums meet by wave reductions, the waves' in
-// LDS, in a fixed order.
+// Bound by reading w once.
+//
+// One or two tokens: a block owns eight columns (eight rows of w) and its four waves split K in
+// 16-byte pieces a lane, so each wave reads 1 KB of a row an instruction with eight rows in flight;
+// x comes from cache. (7168 x 7168 bf16, one token: 21.1 us, 4.9 TB/s; by MFMA fragments, 16 rows
+// of 64 bytes an instruction, 25.4 us.)
 template <typename Elem, int TT>
-__global__ __launch_bounds__(256) void linear_few_kernel(const Elem* __restrict__ x,
+__global__ __launch_bounds__(256) void linear_one_kernel(const Elem* __restrict__ x,
                                                          const Elem* __restrict__ w, int T, int K,
                                                          int N, LinearEpi epi) {
   __shared__ float red[4][TT * 8];
@@ -201,7 +203,7 @@ __global__ __launch_bounds__(256) void linear_few_kernel(const Elem* __restrict_
     for (int i = 0; i < 8; ++i) rw[i].load(w + static_cast<int64_t>(n0 + i) * K + k);
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      if (t >= T) continue;  // uniform (a break would leave the loop rolled, its sums in memory)
+      if (t >= T) continue;
       Row8<Elem> rx;
       float fx[8];
       rx.load(x + static_cast<int64_t>(t) * K + k);
@@ -230,6 +232,79 @@ __global__ __launch_bounds__(256) void linear_few_kernel(const Elem* __restrict_
   for (int i = 0; i < 8; ++i)
     v[i] = (red[0][t * 8 + i] + red[1][t * 8 + i]) + (red[2][t * 8 + i] + red[3][t * 8 + i]);
   linear_finish8<Elem>(epi, t, n0, N, v);
+}
+
+// Up to 16 tokens, where fused multiply-adds would bound the kernel above (16 tokens, 4096 x 2880:
+// 27.4 us, by MFMA 10.2): a block owns 16 columns and its eight waves deal out the reduction in
+// pieces of 16 bytes x 8 steps a lane, straight into MFMA fragments: 16 rows of 64 bytes for w (the
+// MFMA's A operand, so that a lane ends with four consecutive columns of a token) and for x, which
+// comes from L2. Accesses past an operand read zeros. The waves' sums meet in LDS in wave order.
+template <typename Elem> struct Few;
+template <> struct Few<bf16_t> {
+  static constexpr int KSTEP = 32;
+  __device__ static f32x4 mul(const uint4& a, const uint4& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+};
+template <> struct Few<f16_t> {
+  static constexpr int KSTEP = 32;
+  typedef f16_t h8 __attribute__((ext_vector_type(8)));
+  __device__ static f32x4 mul(const uint4& a, const uint4& b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a),
+                                                  __builtin_bit_cast(h8, b), c, 0, 0, 0);
+  }
+};
+// The four floats of a lane go through four products whose k are {j, 4 + j, 8 + j, 12 + j}.
+template <> struct Few<float> {
+  static constexpr int KSTEP = 16;
+  __device__ static f32x4 mul(const uint4& a, const uint4& b, f32x4 c) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(x[j]), __uint_as_float(y[j]), c, 0,
+                                               0, 0);
+    return c;
+  }
+};
+
+template <typename Elem>
+__global__ __launch_bounds__(512) void linear_few_kernel(const Elem* __restrict__ x,
+                                                         const Elem* __restrict__ w, int T, int K,
+                                                         int N, LinearEpi epi) {
+  typedef Few<Elem> F;
+  constexpr int ES = sizeof(Elem), STEPS = 8;
+  __shared__ __attribute__((aligned(16))) float red[8][16][20];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16, row = lane & 15, kl = (lane >> 4) * (16 / ES);
+  const int kb = K * ES;  // bytes of a row
+  const auto bw = row_buf(w + static_cast<int64_t>(n0) * K, 0, min(N - n0, 16) * kb);
+  const auto bx = row_buf(x, 0, T * kb);
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = wave * F::KSTEP * STEPS; k0 < K; k0 += 8 * F::KSTEP * STEPS) {
+    uint4 fw[STEPS], fx[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int k = k0 + s * F::KSTEP + kl;
+      // K is a multiple of 8: the 16 bytes are all in or all out
+      const int at = k < K ? row * kb + k * ES : static_cast<int>(kOOB);
+      fw[s] = buf_load(bw, at);
+      fx[s] = buf_load(bx, at);
+    }
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) acc = F::mul(fw[s], fx[s], acc);
+  }
+  // lane: token lane % 16, columns 4 (lane / 16) .. + 3
+  *reinterpret_cast<f32x4*>(&red[wave][row][(lane >> 4) * 4]) = acc;
+  __syncthreads();
+  const int t = threadIdx.x >> 1, half = threadIdx.x & 1, col = n0 + half * 8;
+  if (t >= T || col >= N) return;
+  float v[8] = {};
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += red[q][t][half * 8 + j];
+  linear_finish8<Elem>(epi, t, col, N, v);
 }
 
 // ------------------------------------------------------------------ dz and dbias
@@ -410,17 +485,13 @@ hipError_t product_rows(const Product& q, GemmArgs& a, void* out, void* part, hi
 template <typename Elem>
 hipError_t few_tokens(const LinearDims& d, const void* x, const void* w, const LinearEpi& epi,
                       hipStream_t s) {
-  auto go = [&](auto tt) {
-    hipLaunchKernelGGL((linear_few_kernel<Elem, decltype(tt)::value>), dim3(d.N / 8), dim3(256), 0,
-                       s, static_cast<const Elem*>(x), static_cast<const Elem*>(w), d.T, d.K, d.N,
-                       epi);
-    return hipGetLastError();
-  };
-  if (d.T == 1) return go(std::integral_constant<int, 1>());
-  if (d.T <= 2) return go(std::integral_constant<int, 2>());
-  if (d.T <= 4) return go(std::integral_constant<int, 4>());
-  if (d.T <= 8) return go(std::integral_constant<int, 8>());
-  return go(std::integral_constant<int, 16>());
+  auto* kern = d.T == 1   ? linear_one_kernel<Elem, 1>
+               : d.T == 2 ? linear_one_kernel<Elem, 2>
+                          : linear_few_kernel<Elem>;
+  const dim3 grid(ceil_div(d.N, d.T <= 2 ? 8 : 16)), block(d.T <= 2 ? 256 : 512);
+  hipLaunchKernelGGL(kern, grid, block, 0, s, static_cast<const Elem*>(x),
+                     static_cast<const Elem*>(w), d.T, d.K, d.N, epi);
+  return hipGetLastError();
 }
 
 inline int dz_groups(const LinearDims& d) {
