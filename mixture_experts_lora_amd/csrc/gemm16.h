@@ -248,7 +248,9 @@ __device__ __forceinline__ int kswz(int row) {
 
 template <int R>
 __device__ __forceinline__ int nswz(int k) {
-  return R >= 128 ? ((k & 3) << 2) : (R == 64 ? (((k >> 1) & 1) << 2) : 0);
+  // 192: rows of 24 chunks, whose last 8 a swizzle within 8 chunks keeps in the row; they shift the
+  // banks as rows of 64 do
+  return R == 64 || R == 192 ? (((k >> 1) & 1) << 2) : R >= 128 ? ((k & 3) << 2) : 0;
 }
 
 template <int N>
@@ -312,6 +314,9 @@ struct Geo {
   static constexpr int NIW = (TI + NW - 1) / NW;   // per wave (upper bound)
   static constexpr int MINW = TI / NW;             // issued by every wave
   static constexpr int CPR = KC ? BK / 8 : ROWS / 8;        // chunks per LDS row
+  // Row and chunk position that lane `lane` of instruction j fills.
+  __device__ static int row(int j, int lane) { return (64 * j + lane) / CPR; }
+  __device__ static int pos(int j, int lane) { return (64 * j + lane) % CPR; }
   static constexpr int RPI = KC ? 512 / BK : 512 / ROWS;    // LDS rows per instruction
 };
 
@@ -344,8 +349,7 @@ __device__ __forceinline__ void make_plan(Plan<ROWS, BK, KC, NW>& P, const View<
 #pragma unroll
   for (int i = 0; i < G::NIW; ++i) {
     const int j = wave + NW * i;  // instruction index within the tile
-    const int r = G::RPI * j + lane / G::CPR;
-    const int p = lane % G::CPR;
+    const int r = G::row(j, lane), p = G::pos(j, lane);
     uint32_t vo = kOOB;
     if (KC) {
       const int c = p ^ kswz<BK>(r);
@@ -533,7 +537,7 @@ __device__ __forceinline__ bf16x8 read_frag(const char* tile,
 // reading 16 row segments, hit distinct LDS banks.
 template <int WN>
 __device__ __forceinline__ int slab_off(int r, int c) {
-  const int sw = WN >= 64 ? (r & 15) : ((r >> 1) & 7);
+  const int sw = WN >= 64 && WN % 64 == 0 ? (r & 15) : ((r >> 1) & 7);
   return r * WN * 4 + ((c ^ sw) << 4);
 }
 
@@ -1112,7 +1116,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
       const int nkf = nk - 1;  // full tiles before the last
       // Tiles 1..C are clean: the tile each stages (it + 2) is a whole tile
       // of the main segment (K tail tile excluded).
-      const int last_clean = MODE == GROUP_M ? nk0 - 1 - (K0 % BK != 0 ? 1 : 0) : -1;
+      const int last_clean = MODE == GROUP_M || DENSE ? nk0 - 1 - (K0 % BK != 0 ? 1 : 0) : -1;
       const int C = min(nkf - 1, last_clean - 2);
       if (nkf > 0) ktile(0, Rt(), mfmac, No(), Yes(), No());
       int it = 1;
@@ -1129,7 +1133,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
     };
     // Waves whose rows all lie past the tile's valid rows, or whose columns
     // all lie past the valid columns, neither read fragments nor multiply.
-    const bool live = MODE != GROUP_M ||
+    const bool live = (MODE != GROUP_M && !DENSE) ||
                       (wm * WM < rows && (PAIRED ? n_tile * (BN / 2) + wn * (WN / 2) < p.I
                                                  : n0 + wn * WN < p.N));
     if (live) kloop(std::true_type());
@@ -1334,6 +1338,65 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
     }
   };
   if constexpr (HPRE) hfetch(0, hpre[0]);
+  if constexpr (DENSE) {
+    // The slab's 32 x WN outputs in pieces of eight columns, 64 at a time. The residual's pieces of
+    // a slab are loaded while the slab before it is finished.
+    typedef std::conditional_t<F16, f16_t, bf16_t> Elem;
+    constexpr int SEGS = WN / 8, PASS = 32 * SEGS / 64;
+    const bool part = p.E > 1, finish = MODE == GROUP_M && !part;
+    const DropKey key = drop_key(p.lin.drop);
+    Row8<Elem> res[2][PASS];
+    auto place = [&](int mi, int pass, int& m_local, int& col) __attribute__((always_inline)) {
+      m_local = wm * WM + mi * 32 + (pass * 64 + lane) / SEGS;
+      col = n0 + wn * WN + 8 * ((pass * 64 + lane) % SEGS);
+      return m_local < rows && col < p.N;  // N is a multiple of 8
+    };
+    auto rfetch = [&](int mi, Row8<Elem> (&r)[PASS]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int pass = 0; pass < PASS; ++pass) {
+        int m_local, col;
+        r[pass].zero();
+        if (finish && p.lin.residual && place(mi, pass, m_local, col))
+          r[pass].load(static_cast<const Elem*>(p.lin.residual) +
+                       static_cast<int64_t>(m0 + m_local) * p.N + col);
+      }
+    };
+    rfetch(0, res[0]);
+#pragma unroll
+    for (int mi = 0; mi < MF; ++mi) {
+      if (mi) wave_lds_sync();  // previous slab fully read
+#pragma unroll
+      for (int ni = 0; ni < NF; ++ni)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          f32x4 v;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] = acc[mi][ni][4 * q + j];
+          *reinterpret_cast<f32x4*>(slab + slab_off<WN>(srow, ni * 8 + 2 * q + shalf)) = v;
+        }
+      if (mi + 1 < MF) rfetch(mi + 1, res[(mi + 1) & 1]);
+      wave_lds_sync();
+#pragma unroll
+      for (int pass = 0; pass < PASS; ++pass) {
+        int m_local, col;
+        const bool in = place(mi, pass, m_local, col);
+        float v[8];
+        read8_interleaved<WN>(slab, (pass * 64 + lane) / SEGS, (pass * 64 + lane) % SEGS, v);
+        if (!in) continue;
+        const int64_t row = m0 + m_local;
+        if (part) {
+          Row8<float> o;
+          o.set(v);
+          o.store(static_cast<float*>(p.out) + (static_cast<int64_t>(e) * p.M + row) * p.N + col);
+        } else if (MODE == GROUP_M) {
+          linear_finish8<Elem>(p.lin, key, row, col, p.N, res[mi & 1][pass], v);
+        } else {
+          store8<F16>(static_cast<bf16_t*>(p.out) + row * p.N + col, v);
+        }
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int mi = 0; mi < MF; ++mi) {
     if constexpr (HPRE) {
@@ -1413,20 +1476,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
           continue;
         }
         if (m_local >= rows) continue;
-        if constexpr (DENSE) {
-          if (col >= p.N) continue;  // N is a multiple of 8
-          const int64_t row = m0 + m_local;
-          if (p.E > 1) {
-            Row8<float> o;
-            o.set(v);
-            o.store(static_cast<float*>(p.out) + (static_cast<int64_t>(e) * p.M + row) * p.N + col);
-          } else if (MODE == GROUP_M) {
-            linear_finish8<std::conditional_t<F16, f16_t, bf16_t>>(p.lin, row, col, p.N, v);
-          } else {
-            store8<F16>(static_cast<bf16_t*>(p.out) + row * p.N + col, v);
-          }
-          continue;
-        }
         if (EPI == EPI_STORE_F32) {
           // GROUP_M: router logits; GROUP_K: split-K partial weight gradients
           float* rp = MODE == GROUP_M

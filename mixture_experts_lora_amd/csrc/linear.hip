@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "colsum.h"
 #include "gemm16.h"
 
 namespace moe {
@@ -167,6 +168,7 @@ __global__ __launch_bounds__(256) void linear_sum_kernel(const float* __restrict
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (i >= MN) return;
   float v[8] = {};
+#pragma unroll 4
   for (int e = 0; e < E; ++e) {
     Row8<float> r;
     float f[8];
@@ -308,41 +310,48 @@ __global__ __launch_bounds__(512) void linear_few_kernel(const Elem* __restrict_
 }
 
 // ------------------------------------------------------------------ dz and dbias
-// 512 columns a block, its four waves on different rows; rows are dealt to gridDim.y groups whose
-// column sums (float32, in row order) linear_colsum_kernel adds. dz null: only the sums.
+// 512 columns a block, its four waves on different rows, two rows of a wave in flight at once; rows
+// are dealt to gridDim.y groups whose column sums (float32, in row order) linear_colsum_kernel adds.
+// dz null: only the sums.
 template <typename Elem>
 __global__ __launch_bounds__(256) void linear_dz_kernel(const Elem* __restrict__ dy, int T, int N,
                                                         LinearEpi epi, Elem* __restrict__ dz,
                                                         float* __restrict__ part) {
+  constexpr int U = 2;
   __shared__ float red[4][512 + 8];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = blockIdx.x * 512 + lane * 8;
-  const bool live = col < N;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int chunk = blockIdx.x * 64 + lane, rb = N * static_cast<int>(sizeof(Elem));
   const DropKey key = drop_key(epi.drop);
+  const bool act = epi.act != MOE_ACT_NONE;
   float sum[8] = {};
-  for (int64_t t = blockIdx.y * 4 + wave; live && t < T; t += gridDim.y * 4) {
-    const int64_t at = t * N + col;
-    Row8<Elem> r, rz;
-    float v[8];
-    r.load(dy + at);
-    if (epi.act != MOE_ACT_NONE) rz.load(static_cast<const Elem*>(epi.pre) + at);
-    r.get(v);
-    if (epi.drop.thr) {
-      const uint4 rnd = drop_words(epi.drop, key, static_cast<uint64_t>(at) / 8);
+  for (int64_t t0 = blockIdx.y * 4 * U + wave; t0 < T; t0 += gridDim.y * 4 * U) {
+    Row8<Elem> r[U], rz[U];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = drop(epi.drop, rnd, j, v[j]);
-    }
-    if (epi.act != MOE_ACT_NONE) {
-      float z[8];
-      rz.get(z);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= act_slope(z[j], epi.act);
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + 4 * u;
+      r[u].load(row_buf(dy, t, rb, t < T), chunk);
+      rz[u].load(row_buf(epi.pre, t, rb, act && t < T), chunk);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] += v[j];
-    if (dz) {
-      r.set(v);
-      r.store(dz + at);
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + 4 * u;
+      float v[8];
+      r[u].get(v);
+      if (epi.drop.thr) {
+        const uint4 rnd = philox(key, static_cast<uint64_t>(t * (N / 8) + chunk));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = drop(epi.drop, rnd, j, v[j]);
+      }
+      if (act) {
+        float z[8];
+        rz[u].get(z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= act_slope(z[j], epi.act);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      r[u].set(v);
+      r[u].store(row_buf(dz, t, rb, t < T), chunk);
     }
   }
   if (!part) return;
@@ -357,62 +366,73 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const Elem* __restrict__
   }
 }
 
-// 32 columns a block: 32 rows of lanes walk every 32nd group, then the 32 sums, in order.
 template <typename Elem>
-__global__ __launch_bounds__(1024) void linear_colsum_kernel(const float* __restrict__ part,
-                                                             int groups, int N,
-                                                             Elem* __restrict__ db) {
-  __shared__ float red[32][33];
-  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, col = blockIdx.x * 32 + cx;
-  float a = 0.f;
-  if (col < N)
-    for (int g = ry; g < groups; g += 32) a += part[static_cast<int64_t>(g) * N + col];
-  red[ry][cx] = a;
-  __syncthreads();
-  if (ry != 0 || col >= N) return;
-  a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) a += red[i][cx];
-  db[col] = from_f32<Elem>(a);
+__global__ __launch_bounds__(1024) void linear_colsum_kernel(const float* part, int groups, int N,
+                                                             Elem* db) {
+  __shared__ float red[128][33];
+  int col;
+  float s;
+  if (block_colsum(part, groups, N, blockIdx.x * 32, N, red, col, s)) db[col] = from_f32<Elem>(s);
 }
 
 // ------------------------------------------------------------------ host side
 constexpr int kFewTokens = 16;
 
 // One product of M x N outputs over K: tile shape, and slices of the reduction.
-enum Tile { TILE_256, TILE_128x64, TILE_128x256, TILE_F32 };
+enum Tile { TILE_256x256, TILE_256x192, TILE_192x192, TILE_128x64, TILE_128x256, TILE_F32 };
 struct Product {
   Tile tile;
   int bm, bn, ntm, ntn, E, kchunk;
   size_t part_bytes;  // 0: one slice, no partials
 };
 
+// The plan of least estimated time: the tiles of the busiest CU at the rate a CU reaches with them,
+// plus what a block cannot overlap, plus the slices' partials written and read and the launch that
+// sums them. `few` is the least number of tiles' time a CU takes: tiles of four waves keep a CU
+// busy by twos. Rates measured on full launches of each tile.
+struct TileModel {
+  Tile tile;
+  int bm, bn;
+  double tflops, few;  // per CU, and see above
+};
+constexpr TileModel kRows16[] = {{TILE_256x256, 256, 256, 4.2, 1.0},
+                                 {TILE_256x192, 256, 192, 4.1, 1.0},
+                                 {TILE_128x64, 128, 64, 2.7, 1.7}};
+constexpr TileModel kReduceRows16[] = {{TILE_192x192, 192, 192, 4.1, 1.0},
+                                       {TILE_128x256, 128, 256, 4.1, 1.4}};
+constexpr TileModel kF32[] = {{TILE_F32, 128, 128, 0.5, 1.5}};
+
 Product plan(int dtype, bool reduce_rows, int64_t M, int64_t N, int64_t K) {
-  Product q{};
-  auto with = [&](Tile t, int bm, int bn) {
-    q.tile = t;
-    q.bm = bm;
-    q.bn = bn;
-    q.ntm = ceil_div(M, bm);
-    q.ntn = ceil_div(N, bn);
-  };
-  int fill = 512, least = 256;
-  if (dtype == MOE_F32) {
-    with(TILE_F32, 128, 128);
-    least = 128;
-  } else if (reduce_rows) {
-    with(TILE_128x256, 128, 256);
-  } else {
-    with(TILE_256, 256, 256);
-    if (static_cast<int64_t>(q.ntm) * q.ntn < 192) with(TILE_128x64, 128, 64);
-    else fill = 0;
+  const bool f32 = dtype == MOE_F32;
+  const TileModel* models = f32 ? kF32 : reduce_rows ? kReduceRows16 : kRows16;
+  const int count = f32 ? 1 : reduce_rows ? 2 : 3, least = f32 ? 128 : 256;
+  // a slice of a row reduction lies within a 32-bit buffer offset
+  const int64_t e0 = reduce_rows ? (K * std::max(M, N) * 2 >> 30) + 1 : 1;
+  const int64_t e1 = std::max<int64_t>(e0, std::min<int64_t>(32, K / least));
+  Product best{};
+  double best_us = 0.0;
+  for (int i = 0; i < count; ++i) {
+    const TileModel& m = models[i];
+    const int64_t tiles = static_cast<int64_t>(ceil_div(M, m.bm)) * ceil_div(N, m.bn);
+    for (int64_t e = e0; e <= e1; ++e) {
+      const int64_t chunk = (((K + e - 1) / e) + 63) / 64 * 64, E = ceil_div(K, chunk);
+      const double busiest = std::max<double>(m.few, static_cast<double>((tiles * E + 255) / 256));
+      const double tile_us = 2.0 * m.bm * m.bn * std::min(chunk, K) / (m.tflops * 1e6);
+      const double part_us = E > 1 ? 4.0 + 8.0 * E * M * N / 4e6 : 0.0;
+      const double us = busiest * (tile_us + 1.5) + part_us;
+      if (best.E != 0 && us >= best_us) continue;
+      best_us = us;
+      best.tile = m.tile;
+      best.bm = m.bm;
+      best.bn = m.bn;
+      best.ntm = ceil_div(M, m.bm);
+      best.ntn = ceil_div(N, m.bn);
+      best.kchunk = static_cast<int>(chunk);
+      best.E = static_cast<int>(E);
+      best.part_bytes = E > 1 ? static_cast<size_t>(E) * M * N * sizeof(float) : 0;
+    }
   }
-  const int64_t tiles = static_cast<int64_t>(q.ntm) * q.ntn;
-  int64_t E = std::max<int64_t>(1, std::min<int64_t>(fill / tiles, K / least));
-  q.kchunk = static_cast<int>((((K + E - 1) / E) + 63) / 64 * 64);
-  q.E = ceil_div(K, q.kchunk);
-  q.part_bytes = q.E > 1 ? static_cast<size_t>(q.E) * M * N * sizeof(float) : 0;
-  return q;
+  return best;
 }
 
 GemmArgs dense_args(const Product& q, int dtype, int64_t M, int64_t N, int64_t K) {
@@ -438,8 +458,12 @@ hipError_t product(const Product& q, GemmArgs& a, const LinearEpi& epi, void* pa
   a.out = part;
   const int grid = q.E * q.ntm * q.ntn;
   switch (q.tile) {
-    case TILE_256:
+    case TILE_256x256:
       MOE_TRY(launch(GEMM16(a.dtype, 256, 256, 128, 64, 64, 2, 1, GROUP_M, EPI_LINEAR, false, true, B_KC, 1),
+                     grid, a, s, 512));
+      break;
+    case TILE_256x192:
+      MOE_TRY(launch(GEMM16(a.dtype, 256, 192, 64, 96, 64, 2, 1, GROUP_M, EPI_LINEAR, false, true, B_KC, 1),
                      grid, a, s, 512));
       break;
     case TILE_128x64:
@@ -467,6 +491,9 @@ hipError_t product_rows(const Product& q, GemmArgs& a, void* out, void* part, hi
   const int grid = q.E * q.ntm * q.ntn;
   if (a.dtype == MOE_F32)
     MOE_TRY(launch(linear_f32_kernel<false, false, false>, grid, a, s));
+  else if (q.tile == TILE_192x192)
+    MOE_TRY(launch(GEMM16(a.dtype, 192, 192, 96, 96, 64, 2, 1, GROUP_K, EPI_LINEAR, false, false, false, 1),
+                   grid, a, s));
   else
     MOE_TRY(launch(GEMM16(a.dtype, 128, 256, 64, 128, 32, 3, 2, GROUP_K, EPI_LINEAR, false, false, false, 0),
                    grid, a, s));
@@ -494,8 +521,9 @@ hipError_t few_tokens(const LinearDims& d, const void* x, const void* w, const L
   return hipGetLastError();
 }
 
+// Groups of rows: about six blocks a CU.
 inline int dz_groups(const LinearDims& d) {
-  return std::min<int>(ceil_div(d.T, 4), std::max<int>(1, 768 / ceil_div(d.N, 512)));
+  return std::min<int>(ceil_div(d.T, 8), std::max<int>(1, 1536 / ceil_div(d.N, 512)));
 }
 
 struct BwdPlan {

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "colsum.h"
 #include "dropout.h"
 #include "residual.h"
 #include "row8.h"
@@ -302,39 +303,16 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
   if constexpr (GATE == MOE_GATE_CHANNEL) put(CS_GATE, a_gate);
 }
 
-// Adds the groups' partials: one block per 32 columns and column sum. 128 rows of 8 lanes, 16
-// bytes a lane, walk every 128th group; the 128 sums meet in LDS, in a fixed order.
+// Adds the blocks' partials: one block per 32 columns and column sum.
 template <typename Elem>
 __global__ __launch_bounds__(1024) void residual_colsum_kernel(ResidualBwdArgs q) {
   __shared__ float red[128][33];
-  const int cx = threadIdx.x & 7, ry = threadIdx.x >> 3, slot = blockIdx.y;
+  const int slot = blockIdx.y;
   const int64_t H = q.f.H;
-  const int c4 = blockIdx.x * 32 + cx * 4;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (c4 < H) {
-#pragma unroll 8
-    for (int64_t g = ry; g < q.groups; g += 128) {
-      const float4 v = *reinterpret_cast<const float4*>(q.part + (g * q.nslots + slot) * H + c4);
-      a.x += v.x;
-      a.y += v.y;
-      a.z += v.z;
-      a.w += v.w;
-    }
-  }
-  red[ry][cx * 4] = a.x;
-  red[ry][cx * 4 + 1] = a.y;
-  red[ry][cx * 4 + 2] = a.z;
-  red[ry][cx * 4 + 3] = a.w;
-  __syncthreads();
-  const int c = threadIdx.x & 31, part = threadIdx.x >> 5, col = blockIdx.x * 32 + c;
-  float s = (red[part][c] + red[part + 32][c]) + (red[part + 64][c] + red[part + 96][c]);
-  __syncthreads();
-  red[part][c] = s;
-  __syncthreads();
-  if (part != 0 || col >= H) return;
-  s = 0.f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) s += red[i][c];
+  int col;
+  float s;
+  if (!block_colsum(q.part + slot * H, q.groups, q.nslots * H, blockIdx.x * 32, q.f.H, red, col, s))
+    return;
   if (slot == q.slot[CS_GATE] && q.f.gate_sigmoid) {
     const float g = gate_value(to_f32<Elem>(static_cast<const Elem*>(q.f.gate)[col]), 1);
     s *= g * (1.f - g);
