@@ -379,33 +379,35 @@ __global__ __launch_bounds__(1024) void linear_colsum_kernel(const float* part, 
 constexpr int kFewTokens = 16;
 
 // One product of M x N outputs over K: tile shape, and slices of the reduction.
-enum Tile { TILE_256x256, TILE_256x192, TILE_192x192, TILE_128x64, TILE_128x256, TILE_F32 };
+enum Tile { TILE_256x256, TILE_256x192, TILE_192x192, TILE_128x128, TILE_128x64, TILE_128x256, TILE_F32 };
 struct Product {
   Tile tile;
   int bm, bn, ntm, ntn, E, kchunk;
   size_t part_bytes;  // 0: one slice, no partials
 };
 
-// The plan of least estimated time: the tiles of the busiest CU at the rate a CU reaches with them,
-// plus what a block cannot overlap, plus the slices' partials written and read and the launch that
-// sums them. `few` is the least number of tiles' time a CU takes: tiles of four waves keep a CU
-// busy by twos. Rates measured on full launches of each tile.
+// The plan of least estimated time: the tiles of the busiest CU at the rate a CU reaches with them
+// and what a tile cannot overlap, plus the slices' partials written and read and the launch that
+// sums them. `few`: the least number of tiles whose time a CU takes (tiles of four waves keep a CU
+// busy by twos). Fitted to launches of 8192 x 4096 x 2880 (full CUs) and of 64 to 2048 tokens; the
+// plans it gives 300 and 1000 tokens of that product take 23.6 and 43 us, 128 x 64 tiles 28.5 and 56.
 struct TileModel {
   Tile tile;
   int bm, bn;
-  double tflops, few;  // per CU, and see above
+  double tflops, few, over_us;  // per CU
 };
-constexpr TileModel kRows16[] = {{TILE_256x256, 256, 256, 4.2, 1.0},
-                                 {TILE_256x192, 256, 192, 4.1, 1.0},
-                                 {TILE_128x64, 128, 64, 2.7, 1.7}};
-constexpr TileModel kReduceRows16[] = {{TILE_192x192, 192, 192, 4.1, 1.0},
-                                       {TILE_128x256, 128, 256, 4.1, 1.4}};
-constexpr TileModel kF32[] = {{TILE_F32, 128, 128, 0.5, 1.5}};
+constexpr TileModel kRows16[] = {{TILE_256x256, 256, 256, 4.2, 1.0, 3.0},
+                                 {TILE_256x192, 256, 192, 4.1, 1.0, 3.0},
+                                 {TILE_128x128, 128, 128, 4.0, 1.2, 2.5},
+                                 {TILE_128x64, 128, 64, 2.7, 1.7, 1.5}};
+constexpr TileModel kReduceRows16[] = {{TILE_192x192, 192, 192, 4.1, 1.0, 2.5},
+                                       {TILE_128x256, 128, 256, 4.1, 1.4, 1.5}};
+constexpr TileModel kF32[] = {{TILE_F32, 128, 128, 0.5, 1.5, 1.5}};
 
 Product plan(int dtype, bool reduce_rows, int64_t M, int64_t N, int64_t K) {
   const bool f32 = dtype == MOE_F32;
   const TileModel* models = f32 ? kF32 : reduce_rows ? kReduceRows16 : kRows16;
-  const int count = f32 ? 1 : reduce_rows ? 2 : 3, least = f32 ? 128 : 256;
+  const int count = f32 ? 1 : reduce_rows ? 2 : 4, least = f32 ? 128 : 256;
   // a slice of a row reduction lies within a 32-bit buffer offset
   const int64_t e0 = reduce_rows ? (K * std::max(M, N) * 2 >> 30) + 1 : 1;
   const int64_t e1 = std::max<int64_t>(e0, std::min<int64_t>(32, K / least));
@@ -418,8 +420,8 @@ Product plan(int dtype, bool reduce_rows, int64_t M, int64_t N, int64_t K) {
       const int64_t chunk = (((K + e - 1) / e) + 63) / 64 * 64, E = ceil_div(K, chunk);
       const double busiest = std::max<double>(m.few, static_cast<double>((tiles * E + 255) / 256));
       const double tile_us = 2.0 * m.bm * m.bn * std::min(chunk, K) / (m.tflops * 1e6);
-      const double part_us = E > 1 ? 4.0 + 8.0 * E * M * N / 4e6 : 0.0;
-      const double us = busiest * (tile_us + 1.5) + part_us;
+      const double part_us = E > 1 ? 5.0 + 8.0 * E * M * N / 4e6 : 0.0;
+      const double us = busiest * (tile_us + m.over_us) + part_us;
       if (best.E != 0 && us >= best_us) continue;
       best_us = us;
       best.tile = m.tile;
@@ -465,6 +467,10 @@ hipError_t product(const Product& q, GemmArgs& a, const LinearEpi& epi, void* pa
     case TILE_256x192:
       MOE_TRY(launch(GEMM16(a.dtype, 256, 192, 64, 96, 64, 2, 1, GROUP_M, EPI_LINEAR, false, true, B_KC, 1),
                      grid, a, s, 512));
+      break;
+    case TILE_128x128:
+      MOE_TRY(launch(GEMM16(a.dtype, 128, 128, 64, 64, 64, 2, 2, GROUP_M, EPI_LINEAR, false, true, B_KC, 1),
+                     grid, a, s));
       break;
     case TILE_128x64:
       MOE_TRY(launch(GEMM16(a.dtype, 128, 64, 32, 64, 64, 3, 2, GROUP_M, EPI_LINEAR, false, true, B_KC, 0),
