@@ -507,8 +507,8 @@ def _device(*tensors):
 
 def _addr(t, shape, dtype, name, optional=False):
     """_ptr's checks; the address as a number."""
-    if (type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous()
-            and t.is_cuda):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
         return t.data_ptr()
     p = _ptr(t, shape, dtype, name, optional)
     return None if p is None else p.value

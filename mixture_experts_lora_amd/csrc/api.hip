@@ -945,6 +945,7 @@ moe_status moe_residual_norm_fwd(const moe_residual* desc, const void* h, const 
   if (st != MOE_OK) return st;
   a.h = h;
   a.y = y;
+  if (!y) a.alpha = 0.f;  // h' = h whatever alpha is
   a.h_out = h_out;
   a.x_out = x_out;
   a.stats = reinterpret_cast<float4*>(stats);
@@ -1041,6 +1042,9 @@ moe_status check_linear(const moe_linear_shape* s) {
     return fail(MOE_ERR_INVALID_ARG, "unknown activation " + std::to_string(s->act));
   if (s->K % 8 != 0 || s->N % 8 != 0)
     return fail(MOE_ERR_UNSUPPORTED, "K and N must be multiples of 8");
+  // 256 rows of a tile lie within a 32-bit buffer offset
+  if (s->K > (1 << 20) || s->N > (1 << 20))
+    return fail(MOE_ERR_UNSUPPORTED, "K or N > 2^20 is not supported");
   const int64_t e = esize(s->dtype);
   if (int64_t(s->T) * std::max(s->K, s->N) > (int64_t(1) << 35) / e)
     return fail(MOE_ERR_INVALID_ARG, "activation tensors larger than 32 GiB");

@@ -146,7 +146,10 @@ def test_residual_backward_refusals(lib):
     assert "no output" in err(lib)
     g = dict(dw_pre=0x60000000)
     assert call(desc(), g=g, ws=None) == 1
-    assert call(desc(), g=g, ws_bytes=64 * 128 * 4 - 1) == 3
+    need = ctypes.c_size_t()
+    assert lib.moe_residual_norm_workspace_bytes(ctypes.byref(desc()), ctypes.byref(need)) == 0
+    assert need.value >= 128 * 4
+    assert call(desc(), g=g, ws_bytes=need.value - 1) == 3
     assert "residual workspace needs" in err(lib)
     for kw in (dict(dx_out=P(0x11000004)), dict(dy=P(0x16000002)), dict(ws=P(0x18000004)),
                dict(g=dict(dw_pre=0x60000004))):
@@ -192,6 +195,7 @@ def lin(T=64, K=128, N=256, dtype=1, act=0, p=0.0):
     (dict(T=1 << 24, K=1032), 1),                        # x above 32 GiB
     (dict(K=32768, N=32768), 1),                         # w of 2 GiB
     (dict(K=16384, N=32768, dtype=0), 1),
+    (dict(K=(1 << 20) + 8, N=8), 2), (dict(N=1 << 21, K=8), 2),
 ])
 def test_linear_shape(lib, kw, status):
     f, b = ctypes.c_size_t(), ctypes.c_size_t()

@@ -118,11 +118,12 @@ def test_linear_backward(dtype, T, K, N):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("T,K,N", [(4000, 264, 3400), (4111, 1160, 520), (4352, 72, 4104),
-                                   (4352, 4104, 72), (300, 2400, 2568), (3000, 136, 136)])
+                                   (4352, 4104, 72), (300, 2400, 2568), (3000, 136, 136),
+                                   (4000, 3400, 264)])
 def test_linear_large_tiles(dtype, T, K, N):
     """Enough tiles for the widest ones: 256 x 256 in the forward (first), 256 x 192 in the forward
-    (third) and the input gradient (fourth), 192 x 192 in the weight gradient (fifth); the last
-    splits the weight gradient's rows into many slices."""
+    (third) and the input gradient (fourth), 192 x 192 in the weight gradient (fifth); the sixth
+    splits the weight gradient's rows into many slices; 256 x 256 in the input gradient (last)."""
     mel = _mel()
     say(f"[linear large] {dtype} T={T} K={K} N={N}")
     check_fwd(mel, T, K, N, dtype, "gelu_tanh", 0.1)

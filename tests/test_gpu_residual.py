@@ -77,7 +77,7 @@ def test_dropout_is_the_mask_and_one_rounding(dtype, n):
     assert torch.equal(inplace, dst)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_dropout_unaligned_and_its_neighbours(dtype):
     mel = _mel()
     say(f"[dropout unaligned] {dtype}")
@@ -124,7 +124,7 @@ def test_dropout_far_element_indexes():
 # ------------------------------------------------------------------ residual
 # (T, H): every width class of both kernels, T odd and down to one token
 SHAPES = [(1, 8), (5, 200), (333, 512), (67, 584), (129, 1024), (40, 2048), (300, 2880), (3, 4096),
-          (33, 7168), (2, 16384), (9, 8200)]
+          (33, 7168), (11, 8000), (2, 16384), (9, 8200)]
 # (post, pre, gate, sigmoid, alpha, shift, p)
 FORMS = [("none", "rms", "none", False, 1.0, 0.0, 0.0),
          ("rms", "rms", "channel", False, 0.5, 1.0, 0.1),
@@ -132,7 +132,9 @@ FORMS = [("none", "rms", "none", False, 1.0, 0.0, 0.0),
          ("none", "layer", "full", True, 0.3, 0.0, 0.25),
          ("rms", "none", "token", False, 1.0, 1.0, 0.5),
          ("none", "none", "none", False, 1.0, 0.0, 0.3),
-         ("layer", "none", "channel", True, -1.0, 0.0, 0.0)]
+         ("layer", "none", "channel", True, -1.0, 0.0, 0.0),
+         ("rms", "rms", "none", False, 0.22, 1.0, 0.1), ("layer", "rms", "none", False, 1.0, 0.0, 0.0),
+         ("none", "layer", "none", False, 1.0, 1.0, 0.05), ("rms", "none", "full", False, 2.0, 0.0, 0.0)]
 
 
 def _case(mel, T, H, dtype, form, seed=0):
