@@ -491,9 +491,16 @@ class Residual:
 # The calls around the residual stream are often a few microseconds of work (single tokens), so
 # their marshalling takes the short way when everything is in order, and the descriptors keep their
 # C structs and workspace sizes.
+@functools.cache
+def _one_gpu() -> bool:
+    return torch.cuda.device_count() == 1
+
+
 def _device(*tensors):
-    """Index of the GPU that a call's tensors are on; the launches run there, whichever device is
-    current. Refuses tensors of two devices."""
+    """Index of the GPU that a call's tensors (already known to be on one) are on; the launches run
+    there, whichever device is current. Refuses tensors of two devices."""
+    if _one_gpu():
+        return 0
     first = None
     for t in tensors:
         if t is None or not isinstance(t, torch.Tensor):
@@ -519,7 +526,7 @@ def _rng(rng, p):
 
 
 def _call(fn, name, device, stream, *args):
-    if device != torch.cuda.current_device():
+    if not _one_gpu() and device != torch.cuda.current_device():
         with torch.cuda.device(device):
             check(fn(*args, _stream(stream)), name)
     elif stream is None:

@@ -48,36 +48,65 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
   const float as = p.alpha * p.drop.scale;
 
   float a_wpre[CH][8], a_bpre[CH][8], a_wpost[CH][8], a_bpost[CH][8], a_gate[CH][8];
-  // the vectors along H, as they are applied (shift + w); 0 past the row, whose lanes then add
-  // nothing to a row's sums
-  float wpre[CH][8], wpost[CH][8], bpost[CH][8], gch[CH][8];
+  // The vectors along H, as they are applied (shift + w, the gate's value; 0 past the row, whose
+  // lanes then add nothing to a row's sums), or where those would not fit the registers (PACKED)
+  // as they are stored.
+  constexpr bool PACKED = CH == 1 && TPR >= 896 && YPATH && LAYER;
+  constexpr int NV = 4;  // w_pre, w_post, b_post, a channel gate
+  float held[PACKED ? 1 : NV][CH][8];
+  Row8<Elem> stored[PACKED ? NV : 1][CH];
+  float add[CH];
+  const int rb = p.H * static_cast<int>(sizeof(Elem));
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = lane + i * TPR;
-    Row8<Elem> r;
-    auto vector = [&](bool there, const void* v, float add, float (&out)[8]) {
-      r.zero();
-      if (there && c < cpr) r.load(static_cast<const Elem*>(v) + 8 * c);
-      r.get(out);
+    add[i] = c < cpr ? p.shift : 0.f;
+    const void* from[NV] = {pre ? p.w_pre : nullptr, post ? p.w_post : nullptr,
+                            post ? p.b_post : nullptr,
+                            GATE == MOE_GATE_CHANNEL ? p.gate : nullptr};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) out[j] = c < cpr ? out[j] + add : 0.f;
-    };
-    vector(pre, p.w_pre, p.shift, wpre[i]);
-    vector(post, p.w_post, p.shift, wpost[i]);
-    vector(post && p.b_post, p.b_post, 0.f, bpost[i]);
-    vector(GATE == MOE_GATE_CHANNEL, p.gate, 0.f, gch[i]);
+    for (int k = 0; k < NV; ++k) {
+      Row8<Elem> r;
+      r.load(row_buf(from[k], 0, rb), c);
+      if constexpr (PACKED) stored[k][i] = r;
+      else r.get(held[k][i]);
+    }
+    if constexpr (!PACKED) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) gch[i][j] = gate_value(gch[i][j], p.gate_sigmoid);
+      for (int j = 0; j < 8; ++j) {
+        held[0][i][j] += add[i];
+        held[1][i][j] += add[i];
+        held[3][i][j] = gate_value(held[3][i][j], p.gate_sigmoid);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       a_wpre[i][j] = a_bpre[i][j] = a_wpost[i][j] = a_bpost[i][j] = a_gate[i][j] = 0.f;
   }
+  auto vec = [&](auto kc, int i, float (&out)[8]) __attribute__((always_inline)) {
+    constexpr int k = decltype(kc)::value;
+    if constexpr (PACKED) {
+      stored[k][i].opaque();  // unpacked here each time, not once before the rows
+      stored[k][i].get(out);
+      if (k < 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] += add[i];
+      }
+      if (k == 3) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] = gate_value(out[j], p.gate_sigmoid);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[j] = held[k][i][j];
+    }
+  };
+  using std::integral_constant;
 
   // The next row is loaded while this one is reduced. Blocks of over 256 threads have registers
   // left for only what a row needs first, dx' and h' (the rest arrives during the first reduction),
-  // and rows of two chunks a thread for nothing.
-  constexpr bool AHEAD = CH == 1, AHEAD_ALL = AHEAD && TPR <= 256;
-  const int rb = p.H * static_cast<int>(sizeof(Elem));
+  // and those with the most sums, or two chunks a thread, for nothing.
+  constexpr bool AHEAD = CH == 1 && !PACKED, AHEAD_ALL = AHEAD && TPR <= 256;
   Row8<Elem> nd[CH], nx[CH], nh[CH], ny[CH];
   float4 nst = make_float4(0.f, 0.f, 0.f, 0.f);
   auto fetch_first = [&](int64_t row) __attribute__((always_inline)) {
@@ -137,13 +166,14 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
       const float off = -st.z * st.w;
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        float x[8], h[8];
+        float x[8], h[8], w[8];
         rx[i].get(x);
         rh[i].get(h);
+        vec(integral_constant<int, 0>(), i, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           hat[i][j] = LAYER ? fmaf(h[j], st.w, off) : h[j] * st.w;
-          d[i][j] = x[j] * wpre[i][j];
+          d[i][j] = x[j] * w[j];
           a_wpre[i][j] = fmaf(x[j], hat[i][j], a_wpre[i][j]);
           s1 = fmaf(d[i][j], hat[i][j], s1);
           if (LAYER) {
@@ -197,12 +227,14 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
       }
       if (YPATH) {
         ry[i].get(u[i]);
-        float v[8];
+        float v[8], w[8], b[8];
+        vec(integral_constant<int, 1>(), i, w);
+        if (LAYER && GATE != MOE_GATE_NONE) vec(integral_constant<int, 2>(), i, b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (post) u[i][j] = LAYER ? fmaf(u[i][j], st.y, off) : u[i][j] * st.y;
-          v[j] = post ? (LAYER ? fmaf(u[i][j], wpost[i][j], bpost[i][j]) : u[i][j] * wpost[i][j])
-                      : u[i][j];
+          if (GATE != MOE_GATE_NONE)
+            v[j] = post ? (LAYER ? fmaf(u[i][j], w[j], b[j]) : u[i][j] * w[j]) : u[i][j];
         }
         if (GATE != MOE_GATE_NONE) {
           // alpha drop(v) D: the gate's gradient before its sum and its sigmoid's slope
@@ -211,10 +243,12 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
             v[j] = !dropout || kept(p.drop, rnd[i], j) ? v[j] * f[j] : 0.f;
         }
         if (GATE == MOE_GATE_CHANNEL) {
+          float g[8];
+          vec(integral_constant<int, 3>(), i, g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             a_gate[i][j] += v[j];
-            f[j] *= gch[i][j];
+            f[j] *= g[j];
           }
         } else if (GATE == MOE_GATE_TOKEN) {
 #pragma unroll
@@ -240,7 +274,7 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
           for (int j = 0; j < 8; ++j) {
             a_wpost[i][j] = fmaf(f[j], u[i][j], a_wpost[i][j]);
             if (LAYER) a_bpost[i][j] += f[j];
-            f[j] *= wpost[i][j];  // d
+            f[j] *= w[j];  // d
             s1 = fmaf(f[j], u[i][j], s1);
             if (LAYER) s2 += f[j];
           }

@@ -37,6 +37,8 @@ template <typename T> struct Row8;
 template <> struct Row8<bf16_t> {
   uint4 a;
   __device__ void load(const bf16_t* p) { a = *reinterpret_cast<const uint4*>(p); }
+  // what is computed from this value after here is not computed before
+  __device__ void opaque() { asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w)); }
   __device__ void store(bf16_t* p) const { *reinterpret_cast<uint4*>(p) = a; }
   // chunk c (elements 8c ..) of a row
   __device__ void load(const __amdgpu_buffer_rsrc_t& b, int c) { a = buf_load(b, 16 * c); }
@@ -62,6 +64,8 @@ template <> struct Row8<bf16_t> {
 template <> struct Row8<f16_t> {
   uint4 a;
   __device__ void load(const f16_t* p) { a = *reinterpret_cast<const uint4*>(p); }
+  // what is computed from this value after here is not computed before
+  __device__ void opaque() { asm volatile("" : "+v"(a.x), "+v"(a.y), "+v"(a.z), "+v"(a.w)); }
   __device__ void store(f16_t* p) const { *reinterpret_cast<uint4*>(p) = a; }
   // chunk c (elements 8c ..) of a row
   __device__ void load(const __amdgpu_buffer_rsrc_t& b, int c) { a = buf_load(b, 16 * c); }
@@ -88,6 +92,7 @@ template <> struct Row8<f16_t> {
 };
 template <> struct Row8<float> {
   float4 a, b;
+  __device__ void opaque() {}  // nothing is unpacked
   __device__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
