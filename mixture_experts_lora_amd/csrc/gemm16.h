@@ -827,6 +827,47 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
   frag_addr<BM, BK, A_KC, MF>(FA, fa_base, lane);
   frag_addr<BN, BK, B_KC, NF>(FB, fb_base, lane);
 
+  // EPI_LINEAR epilogue: a slab's 32 x WN outputs in pieces of eight columns, 64 at a time. The
+  // bias's and residual's pieces of a slab are loaded while the slab before it is finished; those of
+  // the first one before the main loop where the tile is small enough to have registers for them
+  // (there the latency counts, too).
+  typedef std::conditional_t<F16, f16_t, bf16_t> DElem;
+  constexpr int DSEGS = WN / 8, DPASS = DENSE ? 32 * DSEGS / 64 : 1;
+  constexpr bool DEARLY = MF * NF <= 4;
+  DropKey dkey{};
+  // a lane's columns repeat every DREP pieces, so its bias does
+  constexpr int DREP = 64 % DSEGS == 0 ? 1 : 3;
+  static_assert(!DENSE || (DREP * 64 % DSEGS == 0 && DPASS % DREP == 0), "columns repeat");
+  Row8<DElem> dres[2][DPASS], dbias[DREP];
+  auto dplace = [&](int mi, int pass, int& m_local, int& col) __attribute__((always_inline)) {
+    m_local = wm * WM + mi * 32 + (pass * 64 + lane) / DSEGS;
+    col = n0 + wn * WN + 8 * ((pass * 64 + lane) % DSEGS);
+    return m_local < rows && col < p.N;  // N is a multiple of 8
+  };
+  auto dfetch = [&](int mi, Row8<DElem> (&r)[DPASS]) __attribute__((always_inline)) {
+    const bool finish = MODE == GROUP_M && p.E == 1;
+    if (mi == 0) {
+      dkey = drop_key(p.lin.drop);
+#pragma unroll
+      for (int pass = 0; pass < DREP; ++pass) {
+        int m_local, col;
+        dplace(0, pass, m_local, col);
+        dbias[pass].zero();
+        if (finish && p.lin.bias && col < p.N)
+          dbias[pass].load(static_cast<const DElem*>(p.lin.bias) + col);
+      }
+    }
+#pragma unroll
+    for (int pass = 0; pass < DPASS; ++pass) {
+      int m_local, col;
+      r[pass].zero();
+      if (dplace(mi, pass, m_local, col) && finish && p.lin.residual)
+        r[pass].load(static_cast<const DElem*>(p.lin.residual) +
+                     static_cast<int64_t>(m0 + m_local) * p.N + col);
+    }
+  };
+  if constexpr (DENSE && DEARLY) dfetch(0, dres[0]);
+
   f32x16 acc[MF][NF];
 #pragma unroll
   for (int i = 0; i < MF; ++i)
@@ -1339,29 +1380,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
   };
   if constexpr (HPRE) hfetch(0, hpre[0]);
   if constexpr (DENSE) {
-    // The slab's 32 x WN outputs in pieces of eight columns, 64 at a time. The residual's pieces of
-    // a slab are loaded while the slab before it is finished.
-    typedef std::conditional_t<F16, f16_t, bf16_t> Elem;
-    constexpr int SEGS = WN / 8, PASS = 32 * SEGS / 64;
-    const bool part = p.E > 1, finish = MODE == GROUP_M && !part;
-    const DropKey key = drop_key(p.lin.drop);
-    Row8<Elem> res[2][PASS];
-    auto place = [&](int mi, int pass, int& m_local, int& col) __attribute__((always_inline)) {
-      m_local = wm * WM + mi * 32 + (pass * 64 + lane) / SEGS;
-      col = n0 + wn * WN + 8 * ((pass * 64 + lane) % SEGS);
-      return m_local < rows && col < p.N;  // N is a multiple of 8
-    };
-    auto rfetch = [&](int mi, Row8<Elem> (&r)[PASS]) __attribute__((always_inline)) {
-#pragma unroll
-      for (int pass = 0; pass < PASS; ++pass) {
-        int m_local, col;
-        r[pass].zero();
-        if (finish && p.lin.residual && place(mi, pass, m_local, col))
-          r[pass].load(static_cast<const Elem*>(p.lin.residual) +
-                       static_cast<int64_t>(m0 + m_local) * p.N + col);
-      }
-    };
-    rfetch(0, res[0]);
+    if (!DEARLY) dfetch(0, dres[0]);
 #pragma unroll
     for (int mi = 0; mi < MF; ++mi) {
       if (mi) wave_lds_sync();  // previous slab fully read
@@ -1374,22 +1393,23 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
           for (int j = 0; j < 4; ++j) v[j] = acc[mi][ni][4 * q + j];
           *reinterpret_cast<f32x4*>(slab + slab_off<WN>(srow, ni * 8 + 2 * q + shalf)) = v;
         }
-      if (mi + 1 < MF) rfetch(mi + 1, res[(mi + 1) & 1]);
+      if (mi + 1 < MF) dfetch(mi + 1, dres[(mi + 1) & 1]);
       wave_lds_sync();
 #pragma unroll
-      for (int pass = 0; pass < PASS; ++pass) {
+      for (int pass = 0; pass < DPASS; ++pass) {
         int m_local, col;
-        const bool in = place(mi, pass, m_local, col);
+        const bool in = dplace(mi, pass, m_local, col);
         float v[8];
-        read8_interleaved<WN>(slab, (pass * 64 + lane) / SEGS, (pass * 64 + lane) % SEGS, v);
+        read8_interleaved<WN>(slab, (pass * 64 + lane) / DSEGS, (pass * 64 + lane) % DSEGS, v);
         if (!in) continue;
         const int64_t row = m0 + m_local;
-        if (part) {
+        if (p.E > 1) {
           Row8<float> o;
           o.set(v);
           o.store(static_cast<float*>(p.out) + (static_cast<int64_t>(e) * p.M + row) * p.N + col);
         } else if (MODE == GROUP_M) {
-          linear_finish8<Elem>(p.lin, key, row, col, p.N, res[mi & 1][pass], v);
+          linear_finish8<DElem>(p.lin, dkey, row, col, p.N, dbias[pass % DREP],
+                                dres[mi & 1][pass], v);
         } else {
           store8<F16>(static_cast<bf16_t*>(p.out) + row * p.N + col, v);
         }

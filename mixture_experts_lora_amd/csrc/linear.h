@@ -61,21 +61,18 @@ __device__ __forceinline__ float act_slope(float z, int act) {
   }
 }
 
-// v: the product's columns col .. col + 7 of `row`; ncols (a multiple of 8) is y's row length; res:
-// the residual's elements there (zeros without one).
+// v: the product's columns col .. col + 7 of `row`; ncols (a multiple of 8) is y's row length; bias,
+// res: the bias's and the residual's elements there (zeros without one).
 template <typename Elem>
 __device__ __forceinline__ void linear_finish8(const LinearEpi& q, const DropKey& key, int64_t row,
-                                               int col, int ncols, const Row8<Elem>& res,
-                                               float (&v)[8]) {
+                                               int col, int ncols, const Row8<Elem>& bias,
+                                               const Row8<Elem>& res, float (&v)[8]) {
   const int64_t at = row * ncols + col;
   Row8<Elem> r;
   float f[8];
-  if (q.bias) {
-    r.load(static_cast<const Elem*>(q.bias) + col);
-    r.get(f);
+  bias.get(f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += f[j];
-  }
+  for (int j = 0; j < 8; ++j) v[j] += f[j];
   if (q.pre) {
     r.set(v);
     r.store(static_cast<Elem*>(q.pre) + at);
@@ -96,14 +93,16 @@ __device__ __forceinline__ void linear_finish8(const LinearEpi& q, const DropKey
   r.store(static_cast<Elem*>(q.y) + at);
 }
 
-// The same with the residual loaded here.
+// The same with the bias and the residual loaded here.
 template <typename Elem>
 __device__ __forceinline__ void linear_finish8(const LinearEpi& q, int64_t row, int col, int ncols,
                                                float (&v)[8]) {
-  Row8<Elem> res;
+  Row8<Elem> bias, res;
+  bias.zero();
   res.zero();
+  if (q.bias) bias.load(static_cast<const Elem*>(q.bias) + col);
   if (q.residual) res.load(static_cast<const Elem*>(q.residual) + row * ncols + col);
-  linear_finish8<Elem>(q, drop_key(q.drop), row, col, ncols, res, v);
+  linear_finish8<Elem>(q, drop_key(q.drop), row, col, ncols, bias, res, v);
 }
 
 }  // namespace moe
