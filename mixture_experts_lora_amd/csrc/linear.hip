@@ -379,7 +379,7 @@ __global__ __launch_bounds__(1024) void linear_colsum_kernel(const float* part, 
 constexpr int kFewTokens = 16;
 
 // One product of M x N outputs over K: tile shape, and slices of the reduction.
-enum Tile { TILE_256x256, TILE_256x192, TILE_192x192, TILE_128x128, TILE_128x64, TILE_128x256, TILE_F32 };
+enum Tile { TILE_256x256, TILE_256x192, TILE_192x192, TILE_128x128, TILE_128x64, TILE_64x64, TILE_128x256, TILE_F32 };
 struct Product {
   Tile tile;
   int bm, bn, ntm, ntn, E, kchunk;
@@ -399,7 +399,8 @@ struct TileModel {
 constexpr TileModel kRows16[] = {{TILE_256x256, 256, 256, 4.2, 1.0, 3.0},
                                  {TILE_256x192, 256, 192, 4.1, 1.0, 3.0},
                                  {TILE_128x128, 128, 128, 4.0, 1.2, 2.5},
-                                 {TILE_128x64, 128, 64, 2.7, 1.7, 1.5}};
+                                 {TILE_128x64, 128, 64, 2.7, 1.7, 1.5},
+                                 {TILE_64x64, 64, 64, 1.4, 2.0, 0.8}};
 constexpr TileModel kReduceRows16[] = {{TILE_192x192, 192, 192, 4.1, 1.0, 2.5},
                                        {TILE_128x256, 128, 256, 4.1, 1.4, 1.5}};
 constexpr TileModel kF32[] = {{TILE_F32, 128, 128, 0.5, 1.5, 1.5}};
@@ -407,7 +408,7 @@ constexpr TileModel kF32[] = {{TILE_F32, 128, 128, 0.5, 1.5, 1.5}};
 Product plan(int dtype, bool reduce_rows, int64_t M, int64_t N, int64_t K) {
   const bool f32 = dtype == MOE_F32;
   const TileModel* models = f32 ? kF32 : reduce_rows ? kReduceRows16 : kRows16;
-  const int count = f32 ? 1 : reduce_rows ? 2 : 4, least = f32 ? 128 : 256;
+  const int count = f32 ? 1 : reduce_rows ? 2 : 5, least = f32 ? 128 : 256;
   // a slice of a row reduction lies within a 32-bit buffer offset
   const int64_t e0 = reduce_rows ? (K * std::max(M, N) * 2 >> 30) + 1 : 1;
   const int64_t e1 = std::max<int64_t>(e0, std::min<int64_t>(32, K / least));
@@ -474,6 +475,10 @@ hipError_t product(const Product& q, GemmArgs& a, const LinearEpi& epi, void* pa
       break;
     case TILE_128x64:
       MOE_TRY(launch(GEMM16(a.dtype, 128, 64, 32, 64, 64, 3, 2, GROUP_M, EPI_LINEAR, false, true, B_KC, 0),
+                     grid, a, s));
+      break;
+    case TILE_64x64:
+      MOE_TRY(launch(GEMM16(a.dtype, 64, 64, 32, 32, 64, 5, 2, GROUP_M, EPI_LINEAR, false, true, B_KC, 0),
                      grid, a, s));
       break;
     case TILE_F32:
