@@ -314,10 +314,16 @@ struct Geo {
   static constexpr int NIW = (TI + NW - 1) / NW;   // per wave (upper bound)
   static constexpr int MINW = TI / NW;             // issued by every wave
   static constexpr int CPR = KC ? BK / 8 : ROWS / 8;        // chunks per LDS row
-  // Row and chunk position that lane `lane` of instruction j fills.
-  __device__ static int row(int j, int lane) { return (64 * j + lane) / CPR; }
-  __device__ static int pos(int j, int lane) { return (64 * j + lane) % CPR; }
   static constexpr int RPI = KC ? 512 / BK : 512 / ROWS;    // LDS rows per instruction
+  // Row and chunk position that lane `lane` of instruction j fills. Where an instruction fills
+  // whole rows the part that depends on j is kept apart, so that it folds into the instructions'
+  // offsets (one form for both: up to 440 more instructions in a grouped product).
+  __device__ static int row(int j, int lane) {
+    return 64 % CPR == 0 ? RPI * j + lane / CPR : (64 * j + lane) / CPR;
+  }
+  __device__ static int pos(int j, int lane) {
+    return 64 % CPR == 0 ? lane % CPR : (64 * j + lane) % CPR;
+  }
 };
 
 // DMA plan of one operand tile: buffer (base, bytes), per-instruction lane offsets.
@@ -830,7 +836,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
   // EPI_LINEAR epilogue: a slab's 32 x WN outputs in pieces of eight columns, 64 at a time. The
   // bias's and residual's pieces of a slab are loaded while the slab before it is finished; those of
   // the first one before the main loop where the tile is small enough to have registers for them
-  // (there the latency counts, too).
+  // (there the latency counts, too). One block a CU does not overlap it with products: of the 197 us
+  // that 8192 x 4096 x 2880 bf16 with bias, dropout and residual takes (983 TFLOP/s), the bare
+  // product in the same run takes 190.
   typedef std::conditional_t<F16, f16_t, bf16_t> DElem;
   constexpr int DSEGS = WN / 8, DPASS = DENSE ? 32 * DSEGS / 64 : 1;
   constexpr bool DEARLY = MF * NF <= 4;
