@@ -107,6 +107,10 @@ def step_flops(cfg, full_ft, shared_I=None, block=False):
 # headers it includes, and the build flags); a change to any of them makes
 # the recorded traffic stale.
 TRAFFIC_SOURCES = ("mixture_experts_lora_amd/csrc/gemm.hip",
+                   "mixture_experts_lora_amd/csrc/gemm16.h",
+                   "mixture_experts_lora_amd/csrc/linear.h",
+                   "mixture_experts_lora_amd/csrc/dropout.h",
+                   "mixture_experts_lora_amd/csrc/row8.h",
                    "mixture_experts_lora_amd/csrc/device_common.h",
                    "mixture_experts_lora_amd/csrc/launch.h",
                    "mixture_experts_lora_amd/build.py")

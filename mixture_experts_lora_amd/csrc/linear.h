@@ -15,7 +15,7 @@ constexpr float kGeluA = 0.044715f;
 // Phi(z), and e = exp(-z^2 / 2), by Abramowitz and Stegun 7.1.26 (erfc as a polynomial in
 // t = 1 / (1 + p x) times exp(-x^2), within 1.5e-7): a dozen instructions that the slope's
 // exponential is part of, where erff and an exponential of its own take about eighty and bound the
-// kernel that forms dz (8192 x 2880, gelu: 43 us).
+// kernel that forms dz (8192 x 2880, gelu: 43 us, with the polynomial 27.6).
 __device__ __forceinline__ float gelu_phi(float z, float& e) {
   const float x = fabsf(z) * 0.7071067811865476f;
   e = __expf(-x * x);

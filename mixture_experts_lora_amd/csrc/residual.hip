@@ -30,7 +30,9 @@ namespace {
 
 // ------------------------------------------------------------------ element-wise dropout
 // One thread per 8 elements (one counter); VEC: both pointers on a 16-byte boundary. src and dst
-// may be the same buffer: a thread reads its elements before it writes them.
+// may be the same buffer: a thread reads its elements before it writes them. Bound by HBM: the
+// generator's twenty multiplies serve 16 bytes read and 16 written (65536 x 2880 bf16: 123.5 us,
+// 6.1 TB/s, part of it from the last-level cache; 300 x 584: 2.4 us).
 template <typename Elem, bool VEC>
 __global__ __launch_bounds__(256) void dropout_kernel(const Elem* src, Elem* dst, int64_t n,
                                                       DropArgs d) {
@@ -87,7 +89,9 @@ __device__ __forceinline__ void row_stats(const float (&u)[CH][8], const bool (&
 // TPR threads a row, in CH chunks of 8 elements a thread; each takes every so many-th row, with
 // the vectors along H in registers over the rows and the next row in flight while one is reduced.
 // A row is read once and h', x' are written once. A thread reads all of its h and y before it
-// writes anything of that row, so h' may be h.
+// writes anything of that row, so h' may be h. Bound by HBM (8192 x 2880 bf16 with one norm:
+// 37.8 us, 5.0 TB/s, where a large copy takes 37; 16384 x 2048 fp16 with both norms, a gate and
+// dropout: 55.8 us, a copy 53; one row: 2.6 us).
 template <typename Elem, int TPR, int CH, int GATE>
 __global__ __launch_bounds__(row_block<TPR>()) void residual_fwd_kernel(ResidualArgs p) {
   constexpr int BLOCK = row_block<TPR>(), R = BLOCK / TPR;

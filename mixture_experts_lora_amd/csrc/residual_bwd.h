@@ -28,7 +28,8 @@ enum ColSum { CS_W_PRE = 0, CS_B_PRE = 1, CS_W_POST = 2, CS_B_POST = 3, CS_GATE 
 // Vector instructions cost nearly as much as the memory: with sums of 8192 x 7168 rows, both norms,
 // a gate and dropout, 65 an element take 100 of 170 us. So norms are one fused multiply-add an
 // element (uhat = u rstd - mean rstd), constants along a row are folded, and what a row's second
-// pass needs is kept from the first.
+// pass needs is kept from the first (now 158.7 us, where a large copy takes 138; 8192 x 2880 bf16
+// with one norm: 49.1 us, a copy 46).
 template <typename Elem, int TPR, int CH, bool YPATH, bool LAYER, int GATE>
 __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(ResidualBwdArgs q) {
   const ResidualArgs& p = q.f;
@@ -337,7 +338,8 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
   if constexpr (GATE == MOE_GATE_CHANNEL) put(CS_GATE, a_gate);
 }
 
-// Adds the blocks' partials: one block per 32 columns and column sum.
+// Adds the blocks' partials: one block per 32 columns and column sum, bound by the latency of its
+// few loads and the launch (4.9 us after 8192 x 2880 rows).
 template <typename Elem>
 __global__ __launch_bounds__(1024) void residual_colsum_kernel(ResidualBwdArgs q) {
   __shared__ float red[128][33];
