@@ -34,9 +34,9 @@ namespace {
 // generator's twenty multiplies serve 16 bytes read and 16 written (65536 x 2880 bf16: 123.5 us,
 // 6.1 TB/s, part of it from the last-level cache; 300 x 584: 2.4 us).
 template <typename Elem, bool VEC>
-__global__ __launch_bounds__(256) void dropout_kernel(const Elem* src, Elem* dst, int64_t n,
-                                                      DropArgs d) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, i = c * 8;
+__global__ __launch_bounds__(256) void dropout_kernel(const Elem* src, Elem* dst, int64_t c0,
+                                                      int64_t n, DropArgs d) {
+  const int64_t c = c0 + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, i = c * 8;
   if (i >= n) return;
   const DropKey key = drop_key(d);
   Row8<Elem> r;
@@ -227,13 +227,20 @@ hipError_t launch_dropout(int dtype, int64_t n, const DropArgs& d, const void* s
                           hipStream_t s, KernelTimer* tm) {
   TimedScope ts(tm, MOE_K_DROPOUT, s);
   const bool vec = ((reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst)) & 15) == 0;
-  const dim3 grid(static_cast<unsigned>(((n + 7) / 8 + 255) / 256));
+  const int64_t chunks = (n + 7) / 8;
   return by_type(dtype, [&](auto tag) {
     using Elem = decltype(tag);
     auto* kern = vec ? dropout_kernel<Elem, true> : dropout_kernel<Elem, false>;
-    hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, static_cast<const Elem*>(src),
-                       static_cast<Elem*>(dst), n, d);
-    return hipGetLastError();
+    // a grid has fewer than 2^32 threads
+    constexpr int64_t kMost = int64_t(1) << 31;
+    for (int64_t c0 = 0; c0 < chunks; c0 += kMost) {
+      const dim3 grid(static_cast<unsigned>((std::min(kMost, chunks - c0) + 255) / 256));
+      hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, static_cast<const Elem*>(src),
+                         static_cast<Elem*>(dst), c0, n, d);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   });
 }
 

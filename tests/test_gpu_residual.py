@@ -121,6 +121,26 @@ def test_dropout_far_element_indexes():
     assert np.array_equal(_np(src[lo:]), want)
 
 
+def test_dropout_of_more_threads_than_a_grid_holds():
+    """2^35 elements are 2^32 threads, one more than a launch may have: in place, around the
+    borders of the parts and at the end."""
+    mel = _mel()
+    n = (1 << 35) + 8 * 5 + 3
+    if torch.cuda.mem_get_info()[0] < 2 * n + (8 << 30):
+        pytest.skip("needs 72 GiB of free GPU memory")
+    say(f"[dropout huge] n={n}")
+    src = torch.ones(n, device="cuda", dtype=torch.bfloat16)
+    mel.moe_dropout(src, src, 0.5, _rng())
+    for lo, hi in ((0, 4096), ((1 << 34) - 64, (1 << 34) + 64), ((1 << 35) - 64, n)):
+        ctr = np.arange(lo // 8, (hi + 7) // 8, dtype=np.uint64)
+        words = R.philox4x32((ctr & np.uint64(R.MASK32), ctr >> np.uint64(32), 123, 0), (77, 0))
+        u16 = np.stack([h for w in words for h in (w & np.uint64(0xFFFF), w >> np.uint64(16))], 1)
+        want = np.where(u16.reshape(-1)[:hi - lo] >= 32768, 2.0, 0.0)
+        assert np.array_equal(_np(src[lo:hi]), want), lo
+    del src
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ residual
 # (T, H): every width class of both kernels, T odd and down to one token
 SHAPES = [(1, 8), (5, 200), (333, 512), (67, 584), (129, 1024), (40, 2048), (300, 2880), (3, 4096),
