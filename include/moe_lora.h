@@ -502,9 +502,10 @@ typedef struct {
  *   dx, dw, dbias   NULL: not wanted; x is read for dw, w for dx (else may be NULL)
  * ws: moe_linear_workspace_bytes (either may be 0: ws may then be NULL). Results
  * repeat bit for bit. Errors: T, K, N < 1, an unknown act or dtype, T * max(K, N)
- * elements above 32 GiB, w of 2 GiB or more, K or N not a multiple of 8
- * or above 2^20 (MOE_ERR_UNSUPPORTED), a pointer off a 16-byte boundary (rng: 8), an output that
- * overlaps an input or another output (apart from y = residual). */
+ * elements above 32 GiB, w of 2 GiB or more, a pointer off a 16-byte boundary
+ * (rng: 8), an output that overlaps an input or another output (apart from
+ * y = residual); MOE_ERR_UNSUPPORTED: T of 2^30 or more, K or N not a multiple
+ * of 8 or above 2^20. */
 moe_status moe_linear_workspace_bytes(const moe_linear_shape *shape, size_t *fwd_ws,
                                       size_t *bwd_ws);
 moe_status moe_linear_fwd(const moe_linear_shape *shape, const void *x, const void *w,

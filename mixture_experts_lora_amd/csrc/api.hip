@@ -1045,6 +1045,8 @@ moe_status check_linear(const moe_linear_shape* s) {
   // 256 rows of a tile lie within a 32-bit buffer offset
   if (s->K > (1 << 20) || s->N > (1 << 20))
     return fail(MOE_ERR_UNSUPPORTED, "K or N > 2^20 is not supported");
+  // 64 rows a tile of 256 threads: a grid has fewer than 2^32 threads
+  if (s->T >= (1 << 30)) return fail(MOE_ERR_UNSUPPORTED, "T >= 2^30 is not supported");
   const int64_t e = esize(s->dtype);
   if (int64_t(s->T) * std::max(s->K, s->N) > (int64_t(1) << 35) / e)
     return fail(MOE_ERR_INVALID_ARG, "activation tensors larger than 32 GiB");

@@ -189,6 +189,14 @@ def lin(T=64, K=128, N=256, dtype=1, act=0, p=0.0):
     return MoeLinearShape(T, K, N, dtype, act, p)
 
 
+@pytest.mark.parametrize("T,status", [(1 << 30, 2), ((1 << 31) - 1, 2), ((1 << 30) - 1, 0)])
+def test_linear_tokens_fit_a_grid(lib, T, status):
+    """16-byte rows keep the tensors below 32 GiB; from 2^30 on a launch may need 2^32 threads."""
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.moe_linear_workspace_bytes(ctypes.byref(lin(T=T, K=8, N=8)), ctypes.byref(f),
+                                          ctypes.byref(b)) == status
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(T=0), 1), (dict(K=0), 1), (dict(N=-8), 1), (dict(dtype=4), 1), (dict(act=5), 1),
     (dict(act=-1), 1), (dict(K=100), 2), (dict(N=12), 2),
