@@ -6,6 +6,7 @@
 #include <initializer_list>
 #include <mutex>
 #include <string>
+#include <string_view>
 #include <vector>
 
 #include "launch.h"
@@ -759,6 +760,7 @@ struct Range {
   const void* p;
   int64_t bytes;
   const char* name;
+  const char* may_be = nullptr;  // an input: the name of the output that may be this very buffer
 };
 
 bool ranges_overlap(const Range& a, const Range& b) {
@@ -767,13 +769,14 @@ bool ranges_overlap(const Range& a, const Range& b) {
   return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
 }
 
-// No output may overlap an input or another output; the pairs in `same` (an
-// output and an input) may be one and the same buffer.
-moe_status check_ranges(std::initializer_list<Range> outs, std::initializer_list<Range> ins,
-                        const void* same_out, const void* same_in) {
+// No output may overlap an input or another output, apart from the inputs that name one. The name
+// decides, not the address: another input at the same address is read by blocks that the output's
+// own do not wait for.
+moe_status check_ranges(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
   for (const Range& o : outs) {
     for (const Range& i : ins)
-      if (ranges_overlap(o, i) && !(o.p == same_out && i.p == same_in && o.p == i.p))
+      if (ranges_overlap(o, i) &&
+          !(i.may_be && o.p == i.p && std::string_view(i.may_be) == o.name))
         return fail(MOE_ERR_INVALID_ARG, std::string(o.name) + " overlaps " + i.name);
     for (const Range& other : outs)
       if (&o != &other && ranges_overlap(o, other))
@@ -900,8 +903,7 @@ moe_status moe_dropout(int32_t dtype, int64_t n, float p, const int64_t* rng, in
   CHECK_PTR(src);
   CHECK_PTR(dst);
   const int64_t bytes = n * esize(dtype);
-  st = check_ranges({{dst, bytes, "dst"}}, {{src, bytes, "src"}, {d.thr ? rng : nullptr, 16, "rng"}},
-                    dst, src);
+  st = check_ranges({{dst, bytes, "dst"}}, {{src, bytes, "src", "dst"}, {d.thr ? rng : nullptr, 16, "rng"}});
   if (st != MOE_OK) return st;
   hipError_t e = moe::launch_dropout(dtype, n, d, src, dst, as_stream(stream), moe::active_timer());
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_dropout");
@@ -938,10 +940,9 @@ moe_status moe_residual_norm_fwd(const moe_residual* desc, const void* h, const 
   CHECK_ROWS(stats);
   const int64_t row = desc->H * esize(desc->dtype), rows = row * desc->T;
   st = check_ranges({{h_out, rows, "h_out"}, {x_out, rows, "x_out"}, {stats, int64_t(desc->T) * 16, "stats"}},
-                    {{h, rows, "h"}, {y, rows, "y"}, {a.w_post, row, "w_post"}, {a.b_post, row, "b_post"},
+                    {{h, rows, "h", "h_out"}, {y, rows, "y"}, {a.w_post, row, "w_post"}, {a.b_post, row, "b_post"},
                      {a.gate, gate_bytes(desc), "gate"}, {a.w_pre, row, "w_pre"}, {a.b_pre, row, "b_pre"},
-                     {a.drop.thr ? rng : nullptr, 16, "rng"}},
-                    h_out, h);
+                     {a.drop.thr ? rng : nullptr, 16, "rng"}});
   if (st != MOE_OK) return st;
   a.h = h;
   a.y = y;
@@ -1011,12 +1012,11 @@ moe_status moe_residual_norm_bwd(const moe_residual* desc, const void* dh_out, c
        {q.colsum[0], row, "dw_pre"}, {q.colsum[1], row, "db_pre"}, {q.colsum[2], row, "dw_post"},
        {q.colsum[3], row, "db_post"}, {q.colsum[4], row, "dgate"},
        {q.nslots ? ws : nullptr, static_cast<int64_t>(need), "ws"}},
-      {{dh_out, rows, "dh_out"}, {dx_out, rows, "dx_out"}, {pre ? h_out : nullptr, rows, "h_out"},
+      {{dh_out, rows, "dh_out", "dh"}, {dx_out, rows, "dx_out"}, {pre ? h_out : nullptr, rows, "h_out"},
        {post || gate ? y : nullptr, rows, "y"}, {pre || post ? stats : nullptr, int64_t(desc->T) * 16, "stats"},
        {q.f.w_post, row, "w_post"}, {q.f.b_post, row, "b_post"}, {q.f.gate, gate_bytes(desc), "gate"},
        {q.f.w_pre, row, "w_pre"}, {q.f.b_pre, row, "b_pre"},
-       {q.f.drop.thr ? rng : nullptr, 16, "rng"}},
-      dh, dh_out);
+       {q.f.drop.thr ? rng : nullptr, 16, "rng"}});
   if (st != MOE_OK) return st;
   q.f.y = y;
   q.f.stats = pre || post ? reinterpret_cast<float4*>(const_cast<float*>(stats)) : nullptr;
@@ -1100,9 +1100,8 @@ moe_status moe_linear_fwd(const moe_linear_shape* shape, const void* x, const vo
   const int64_t e = esize(d.dtype), out = int64_t(d.T) * d.N * e;
   st = check_ranges({{y, out, "y"}, {pre, out, "pre"}, {need ? ws : nullptr, int64_t(need), "ws"}},
                     {{x, int64_t(d.T) * d.K * e, "x"}, {w, int64_t(d.N) * d.K * e, "w"},
-                     {bias, d.N * e, "bias"}, {residual, out, "residual"},
-                     {epi.drop.thr ? rng : nullptr, 16, "rng"}},
-                    y, residual);
+                     {bias, d.N * e, "bias"}, {residual, out, "residual", "y"},
+                     {epi.drop.thr ? rng : nullptr, 16, "rng"}});
   if (st != MOE_OK) return st;
   epi.bias = bias;
   epi.residual = residual;
@@ -1146,8 +1145,7 @@ moe_status moe_linear_bwd(const moe_linear_shape* shape, const void* dy, const v
                      {need ? ws : nullptr, int64_t(need), "ws"}},
                     {{dy, out, "dy"}, {dw ? x : nullptr, in, "x"}, {dx ? w : nullptr, wb, "w"},
                      {shape->act != MOE_ACT_NONE ? pre : nullptr, out, "pre"},
-                     {epi.drop.thr ? rng : nullptr, 16, "rng"}},
-                    nullptr, nullptr);
+                     {epi.drop.thr ? rng : nullptr, 16, "rng"}});
   if (st != MOE_OK) return st;
   epi.pre = const_cast<void*>(pre);
   epi.act = shape->act;

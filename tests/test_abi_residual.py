@@ -247,3 +247,42 @@ def test_linear_refusals(lib):
     for kw in (dict(dx=at(0)), dict(dx=at(6)), dict(dw=at(1)), dict(db=at(3)), dict(ws=at(5)),
                dict(dx=P(at(2).value + 16))):
         assert bwd(**kw) == 1 and "overlaps" in err(lib), kw
+
+
+def test_only_the_named_input_may_be_the_output(lib):
+    """In place means one input and one output: another input at the same address is read by
+    blocks that do not wait for the one that writes it."""
+    from mixture_experts_lora_amd._lib import MoeResidualGrads
+    B = ctypes.byref
+
+    def overlaps(status, what):
+        assert status == 1 and what in err(lib), (status, err(lib))
+
+    # a square product: y over the residual, which x, w or the bias is too
+    for T in (1, 2, 16, 300):
+        sh = lin(T=T, K=520, N=520)
+        f = ctypes.c_size_t()
+        assert lib.moe_linear_workspace_bytes(B(sh), B(f), None) == 0
+
+        def fwd(x=at(0), w=at(1), bias=at(2), y=at(3), sh=sh, n=f.value):
+            return lib.moe_linear_fwd(B(sh), x, w, bias, at(3), None, 0, y, None, at(7), n, None)
+
+        overlaps(fwd(x=at(3)), "y overlaps x")
+        overlaps(fwd(w=at(3)), "y overlaps w")
+        overlaps(fwd(bias=at(3)), "y overlaps bias")
+    # the stream written over, whose buffer is another input's too
+    for kw, q, y, what in ((dict(), {}, at(0), "y"), (dict(), dict(w_pre=at(0).value), at(1), "w_pre"),
+                           (dict(gate=2), dict(gate=at(0).value), at(1), "gate"),
+                           (dict(post=2), dict(b_post=at(0).value), at(1), "b_post")):
+        overlaps(lib.moe_residual_norm_fwd(B(desc(**kw)), at(0), y, B(params(**q)), None, 0, at(0),
+                                           at(3), at(4), None), "h_out overlaps " + what)
+    for kw, dx, h_out, y, stats, q, what in (
+            (dict(), at(0), at(2), at(3), at(4), {}, "dx_out"),
+            (dict(), at(1), at(0), at(3), at(4), {}, "h_out"),
+            (dict(post=1), at(1), at(2), at(0), at(4), {}, "y"),
+            (dict(), at(1), at(2), at(3), at(0), {}, "stats"),
+            (dict(gate=3), at(1), at(2), at(3), at(4), dict(gate=at(0).value), "gate")):
+        overlaps(lib.moe_residual_norm_bwd(B(desc(**kw)), at(0), dx, h_out, y, B(params(**q)), stats,
+                                           None, 0, at(0), at(6), B(MoeResidualGrads()), at(8),
+                                           1 << 20, None), "dh overlaps " + what)
+    overlaps(lib.moe_dropout(1, 64, 0.1, at(0), 0, at(0), at(0), None), "dst overlaps rng")
