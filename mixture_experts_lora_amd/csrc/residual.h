@@ -71,6 +71,9 @@ __device__ __forceinline__ int row_in_block() {
 __device__ __forceinline__ float gate_value(float g, int sigmoid) {
   return sigmoid ? sigmoidf_(g) : g;
 }
+// The sigmoid's slope s(g) (1 - s(g)) as s(g) s(-g): 1 - s would cancel for large g, down to 0 where
+// s rounds to 1.
+__device__ __forceinline__ float gate_slope(float g) { return sigmoidf_(g) * sigmoidf_(-g); }
 
 // Threads of a block whose rows take TPR threads each: four rows of a wave, or one row.
 template <int TPR>

@@ -209,9 +209,11 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
       o.store(bdh, lane + i * TPR);
     }
     if (!q.dy && !YPATH) continue;
-    float gt = 1.f;
-    if (GATE == MOE_GATE_TOKEN)
-      gt = gate_value(to_f32<Elem>(static_cast<const Elem*>(p.gate)[row]), p.gate_sigmoid);
+    float raw = 0.f, gt = 1.f;
+    if (GATE == MOE_GATE_TOKEN) {
+      raw = to_f32<Elem>(static_cast<const Elem*>(p.gate)[row]);
+      gt = gate_value(raw, p.gate_sigmoid);
+    }
     // u: yhat (y itself without a post norm); e, the gradient at v, takes D's place
     float u[CH][8], s1 = 0.f, s2 = 0.f, sg = 0.f;
     const float off = -st.x * st.y;
@@ -262,9 +264,8 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
           rg[i].get(g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            g[j] = gate_value(g[j], p.gate_sigmoid);
-            f[j] *= g[j];
-            if (p.gate_sigmoid) v[j] *= g[j] * (1.f - g[j]);
+            f[j] *= gate_value(g[j], p.gate_sigmoid);
+            if (p.gate_sigmoid) v[j] *= gate_slope(g[j]);
           }
           Row8<Elem> o;
           o.set(v);
@@ -286,7 +287,7 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
     }
     if (GATE == MOE_GATE_TOKEN) {
       sg = sum(sg, 0.f).x;
-      if (p.gate_sigmoid) sg *= gt * (1.f - gt);
+      if (p.gate_sigmoid) sg *= gate_slope(raw);
       if (lane == 0 && q.dgate) static_cast<Elem*>(q.dgate)[row] = from_f32<Elem>(sg);
     }
     if (post) {
@@ -350,8 +351,7 @@ __global__ __launch_bounds__(1024) void residual_colsum_kernel(ResidualBwdArgs q
   if (!block_colsum(q.part + slot * H, q.groups, q.nslots * H, blockIdx.x * 32, q.f.H, red, col, s))
     return;
   if (slot == q.slot[CS_GATE] && q.f.gate_sigmoid) {
-    const float g = gate_value(to_f32<Elem>(static_cast<const Elem*>(q.f.gate)[col]), 1);
-    s *= g * (1.f - g);
+    s *= gate_slope(to_f32<Elem>(static_cast<const Elem*>(q.f.gate)[col]));
   }
   void* out = nullptr;
 #pragma unroll

@@ -404,3 +404,33 @@ def test_captured_calls_draw_new_masks_from_a_changed_rng():
             assert torch.equal(a, b)
         masks.append(got[4])
     assert torch.equal(masks[0], masks[2]) and not torch.equal(masks[0], masks[1])
+
+
+@pytest.mark.parametrize("kind", ["channel", "token", "full"])
+def test_sigmoid_gate_gradient_far_from_zero(kind):
+    """float32, each element by itself: the slope keeps its accuracy where the gate is nearly open.
+    A sigmoid of z is off by 2 |z| e for its exponential's argument and 5 e for the exponential, the
+    sum and the reciprocal; the slope is two of them, and six products, a few positive terms' sums
+    (256 e over a row, 4 e over three tokens) come on top: (4 |gate| + 16) e, and those."""
+    mel = _mel()
+    say(f"[gate slope] {kind}")
+    T, H = (7, 56) if kind == "token" else (3, 56)
+    far = np.array([-20.0, -8.0, -1.0, 0.0, 1.0, 8.0, 20.0], np.float32)
+    gate = {"channel": np.tile(far, 8), "token": far, "full": np.tile(far, (T, 8))}[kind]
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    y, dh = (0.5 + torch.rand(T, H, device="cuda", generator=g) for _ in range(2))
+    d = mel.Residual(T, H, "f32", pre="none", gate=kind, gate_sigmoid=True, alpha=0.5)
+    ws = torch.empty(max(1, mel.moe_residual_norm_workspace_bytes(d)), device="cuda",
+                     dtype=torch.uint8)
+    raw = torch.from_numpy(gate).cuda()
+    out = torch.full_like(raw, float("nan"))
+    mel.moe_residual_norm_bwd(d, dh, None, None, y, {"gate": raw}, None, None, None,
+                              {"dgate": out}, ws)
+    z = gate.astype(np.float64)
+    slope = 1.0 / ((1.0 + np.exp(-z)) * (1.0 + np.exp(z)))
+    term = 0.5 * _np(y) * _np(dh)
+    term = {"channel": term.sum(0), "token": term.sum(1), "full": term}[kind]
+    bound = (4 * np.abs(z) + 16 + {"channel": 4, "token": 256, "full": 0}[kind]) * E
+    rel = np.abs(_np(out) - term * slope) / (term * slope)
+    assert (rel <= bound).all(), (rel / E).max()
