@@ -480,9 +480,9 @@ moe_status moe_residual_norm_bwd(const moe_residual *desc, const void *dh_out, c
  *   z = x w^T + bias            x [T, K], w [N, K], bias [N]
  *   y = residual + dropout(act(z))      y, residual, z [T, N]
  * Products, bias, activation and sums are float32; z and y are rounded once.
- * Dropout's element index is t * N + n. gelu is z Phi(z), Phi within 1.5e-7
- * (absolute, for every dtype); gelu_tanh its tanh form with sqrt(2/pi) and
- * 0.044715. */
+ * Dropout's element index is t * N + n. gelu is z Phi(z): float32 with Phi to a
+ * few units of float32 rounding, the 16-bit types with Phi within 1.5e-7
+ * (absolute); gelu_tanh its tanh form with sqrt(2/pi) and 0.044715. */
 typedef enum {
   MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_SILU = 2, MOE_ACT_GELU = 3, MOE_ACT_GELU_TANH = 4
 } moe_act;

@@ -2,6 +2,8 @@
 // consecutive columns of a row, shared by its GEMMs, its few-token kernel and its split-K sum.
 #pragma once
 
+#include <type_traits>
+
 #include "dropout.h"
 #include "row8.h"
 
@@ -12,11 +14,23 @@ namespace moe {
 constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-// Phi(z), and e = exp(-z^2 / 2), by Abramowitz and Stegun 7.1.26 (erfc as a polynomial in
-// t = 1 / (1 + p x) times exp(-x^2), within 1.5e-7): a dozen instructions that the slope's
-// exponential is part of, where erff and an exponential of its own take about eighty and bound the
-// kernel that forms dz (8192 x 2880, gelu: 43 us, with the polynomial 27.6).
+// Phi(z), and e = exp(-z^2 / 2).
+//
+// float: erfc(-z / sqrt 2) / 2, which keeps its relative accuracy where Phi is small, by the math
+// library; the float32 products take far longer than its about eighty instructions.
+//
+// 16-bit types: Abramowitz and Stegun 7.1.26 (erfc as a polynomial in t = 1 / (1 + p x) times
+// exp(-x^2), within 1.5e-7), a dozen instructions that the slope's exponential is part of: the
+// library's erf and exponential bound the kernel that forms dz (8192 x 2880, gelu: 43 us, with the
+// polynomial 27.6). Relative to Phi it is off by 8e-7 at most above -1, 5.3e-5 above -3, 4.7e-4
+// above -4 and 3.6e-3 above -6, so the output's rounding is the larger error (bf16: 3.9e-3; fp16:
+// 4.9e-4, and coarser below 6e-5, which |z Phi(z)| reaches at -4.2) until |z Phi(z)| is below 6e-9.
+template <typename Elem>
 __device__ __forceinline__ float gelu_phi(float z, float& e) {
+  if constexpr (std::is_same_v<Elem, float>) {
+    e = expf(-0.5f * z * z);
+    return 0.5f * erfcf(z * -0.7071067811865476f);
+  }
   const float x = fabsf(z) * 0.7071067811865476f;
   e = __expf(-x * x);
   const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.f));
@@ -28,19 +42,21 @@ __device__ __forceinline__ float gelu_phi(float z, float& e) {
   return z < 0.f ? half_erfc : 1.f - half_erfc;
 }
 
+template <typename Elem>
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z < 0.f ? 0.f : z;
     case MOE_ACT_SILU: return z * sigmoidf_(z);
     case MOE_ACT_GELU: {
       float e;
-      return z * gelu_phi(z, e);
+      return z * gelu_phi<Elem>(z, e);
     }
     case MOE_ACT_GELU_TANH: return z * sigmoidf_(2.f * kGeluC * (z + kGeluA * z * z * z));
     default: return z;
   }
 }
 
+template <typename Elem>
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
@@ -50,7 +66,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     }
     case MOE_ACT_GELU: {  // Phi(z) + z phi(z)
       float e;
-      const float phi = gelu_phi(z, e);
+      const float phi = gelu_phi<Elem>(z, e);
       return fmaf(z * 0.3989422804014327f, e, phi);
     }
     case MOE_ACT_GELU_TANH: {
@@ -79,7 +95,7 @@ __device__ __forceinline__ void linear_finish8(const LinearEpi& q, const DropKey
   }
   if (q.act != MOE_ACT_NONE) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = act_value(v[j], q.act);
+    for (int j = 0; j < 8; ++j) v[j] = act_value<Elem>(v[j], q.act);
   }
   if (q.drop.thr) {
     const uint4 rnd = philox(key, static_cast<uint64_t>(at) / 8);

@@ -349,7 +349,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const Elem* __restrict__
         float z[8];
         rz[u].get(z);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= act_slope(z[j], epi.act);
+        for (int j = 0; j < 8; ++j) v[j] *= act_slope<Elem>(z[j], epi.act);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[j];

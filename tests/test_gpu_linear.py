@@ -205,3 +205,34 @@ def test_linear_nonfinite_inputs_stay_in_their_rows():
         rows = [r for r in range(T) if r not in (2, 4)]
         assert torch.equal(y0[rows], y1[rows])
         assert torch.isnan(y1[2]).all() and not torch.isfinite(y1[4]).all()
+
+
+def test_float32_gelu_keeps_its_accuracy_in_the_tail():
+    """z = x w^T of one term is exact, so y is gelu(z) alone and dx its slope. Phi by erfc: its
+    argument is off by 2 e of it (a product and a constant), which erfc's logarithm takes times at most
+    2 x^2 + 1 = z^2 + 1 for negative z: (2 z^2 + 2) e, and 12 e for erfc itself and two products. The
+    density's exponential: z^2 / 2 with three roundings, (1.5 z^2) e, and 10 e for it and its products."""
+    from scipy.special import erfc
+    mel = _mel()
+    say("[gelu f32]")
+    z = np.linspace(-9, 9, 4099).astype(np.float32)
+    T, n = z.size, 8
+    x = torch.zeros(T, n, device="cuda")
+    x[:, 0] = torch.from_numpy(z)
+    w = torch.zeros(n, n, device="cuda")
+    w[0, 0] = 1.0
+    z = z.astype(np.float64)
+    phi, pdf = 0.5 * erfc(-z * np.sqrt(0.5)), np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+    eval_, edf = (2 * z * z + 14) * E * phi, (1.5 * z * z + 10) * E * np.abs(z) * pdf
+    for rows in (slice(None), slice(1600, 1601), slice(1600, 1613)):
+        t = x[rows].contiguous()
+        sh = mel.LinearShape(t.shape[0], n, n, "f32", act="gelu")
+        f, b = (_ws(m) for m in mel.moe_linear_workspace_bytes(sh))
+        y = _nan(t.shape[0], n, dtype="f32")
+        mel.moe_linear_fwd(sh, t, w, y, f)
+        d = np.abs(_np(y)[:, 0] - (z * phi)[rows])
+        assert (d <= (np.abs(z) * eval_)[rows] + 1e-38).all(), d.max()
+        dx, pre = _nan(t.shape[0], n, dtype="f32"), t.clone()
+        mel.moe_linear_bwd(sh, torch.ones_like(t), t, w, pre, dx, None, None, b)
+        d = np.abs(_np(dx)[:, 0] - (phi + z * pdf)[rows])
+        assert (d <= (eval_ + edf + E * np.abs(phi + z * pdf))[rows]).all(), d.max()
