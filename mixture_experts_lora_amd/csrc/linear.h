@@ -56,22 +56,25 @@ __device__ __forceinline__ float act_value(float z, int act) {
   }
 }
 
+// Slopes. Their terms that grow with z take it clamped to where its other factor is 0 or 1 already, so
+// that the limits 0 and 1 come out however large z is (z^2 overflows from 2e19 on).
 template <typename Elem>
 __device__ __forceinline__ float act_slope(float z, int act) {
+  const float c = fminf(fmaxf(z, -128.f), 128.f);
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case MOE_ACT_SILU: {
       const float s = sigmoidf_(z);
-      return s * (1.f + z * (1.f - s));
+      return s * (1.f + c * (1.f - s));
     }
     case MOE_ACT_GELU: {  // Phi(z) + z phi(z)
       float e;
       const float phi = gelu_phi<Elem>(z, e);
-      return fmaf(z * 0.3989422804014327f, e, phi);
+      return fmaf(c * 0.3989422804014327f, e, phi);
     }
     case MOE_ACT_GELU_TANH: {
       const float s = sigmoidf_(2.f * kGeluC * (z + kGeluA * z * z * z));
-      return s + 2.f * kGeluC * z * s * (1.f - s) * (1.f + 3.f * kGeluA * z * z);
+      return s + 2.f * kGeluC * c * s * (1.f - s) * (1.f + 3.f * kGeluA * c * c);
     }
     default: return 1.f;
   }

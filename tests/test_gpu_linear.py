@@ -236,3 +236,23 @@ def test_float32_gelu_keeps_its_accuracy_in_the_tail():
         mel.moe_linear_bwd(sh, torch.ones_like(t), t, w, pre, dx, None, None, b)
         d = np.abs(_np(dx)[:, 0] - (phi + z * pdf)[rows])
         assert (d <= (eval_ + edf + E * np.abs(phi + z * pdf))[rows]).all(), d.max()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_slopes_of_huge_products_are_their_limits(act, dtype):
+    """Where z^2 or z^3 overflows, and at infinity: 1 for positive z, 0 for negative, no NaN from a
+    product of infinity and zero. A NaN stays one."""
+    mel = _mel()
+    say(f"[slope limits] {act} {dtype}")
+    big = [200.0, 6e4] if dtype == "f16" else [200.0, 6e4, 1e13, 1e20, 3e38]
+    z = torch.tensor([v * s for v in big + [float("inf")] for s in (1, -1)] + [float("nan")])
+    T, n = z.numel(), 8
+    pre = z[:, None].expand(T, n).to(DT[dtype]).cuda().contiguous()
+    w = torch.eye(n, device="cuda", dtype=DT[dtype])
+    dy, dx = torch.full_like(pre, 3.0), torch.empty_like(pre)
+    sh = mel.LinearShape(T, n, n, dtype, act=act)
+    mel.moe_linear_bwd(sh, dy, None, w, pre, dx, None, None, _ws(mel.moe_linear_workspace_bytes(sh)[1]))
+    want = torch.tensor([3.0, 0.0] * (len(big) + 1))[:, None].expand(T - 1, n)
+    assert torch.equal(dx[:-1].float().cpu(), want)
+    assert act == "relu" or dx[-1].isnan().all()
