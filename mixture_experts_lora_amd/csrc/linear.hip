@@ -412,14 +412,15 @@ Product plan(int dtype, bool reduce_rows, int64_t M, int64_t N, int64_t K) {
   const bool f32 = dtype == MOE_F32;
   const TileModel* models = f32 ? kF32 : reduce_rows ? kReduceRows16 : kRows16;
   const int count = f32 ? 1 : reduce_rows ? 2 : 5, least = f32 ? 128 : 256;
-  // a slice of a row reduction lies within a 32-bit buffer offset
-  const int64_t e0 = reduce_rows ? (K * std::max(M, N) * 2 >> 30) + 1 : 1;
-  const int64_t e1 = std::max<int64_t>(e0, std::min<int64_t>(32, K / least));
   Product best{};
   double best_us = 0.0;
   for (int i = 0; i < count; ++i) {
     const TileModel& m = models[i];
     const int64_t tiles = static_cast<int64_t>(ceil_div(M, m.bm)) * ceil_div(N, m.bn);
+    // The register-staged tiles address a slice of a row reduction by 32-bit buffer offsets; the DMA
+    // tiles move their buffer's 64-bit base with each k tile, and the float32 ones use pointers.
+    const int64_t e0 = m.tile == TILE_192x192 ? (K * std::max(M, N) * 2 >> 30) + 1 : 1;
+    const int64_t e1 = std::max<int64_t>(e0, std::min<int64_t>(32, K / least));
     for (int64_t e = e0; e <= e1; ++e) {
       const int64_t chunk = (((K + e - 1) / e) + 63) / 64 * 64, E = ceil_div(K, chunk);
       const double busiest = std::max<double>(m.few, static_cast<double>((tiles * E + 255) / 256));

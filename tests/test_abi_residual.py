@@ -286,3 +286,13 @@ def test_only_the_named_input_may_be_the_output(lib):
                                            None, 0, at(0), at(6), B(MoeResidualGrads()), at(8),
                                            1 << 20, None), "dh overlaps " + what)
     overlaps(lib.moe_dropout(1, 64, 0.1, at(0), 0, at(0), at(0), None), "dst overlaps rng")
+
+
+@pytest.mark.parametrize("dtype,T,K,N", [(0, 262144, 16384, 16384), (1, 1 << 20, 8192, 8192)])
+def test_linear_backward_forms_no_needless_partials(lib, dtype, T, K, N):
+    """Enough tiles for every CU: the weight gradient takes its rows in a few slices at most, however
+    many bytes they have, and the workspace is a fraction of the activations (16 GiB)."""
+    b = ctypes.c_size_t()
+    assert lib.moe_linear_workspace_bytes(ctypes.byref(lin(T=T, K=K, N=N, dtype=dtype)), None,
+                                          ctypes.byref(b)) == 0
+    assert b.value <= 2 * N * K * 4

@@ -256,3 +256,30 @@ def test_slopes_of_huge_products_are_their_limits(act, dtype):
     want = torch.tensor([3.0, 0.0] * (len(big) + 1))[:, None].expand(T - 1, n)
     assert torch.equal(dx[:-1].float().cpu(), want)
     assert act == "relu" or dx[-1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 530000), ("f32", 270000)])
+def test_linear_operands_past_two_gigabytes(dtype, T):
+    """x, y, dy and dx of 2.2e9 bytes each: rows at both ends and around byte 2^31, and a weight
+    gradient whose rows have to be sliced where a tile addresses them by 32-bit offsets (bf16)."""
+    mel = _mel()
+    K = N = 2056
+    say(f"[linear far] {dtype} T={T}")
+    x, w, b, _, dy = _inputs(T, K, N, dtype)
+    sh = mel.LinearShape(T, K, N, dtype)
+    f, bw = (_ws(n) for n in mel.moe_linear_workspace_bytes(sh))
+    y, dx, dw, db = _nan(T, N, dtype=dtype), _nan(T, K, dtype=dtype), torch.empty_like(w), torch.empty_like(b)
+    mel.moe_linear_fwd(sh, x, w, y, f, bias=b)
+    mel.moe_linear_bwd(sh, dy, x, w, None, dx, dw, db, bw)
+    assert y.isfinite().all() and dx.isfinite().all()
+    mid = (1 << 31) // (K * x.element_size())
+    rows = torch.tensor([0, 1, 255, 256, mid - 1, mid, mid + 1, T // 2, T - 2, T - 1], device="cuda")
+    for got, a, m, add in ((y, x, w.t(), b), (dx, dy, w, None)):
+        a, m = _np(a[rows]), _np(m)
+        ref = a @ m + (0 if add is None else _np(add))
+        mag = np.abs(a) @ np.abs(m) + (0 if add is None else np.abs(_np(add)))
+        within("rows", got[rows], ref, dtype, 4 * np.sqrt(K) * E * mag)
+    cols = [0, 100, 1023, N - 1]
+    d, xx = dy[:, cols].double().t().contiguous(), x.double()
+    within("dw", dw[cols], _np(d @ xx), dtype, 4 * np.sqrt(T) * E * _np(d.abs() @ xx.abs_()))
+    within("db", db[cols], _np(d.sum(1)), dtype, (4 * np.sqrt(T) + 32) * E * _np(d.abs().sum(1)))
