@@ -432,6 +432,13 @@ def moe_merge_lora(shape: Shape, weights: dict, w_gu_merged=None, w_d_merged=Non
         _stream(stream)), "moe_merge_lora")
 
 
+def _sizes(desc, *names):
+    """Refuses sizes that the descriptor's 32-bit fields would wrap into other valid ones."""
+    for n in names:
+        if not 0 < getattr(desc, n) < 1 << 31:
+            raise ValueError(f"{n} must be in [1, 2^31), got {getattr(desc, n)}")
+
+
 @dataclass(frozen=True)
 class Residual:
     """The residual stream around a block: h' = h + alpha * g * dropout(post(y)), x' = pre(h').
@@ -454,6 +461,7 @@ class Residual:
         return _TORCH_DTYPES[self.dtype]
 
     def c(self) -> MoeResidual:
+        _sizes(self, "T", "H")
         return MoeResidual(self.T, self.H, _ABI_DTYPES[self.dtype], NORM_IDS[self.post],
                            NORM_IDS[self.pre], GATE_IDS[self.gate], int(self.gate_sigmoid),
                            float(self.alpha), float(self.eps), float(self.weight_shift),
@@ -614,6 +622,7 @@ class LinearShape:
         return _TORCH_DTYPES[self.dtype]
 
     def c(self) -> MoeLinearShape:
+        _sizes(self, "T", "K", "N")
         return MoeLinearShape(self.T, self.K, self.N, _ABI_DTYPES[self.dtype], ACT_IDS[self.act],
                               float(self.dropout))
 

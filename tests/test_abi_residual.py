@@ -296,3 +296,16 @@ def test_linear_backward_forms_no_needless_partials(lib, dtype, T, K, N):
     assert lib.moe_linear_workspace_bytes(ctypes.byref(lin(T=T, K=K, N=N, dtype=dtype)), None,
                                           ctypes.byref(b)) == 0
     assert b.value <= 2 * N * K * 4
+
+
+def test_sizes_past_32_bits_are_refused():
+    """ctypes would wrap 2^32 + 8 rows to 8, and the call would leave all others as they were."""
+    import mixture_experts_lora_amd as mel
+    for d in (mel.Residual((1 << 32) + 8, 8), mel.Residual(8, (1 << 32) + 8),
+              mel.LinearShape((1 << 32) + 8, 8, 8), mel.LinearShape(8, (1 << 32) + 8, 8),
+              mel.LinearShape(8, 8, (1 << 32) + 8), mel.Residual(1 << 31, 8), mel.Residual(0, 8)):
+        with pytest.raises(ValueError, match="must be in"):
+            d.c()
+        with pytest.raises(ValueError, match="must be in"):
+            (mel.moe_linear_workspace_bytes if isinstance(d, mel.LinearShape)
+             else mel.moe_residual_norm_workspace_bytes)(d)
