@@ -481,14 +481,15 @@ class MoELoRASublayer:
     def backward(self, dh2, params: dict, w_r, weights: dict, shared_weights: dict | None = None,
                  attn=None, rng=None, site: int = 0, stream=None):
         """From the gradient at h2: returns (dh, dattn or None, routed LoRA grads, shared LoRA
-        grads or None); the gradients of `params` are in self.grads. rng must hold the forward's
-        values."""
+        grads or None); the gradients of `params` are in self.grads, that of the router's logits
+        in self.d_logits, and with full_ft those of the base weights in self.block.routed.base_grads
+        and self.block.shared.base_grads. rng must hold the forward's values."""
         g = self.grads
         moe_residual_norm_bwd(self.after, dh2, None, None, self.y, self._sub(params, self.after),
                               self.stats_after, None, self.dy, self._sub(g, self.after, "d"),
                               self.ws, rng=rng, site=site + 1, stream=stream)
-        dx, _, lora, shared = self.block.backward(self.dy, self.x, w_r, weights, shared_weights,
-                                                  stream)
+        dx, self.d_logits, lora, shared = self.block.backward(self.dy, self.x, w_r, weights,
+                                                              shared_weights, stream)
         moe_residual_norm_bwd(self.before, dh2, dx, self.stream_in, None,
                               self._sub(params, self.before), self.stats_before, self.dh, None,
                               self._sub(g, self.before, "d"), self.ws, stream=stream)

@@ -141,3 +141,29 @@ def test_sublayer_trains_only_what_it_is_told():
     torch.cuda.synchronize()
     assert set(part.grads) == {"dw_pre"} and torch.equal(part.grads["dw_pre"], full.grads["dw_pre"])
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("name,shared_I,opts", [
+    ("mini-bf16", 136, dict(full_ft=True)), ("mini-f32", 72, dict(recompute=True)),
+    ("mini-f16", 104, dict(full_ft=True, recompute=True)), ("mini-renorm", None, dict(full_ft=True)),
+])
+def test_sublayer_passes_the_blocks_options_and_gradients_on(name, shared_I, opts):
+    """The block's own run (tested against the oracle elsewhere) on the input and output gradient
+    that the sublayer handed its block: the router logits', LoRA and base gradients bit for bit."""
+    import mixture_experts_lora_amd as mel
+    cfg, inp, sub, args = _build(name, shared_I, 264, dict(dropout=0.1, post="rms", **opts))
+    say(f"[sublayer options] {name} {opts}")
+    _, _, lora, shared = sub.step(2 * inp["x"], inp["dy"], **args)
+    blk = mel.MoELoRABlock(mel.Shape.of(cfg), cfg.router, shared_I, **opts)
+    _, dl, lora2, shared2 = blk.step(sub.x, args["w_r"], sub.dy, args["weights"],
+                                     args["shared_weights"])
+    torch.cuda.synchronize()
+    assert torch.equal(sub.d_logits, dl) and sub.d_logits.abs().max() > 0
+    pairs = [(lora, lora2), (shared or {}, shared2 or {})]
+    if opts.get("full_ft"):
+        pairs.append((sub.block.routed.base_grads, blk.routed.base_grads))
+        if shared_I:
+            pairs.append((sub.block.shared.base_grads, blk.shared.base_grads))
+    for a, b in pairs:
+        assert a.keys() == b.keys()
+        assert all(torch.equal(a[n], b[n]) and a[n].isfinite().all() for n in a)
