@@ -167,3 +167,21 @@ def test_sublayer_passes_the_blocks_options_and_gradients_on(name, shared_I, opt
     for a, b in pairs:
         assert a.keys() == b.keys()
         assert all(torch.equal(a[n], b[n]) and a[n].isfinite().all() for n in a)
+
+
+def test_sublayer_run_on_its_own_output_has_no_backward():
+    """Forward in place is the same numbers, but the norm's input is gone; with a projection the
+    backward reads h1 instead and runs."""
+    say("[sublayer in place]")
+    for width in (None, 264):
+        cfg, inp, sub, args = _build("mini-bf16", None, width, {})
+        h = 2 * inp["x"]
+        want = sub.forward(h, **args).clone()
+        dh = sub.backward(inp["dy"], **args)[0].clone()
+        sub.h2.copy_(h)
+        assert torch.equal(sub.forward(sub.h2, **args), want)
+        if width is None:
+            with pytest.raises(ValueError, match="own output"):
+                sub.backward(inp["dy"], **args)
+        else:
+            assert torch.equal(sub.backward(inp["dy"], **args)[0], dh)
