@@ -496,8 +496,10 @@ typedef struct {
 /*   bias, residual  NULL: none; y may be residual
  *   pre    z out, kept for the backward; NULL: not wanted
  * moe_linear_bwd, from dy [T, N] (the residual's gradient is dy itself):
- *   dz = act'(pre) * dropout(dy), rounded to `dtype` (it feeds the MFMA)
- *   dx [T, K] = dz w    dw [N, K] = dz^T x    dbias [N] = sum_t dz (unrounded dz)
+ *   dz = act'(pre) * (kept(dy) ? dy : 0), rounded to `dtype` (it feeds the MFMA; exact
+ *        when act is none)
+ *   dx [T, K] = c dz w    dw [N, K] = c dz^T x    dbias [N] = c sum_t dz (unrounded dz),
+ *        c the scale of dropout's kept elements, applied to the float32 results
  *   pre    as kept by the forward; read (and required) when act is not none
  *   dx, dw, dbias   NULL: not wanted; x is read for dw, w for dx (else may be NULL)
  * ws: moe_linear_workspace_bytes (either may be 0: ws may then be NULL). Results

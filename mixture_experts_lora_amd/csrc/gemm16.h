@@ -1419,6 +1419,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void gemm16(GemmA
           linear_finish8<DElem>(p.lin, dkey, row, col, p.N, dbias[pass % DREP],
                                 dres[mi & 1][pass], v);
         } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= p.scale;
           store8<F16>(static_cast<bf16_t*>(p.out) + row * p.N + col, v);
         }
       }

@@ -158,6 +158,7 @@ struct LinearEpi {
   const void *bias, *residual;
   void *pre, *y;
   int32_t act;
+  float scale = 1.0f;  // of the product, before the bias
   DropArgs drop;
 };
 
@@ -202,7 +203,7 @@ size_t linear_fwd_ws_bytes(const LinearDims& d);
 size_t linear_bwd_ws_bytes(const LinearDims& d, bool form_dz);
 hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* w,
                              const LinearEpi& epi, void* ws, hipStream_t s, KernelTimer* tm);
-// epi: act and drop of the forward; pre its kept product. dx, dw, db: null when not wanted.
+// epi: act and drop of the forward, pre its kept product; nothing else of it is read. dx, dw, db: null when not wanted.
 hipError_t launch_linear_bwd(const LinearDims& d, const void* dy, const void* x, const void* w,
                              const LinearEpi& epi, void* dx, void* dw, void* db, void* ws,
                              hipStream_t s, KernelTimer* tm);

@@ -91,7 +91,7 @@ __device__ __forceinline__ void linear_finish8(const LinearEpi& q, const DropKey
   float f[8];
   bias.get(f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] += f[j];
+  for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], q.scale, f[j]);
   if (q.pre) {
     r.set(v);
     r.store(static_cast<Elem*>(q.pre) + at);

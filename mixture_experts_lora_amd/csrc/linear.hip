@@ -2,8 +2,11 @@
 //
 //   z = x w^T + bias        x [T, K], w [N, K]
 //   y = residual + dropout(act(z))
-//   dz = act'(z) dropout(dy)   (rounded to the layer dtype, as the experts' dH is: it feeds MFMA)
-//   dx = dz w    dw = dz^T x    dbias = sum_t dz (summed before the rounding)
+//   dz = act'(z) kept(dy)      kept(dy): dy where the mask keeps it, else 0
+//   dx = c dz w    dw = c dz^T x    dbias = c sum_t dz      c: the kept elements' scale
+//
+// dz is rounded to the layer dtype (it feeds MFMA, as the experts' dH does), dbias summed before
+// that. c goes to the float32 results, so that without an activation dz is exact.
 //
 // Many tokens: MFMA tiles (gemm16 for the 16-bit types, linear_f32_kernel for float32) whose
 // epilogue applies bias, activation, dropout and residual to the float32 product, so z and y move
@@ -153,6 +156,8 @@ __global__ __launch_bounds__(256, 2) void linear_f32_kernel(GemmArgs p) {
       if (EPI && p.E == 1) {
         linear_finish8<float>(p.lin, row, col, p.N, v);
       } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= p.scale;
         Row8<float> o;
         o.set(v);
         o.store(static_cast<float*>(p.out) + (static_cast<int64_t>(e) * p.M + row) * p.N + col);
@@ -343,7 +348,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const Elem* __restrict__
       if (epi.drop.thr) {
         const uint4 rnd = philox(key, static_cast<uint64_t>(t * (N / 8) + chunk));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = drop(epi.drop, rnd, j, v[j]);
+        for (int j = 0; j < 8; ++j) v[j] = kept(epi.drop, rnd, j) ? v[j] : 0.f;
       }
       if (act) {
         float z[8];
@@ -365,7 +370,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const Elem* __restrict__
     const int n = blockIdx.x * 512 + c;
     if (n < N)
       part[static_cast<int64_t>(blockIdx.y) * N + n] =
-          (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
+          epi.drop.scale * ((red[0][c] + red[1][c]) + (red[2][c] + red[3][c]));
   }
 }
 
@@ -500,9 +505,11 @@ hipError_t product(const Product& q, GemmArgs& a, const LinearEpi& epi, void* pa
   });
 }
 
-// dw [N, K] = dz^T x: the reduction runs over the rows of both.
-hipError_t product_rows(const Product& q, GemmArgs& a, void* out, void* part, hipStream_t s) {
+// dw [N, K] = scale dz^T x: the reduction runs over the rows of both.
+hipError_t product_rows(const Product& q, GemmArgs& a, float scale, void* out, void* part,
+                        hipStream_t s) {
   a.out = q.E > 1 ? part : out;
+  a.scale = q.E > 1 ? 1.0f : scale;
   const int grid = q.E * q.ntm * q.ntn;
   if (a.dtype == MOE_F32)
     MOE_TRY(launch(linear_f32_kernel<false, false, false>, grid, a, s));
@@ -515,6 +522,7 @@ hipError_t product_rows(const Product& q, GemmArgs& a, void* out, void* part, hi
   if (q.E == 1) return hipSuccess;
   LinearEpi epi{};
   epi.y = out;
+  epi.scale = scale;
   return by_type(a.dtype, [&](auto tag) {
     const int64_t MN = static_cast<int64_t>(a.M) * a.N;
     hipLaunchKernelGGL(linear_sum_kernel<decltype(tag)>,
@@ -611,13 +619,14 @@ hipError_t launch_linear_bwd(const LinearDims& d, const void* dy, const void* x,
     a.b[0] = opnd(w, 0, d.K, 0, true);
     LinearEpi out{};
     out.y = dx;
+    out.scale = epi.drop.scale;
     MOE_TRY(product<false>(b.dx, a, out, part, s));
   }
   if (dw) {
     GemmArgs a = dense_args(b.dw, d.dtype, d.N, d.K, d.T);
     a.a[0] = opnd(dz, 0, d.N, 0, true);
     a.b[0] = opnd(x, 0, d.K, 0, true);
-    MOE_TRY(product_rows(b.dw, a, dw, part, s));
+    MOE_TRY(product_rows(b.dw, a, epi.drop.scale, dw, part, s));
   }
   return hipSuccess;
 }

@@ -283,3 +283,24 @@ def test_linear_operands_past_two_gigabytes(dtype, T):
     d, xx = dy[:, cols].double().t().contiguous(), x.double()
     within("dw", dw[cols], _np(d @ xx), dtype, 4 * np.sqrt(T) * E * _np(d.abs() @ xx.abs_()))
     within("db", db[cols], _np(d.sum(1)), dtype, (4 * np.sqrt(T) + 32) * E * _np(d.abs().sum(1)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("T,K,N", [(7, 1032, 264), (300, 584, 1032), (3000, 136, 136),
+                                   (4111, 1160, 520), (4352, 4104, 72), (4000, 264, 3400)])
+def test_dropout_alone_adds_no_rounding_to_the_backward(dtype, T, K, N):
+    """Without an activation dz is dy or 0, and the kept elements' scale multiplies float32 sums:
+    the results are off by their own sums' rounding and one of the output."""
+    mel = _mel()
+    say(f"[linear bwd dropout] {dtype} T={T} K={K} N={N}")
+    x, w, b, _, dy = _inputs(T, K, N, dtype)
+    sh = mel.LinearShape(T, K, N, dtype, dropout=0.3)
+    dx, dw, db = _nan(T, K, dtype=dtype), _nan(N, K, dtype=dtype), _nan(N, dtype=dtype)
+    mel.moe_linear_bwd(sh, dy, x, w, None, dx, dw, db, _ws(mel.moe_linear_workspace_bytes(sh)[1]),
+                       rng=_rng(), site=4)
+    xs, ws = _np(x), _np(w)
+    dz, rx, rw, rb = R.linear_bwd(_np(dy), xs, ws, None, "none", (0.3, 77, 123, 4))
+    a = np.abs(dz)
+    for name, got, ref, n, mag in (("dx", dx, rx, N, a @ np.abs(ws)), ("dw", dw, rw, T, a.T @ np.abs(xs)),
+                                   ("db", db, rb, T, a.sum(0))):
+        within(name, got, ref, dtype, (4 * np.sqrt(n) * mag + 4 * np.abs(ref)) * E)
