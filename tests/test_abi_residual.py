@@ -309,3 +309,51 @@ def test_sizes_past_32_bits_are_refused():
         with pytest.raises(ValueError, match="must be in"):
             (mel.moe_linear_workspace_bytes if isinstance(d, mel.LinearShape)
              else mel.moe_residual_norm_workspace_bytes)(d)
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """Several GPUs, shown with the binding's calls replaced: a launch happens under the device of
+    its tensors, on that device's current stream or the one it is given, and tensors of two devices
+    are refused."""
+    import contextlib
+    import types
+
+    import torch
+    import mixture_experts_lora_amd as mel
+
+    class On(torch.Tensor):
+        def get_device(self):
+            return self.index_
+
+    def on(i):
+        t = torch.zeros(1).as_subclass(On)
+        t.index_ = i
+        return t
+
+    now, log = [0], []
+
+    @contextlib.contextmanager
+    def device(i):
+        before, now[0] = now[0], i
+        yield
+        now[0] = before
+
+    monkeypatch.setattr(mel, "_one_gpu", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda: types.SimpleNamespace(cuda_stream=100 + now[0]))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+
+    def fn(arg, stream):
+        log.append((arg, now[0], getattr(stream, "value", stream)))
+        return 0
+
+    assert mel._device(None, on(1), None, on(1)) == 1 and mel._device(None) == -1
+    with pytest.raises(ValueError, match="tensors on"):
+        mel._device(on(0), None, on(1))
+    mel._call(fn, "call", 0, None, "a")
+    mel._call(fn, "call", 1, None, "b")
+    mel._call(fn, "call", 1, 55, "c")
+    mel._call(fn, "call", 0, 56, "d")
+    assert log == [("a", 0, 100), ("b", 1, 101), ("c", 1, 55), ("d", 0, 56)] and now == [0]
