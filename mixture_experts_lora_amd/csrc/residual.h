@@ -71,9 +71,14 @@ __device__ __forceinline__ int row_in_block() {
 __device__ __forceinline__ float gate_value(float g, int sigmoid) {
   return sigmoid ? sigmoidf_(g) : g;
 }
-// The sigmoid's slope s(g) (1 - s(g)) as s(g) s(-g): 1 - s would cancel for large g, down to 0 where
-// s rounds to 1.
-__device__ __forceinline__ float gate_slope(float g) { return sigmoidf_(g) * sigmoidf_(-g); }
+// The sigmoid and its slope s(g) (1 - s(g)) = s(g) s(-g) from t = exp(-|g|) alone: 1 / (1 + t) is the
+// larger of s(g) and s(-g), t / (1 + t) the other. (1 - s would cancel for large g, down to 0 where s
+// rounds to 1; two sigmoids cost a gate per element 4% of the backward.)
+__device__ __forceinline__ float gate_slope(float g, float& value) {
+  const float t = __expf(-fabsf(g)), r = __builtin_amdgcn_rcpf(1.f + t);
+  value = g < 0.f ? t * r : r;
+  return t * r * r;
+}
 
 // Threads of a block whose rows take TPR threads each: four rows of a wave, or one row.
 template <int TPR>

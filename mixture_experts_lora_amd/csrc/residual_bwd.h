@@ -209,10 +209,10 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
       o.store(bdh, lane + i * TPR);
     }
     if (!q.dy && !YPATH) continue;
-    float raw = 0.f, gt = 1.f;
+    float gt = 1.f, slope = 1.f;
     if (GATE == MOE_GATE_TOKEN) {
-      raw = to_f32<Elem>(static_cast<const Elem*>(p.gate)[row]);
-      gt = gate_value(raw, p.gate_sigmoid);
+      gt = to_f32<Elem>(static_cast<const Elem*>(p.gate)[row]);
+      if (p.gate_sigmoid) slope = gate_slope(gt, gt);
     }
     // u: yhat (y itself without a post norm); e, the gradient at v, takes D's place
     float u[CH][8], s1 = 0.f, s2 = 0.f, sg = 0.f;
@@ -264,8 +264,8 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
           rg[i].get(g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            f[j] *= gate_value(g[j], p.gate_sigmoid);
-            if (p.gate_sigmoid) v[j] *= gate_slope(g[j]);
+            if (p.gate_sigmoid) v[j] *= gate_slope(g[j], g[j]);
+            f[j] *= g[j];
           }
           Row8<Elem> o;
           o.set(v);
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
     }
     if (GATE == MOE_GATE_TOKEN) {
       sg = sum(sg, 0.f).x;
-      if (p.gate_sigmoid) sg *= gate_slope(raw);
+      sg *= slope;
       if (lane == 0 && q.dgate) static_cast<Elem*>(q.dgate)[row] = from_f32<Elem>(sg);
     }
     if (post) {
@@ -351,7 +351,8 @@ __global__ __launch_bounds__(1024) void residual_colsum_kernel(ResidualBwdArgs q
   if (!block_colsum(q.part + slot * H, q.groups, q.nslots * H, blockIdx.x * 32, q.f.H, red, col, s))
     return;
   if (slot == q.slot[CS_GATE] && q.f.gate_sigmoid) {
-    s *= gate_slope(to_f32<Elem>(static_cast<const Elem*>(q.f.gate)[col]));
+    float g = to_f32<Elem>(static_cast<const Elem*>(q.f.gate)[col]);
+    s *= gate_slope(g, g);
   }
   void* out = nullptr;
 #pragma unroll
