@@ -51,7 +51,9 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
   float a_wpre[CH][8], a_bpre[CH][8], a_wpost[CH][8], a_bpost[CH][8], a_gate[CH][8];
   // The vectors along H, as they are applied (shift + w, the gate's value; 0 past the row, whose
   // lanes then add nothing to a row's sums), or where those would not fit the registers (PACKED)
-  // as they are stored.
+  // as they are stored. (For float32 that saves nothing: there the channel gate's variants at 896 and
+  // 1024 threads spill 20 to 72 bytes a lane, the full gate's at 896 with a layer norm 12. No 16-bit
+  // variant of one chunk spills.)
   constexpr bool PACKED = CH == 1 && TPR >= 896 && YPATH && LAYER;
   constexpr int NV = 4;  // w_pre, w_post, b_post, a channel gate
   float held[PACKED ? 1 : NV][CH][8];
