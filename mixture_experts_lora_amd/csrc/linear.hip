@@ -345,16 +345,17 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(const Elem* __restrict__
       const int64_t t = t0 + 4 * u;
       float v[8];
       r[u].get(v);
-      if (epi.drop.thr) {
-        const uint4 rnd = philox(key, static_cast<uint64_t>(t * (N / 8) + chunk));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = kept(epi.drop, rnd, j) ? v[j] : 0.f;
-      }
       if (act) {
         float z[8];
         rz[u].get(z);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= act_slope<Elem>(z[j], epi.act);
+      }
+      // last, so that a dropped element is 0 whatever z holds, as in the forward
+      if (epi.drop.thr) {
+        const uint4 rnd = philox(key, static_cast<uint64_t>(t * (N / 8) + chunk));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = kept(epi.drop, rnd, j) ? v[j] : 0.f;
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) sum[j] += v[j];

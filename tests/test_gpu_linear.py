@@ -304,3 +304,24 @@ def test_dropout_alone_adds_no_rounding_to_the_backward(dtype, T, K, N):
     for name, got, ref, n, mag in (("dx", dx, rx, N, a @ np.abs(ws)), ("dw", dw, rw, T, a.T @ np.abs(xs)),
                                    ("db", db, rb, T, a.sum(0))):
         within(name, got, ref, dtype, (4 * np.sqrt(n) * mag + 4 * np.abs(ref)) * E)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_dropped_products_pass_no_gradient_whatever_they_hold(act):
+    mel = _mel()
+    say(f"[linear dropped nan] {act}")
+    T, K, N = 65, 72, 136
+    x, w, b, _, dy = _inputs(T, K, N, "bf16")
+    sh = mel.LinearShape(T, K, N, act=act, dropout=0.5)
+    dropped = torch.from_numpy(~R.dropout_keep(T * N, 0.5, 77, 123, 4)).view(T, N).cuda()
+    pre = torch.where(dropped, torch.zeros_like(dy), dy.roll(1, 0))
+    runs = []
+    for fill in (0.0, float("nan"), float("inf"), -float("inf")):
+        z = torch.where(dropped, torch.full_like(pre, fill), pre)
+        g = torch.where(dropped, torch.full_like(dy, fill), dy)
+        out = [_nan(*t.shape, dtype="bf16") for t in (x, w, b)]
+        mel.moe_linear_bwd(sh, g, x, w, z, *out, _ws(mel.moe_linear_workspace_bytes(sh)[1]),
+                           rng=_rng(), site=4)
+        runs.append(out)
+    for out in runs:
+        assert all(torch.equal(a, c) and a.isfinite().all() for a, c in zip(runs[0], out))
