@@ -266,6 +266,8 @@ __global__ __launch_bounds__(row_block<TPR>()) void residual_bwd_kernel(Residual
           rg[i].get(g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
+            // a dropped element is 0 whatever its gate holds, as in the forward
+            if (dropout && !kept(p.drop, rnd[i], j)) g[j] = 0.f;
             if (p.gate_sigmoid) v[j] *= gate_slope(g[j], g[j]);
             f[j] *= g[j];
           }

@@ -434,3 +434,28 @@ def test_sigmoid_gate_gradient_far_from_zero(kind):
     bound = (4 * np.abs(z) + 16 + {"channel": 4, "token": 256, "full": 0}[kind]) * E
     rel = np.abs(_np(out) - term * slope) / (term * slope)
     assert (rel <= bound).all(), (rel / E).max()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dropped_elements_ignore_their_gate(dtype, sigmoid):
+    """A gate per element that is NaN or infinite where the mask drops: the forward adds nothing
+    there, the backward passes nothing, and the rest of the row keeps its bits."""
+    mel = _mel()
+    say(f"[residual dropped gate] {dtype} {sigmoid}")
+    T, H = 33, 584
+    d, prm, h, y, new = _case(mel, T, H, dtype, ("rms", "layer", "full", sigmoid, 1.0, 0.0, 0.5))
+    dropped = torch.from_numpy(~R.dropout_keep(T * H, 0.5, 77, 123, 4)).view(T, H).cuda()
+    dho, dxo, gate = new(T, H), new(T, H), prm["gate"]
+    runs = []
+    for fill in (0.0, float("nan"), float("inf"), -float("inf")):
+        prm["gate"] = torch.where(dropped, torch.full_like(gate, fill), gate)
+        h_out, x_out, st = _fwd(mel, d, h, y, prm)
+        dh, dy = torch.full_like(h, float("nan")), torch.full_like(h, float("nan"))
+        grads = {"d" + n: torch.full_like(t, float("nan")) for n, t in prm.items()}
+        ws = torch.empty(mel.moe_residual_norm_workspace_bytes(d), device="cuda", dtype=torch.uint8)
+        mel.moe_residual_norm_bwd(d, dho, dxo, h_out, y, prm, st, dh, dy, grads, ws, rng=_rng(), site=4)
+        assert (grads["dgate"][dropped] == 0).all() and torch.equal(h_out[dropped], h[dropped])
+        runs.append([h_out, x_out, dh, dy, *grads.values()])
+    for out in runs:
+        assert all(torch.equal(a, c) and a.isfinite().all() for a, c in zip(runs[0], out))
