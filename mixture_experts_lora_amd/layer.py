@@ -484,9 +484,10 @@ class MoELoRASublayer:
         grads or None); the gradients of `params` are in self.grads, that of the router's logits
         in self.d_logits, and with full_ft those of the base weights in self.block.routed.base_grads
         and self.block.shared.base_grads. rng must hold the forward's values."""
-        if self.stream_in.data_ptr() == self.h2.data_ptr():
-            raise ValueError("the forward ran on its own output h2: its input, which the backward "
-                             "reads, is written over")
+        for t in (self.stream_in, attn if self.proj is not None else None):
+            if t is not None and t.data_ptr() == self.h2.data_ptr():
+                raise ValueError("the forward ran on its own output h2: its input, which the "
+                                 "backward reads, is written over")
         g = self.grads
         moe_residual_norm_bwd(self.after, dh2, None, None, self.y, self._sub(params, self.after),
                               self.stats_after, None, self.dy, self._sub(g, self.after, "d"),

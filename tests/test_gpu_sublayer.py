@@ -185,3 +185,12 @@ def test_sublayer_run_on_its_own_output_has_no_backward():
                 sub.backward(inp["dy"], **args)
         else:
             assert torch.equal(sub.backward(inp["dy"], **args)[0], dh)
+
+
+def test_sublayer_projection_of_its_own_output_has_no_backward():
+    say("[sublayer attn in place]")
+    cfg, inp, sub, args = _build("mini-bf16", None, PARITY_CONFIGS["mini-bf16"].H, {})
+    args["attn"] = sub.h2.copy_(inp["x"])
+    sub.forward(2 * inp["x"], **args)
+    with pytest.raises(ValueError, match="own output"):
+        sub.backward(inp["dy"], **args)
