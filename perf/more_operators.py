@@ -95,7 +95,7 @@ def draw(rng):
         case = _quantize("", rows, cols, dtype, rng.choice(["fp4", "fp8"]))
     elif kind == "product":
         K, act = 32 * _log(rng, 2, 224), rng.choice(["none", "swiglu"])
-        out = rng.choice(["bf16", "f16", "f32", "mx8"])
+        out = rng.choice(["bf16", "f16", "mx8"])
         N = 32 * _log(rng, 1, 180) if out == "mx8" else 8 * _log(rng, 2, 720)
         E = rng.choice([0, 0, 4, 8, 32, 100])
         E = min(E, 32 * 5760 * 2880 // (K * N)) if E else 0
@@ -329,7 +329,7 @@ def _plain_route(s):
 
 # ---- microscaled formats: an element is v * 2^e, e one number per 32 elements
 def _scale_cols(cols):
-    return 4 * ((cols + 127) // 128)
+    return 16 * ((cols + 511) // 512)
 
 
 def _mx(x, fmt):
@@ -442,7 +442,7 @@ def work(case):
         a_rows = T if case["gather"] else M
         a = a_rows * (K * (0.5 if case["fmt"] == "fp4" else 1.0) + _scale_cols(K))
         w = n_w * (K * 0.5 + _scale_cols(K)) * max(1, min(E, M))
-        y = M * {"f32": 4 * N, "mx8": N + _scale_cols(N)}.get(case["out"], 2 * N)
+        y = M * (N + _scale_cols(N) if case["out"] == "mx8" else 2 * N)
         return {"bytes": a + w + y + 4 * (E + 1) * (E > 0) + 4 * M * case["gather"],
                 "flops": 2 * M * n_w * K}
     if op == "norm":
