@@ -232,7 +232,8 @@ def _prepare_clip(case, s, normal):
     s["max_norm"] = 0.37e-3 * math.sqrt(sum(g.numel() for g in s["grads"]))
     if own:
         import mixture_experts_lora_amd as mel
-        s["ws"] = torch.empty(max(1, mel.moe_grad_norm_workspace_bytes(s["grads"])), device="cuda",
+        s["list"] = mel.GradList(s["grads"], out=s["out"])
+        s["ws"] = torch.empty(max(1, mel.moe_grad_norm_workspace_bytes(s["list"])), device="cuda",
                               dtype=torch.uint8)
 
 
@@ -276,8 +277,8 @@ def _run_own(s):
                                      s["codes"], s["scales"], s["stats"])
         return {"h_out": s["h_out"], "codes": _e4m3(s["codes"]), "scales": _e8m0(s["scales"]),
                 "stats": s["stats"]}
-    mel.moe_grad_norm(s["grads"], s["norm"], s["ws"])
-    mel.moe_grad_clip(s["grads"], s["norm"], s["max_norm"], out=s["out"])
+    mel.moe_grad_norm(s["list"], s["norm"], s["ws"])
+    mel.moe_grad_clip(s["list"], s["norm"], s["max_norm"])
     return {"norm": s["norm"], "grads": s["out"]}
 
 
