@@ -160,6 +160,40 @@ moe_status moe_route_bwd(const float *logits, const int32_t *topk_ids, const flo
                          int32_t T, int32_t E, int32_t k, int32_t router, float *d_logits,
                          void *stream);
 
+/* Routing with a bias for balance and groups of experts:
+ *   s = softmax(logits) or sigmoid(logits)      v = s + bias
+ *   experts form `groups` equal runs of consecutive indices; a group's score is the sum of its
+ *   group_top (1 or 2) largest v; the topk_groups best groups stay (groups = 1: all experts)
+ *   topk_ids: the k largest v within them, descending; ties, of groups too, to the lower index
+ *   topk_w_j = scale * s_j, or with renorm scale * s_j / (sum of the chosen s)
+ * The bias decides the choice only. v is formed in float64 and compared to 2^-41 of its value; NaN
+ * ranks below -infinity. Experts masked by a logit of -infinity are chosen only where the others
+ * do not suffice and weigh 0, as does every expert of a row of nothing else. */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct {
+  int32_t T, E, k;
+  int32_t score;  /* moe_score */
+  int32_t groups, topk_groups, group_top;
+  int32_t renorm; /* nonzero: the weights of a token sum to scale */
+  float scale;
+} moe_grouped_router;
+
+/*   logits [T, E] float32 in;  bias [E] float32 in, NULL: none;  topk_ids, topk_w [T, k] out
+ * Errors: T, E and k as moe_route, an unknown score, groups that do not divide E, topk_groups
+ * outside [1, groups], kept groups of fewer than k experts, group_top other than 1 or 2, a scale
+ * that is not finite, an output that overlaps another buffer; MOE_ERR_UNSUPPORTED: k > 32,
+ * groups > 64. */
+moe_status moe_route_grouped(const moe_grouped_router *router, const float *logits,
+                             const float *bias, int32_t *topk_ids, float *topk_w, void *stream);
+
+/* Gradient of the weights with respect to the logits, the choice held fixed (so the bias gets
+ * none). topk_ids [T, k] as moe_route_grouped gave them; d_topk_w [T, k] in; d_logits [T, E] out,
+ * zeros where there is no gradient. */
+moe_status moe_route_grouped_bwd(const moe_grouped_router *router, const float *logits,
+                                 const int32_t *topk_ids, const float *d_topk_w, float *d_logits,
+                                 void *stream);
+
 /* Group the N (token, slot) pairs by expert, stably in pair order p = t*k + j
  * (the per-expert token_idx of the faster-moe page's loop), and gather rows.
  *   topk_ids    [T, k] int32 in, each in [0, E)
@@ -519,6 +553,66 @@ moe_status moe_linear_bwd(const moe_linear_shape *shape, const void *dy, const v
                           void *dx, void *dw, void *dbias, void *ws, size_t ws_bytes,
                           void *stream);
 
+/* ---- Gradients of many tensors together.
+ *   norm[0] = sqrt(sum over the tensors of src^2)        squares and sums in float64
+ *   dst = src * min(1, max_norm / (norm[0] + eps)), one rounding
+ * Between the two calls a program whose gradients are spread over GPUs replaces norm[0] by the
+ * norm over all of them. src and dst (may be src; not read by moe_grad_norm) hold n elements of
+ * dtype; n may be 0. A NaN norm makes every gradient NaN; an infinite one, zeros (NaN where the
+ * gradient is not finite). dst = src is left untouched where nothing is clipped. Sums have an
+ * order that depends on the sizes alone, so results repeat bit for bit. The list is read before
+ * the call returns.
+ * Errors: an unknown dtype, n outside [0, 2^40], a tensor not aligned to its type, max_norm < 0
+ * or not finite, eps <= 0 or not finite, a dst that overlaps another dst, another tensor's src or
+ * the norm; norm or ws (16-byte boundary) overlapping a src. */
+typedef struct {
+  const void *src;
+  void *dst;
+  int64_t n;
+  int32_t dtype;
+} moe_grad;
+moe_status moe_grad_norm_workspace_bytes(int32_t count, const moe_grad *grads, size_t *ws);
+moe_status moe_grad_norm(int32_t count, const moe_grad *grads, float *norm, void *ws,
+                         size_t ws_bytes, void *stream);
+moe_status moe_grad_clip(int32_t count, const moe_grad *grads, const float *norm, float max_norm,
+                         float eps, void *stream);
+
+/* ---- Microscaled formats: the merged weights of an export, and the activations they multiply.
+ *
+ * 32 consecutive elements of a row share a scale 2^(s - 127), s one byte (255: NaN), and are held
+ * as E4M3 (one byte) or E2M1 (4 bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two a byte,
+ * the first in the low half):
+ *   s = max(0, floor(log2(largest magnitude)) + 127 - top), top = 8 (E4M3) or 2 (E2M1); 0 for zeros
+ *   an element is the nearest code to x / 2^(s - 127), ties to the even code, at most 448 or 6
+ * An infinity or NaN makes its block NaN (s = 255). This is the conversion of the OCP microscaling
+ * formats (MXFP8, MXFP4), the form in which such checkpoints store their expert weights.
+ *   codes  [rows, cols] bytes (E4M3) or [rows, cols / 2] (E2M1)
+ *   scales [rows, moe_mx_scale_cols(cols)] bytes, cols / 32 of them used, then zeros: a row is a
+ *          whole number of 16-byte pieces (moe_mx_linear reads it whole: the bytes past the
+ *          blocks may hold anything but 255) */
+typedef enum { MOE_MX_FP8 = 0, MOE_MX_FP4 = 1 } moe_mx_format;
+
+/* 16 * ceil(cols / 512) */
+int64_t moe_mx_scale_cols(int64_t cols);
+
+/* src, dst [rows, cols] of dtype. Dequantised values are exact in float32 and rounded once to
+ * dtype. Errors: rows < 0 (0: nothing is done), cols not a positive multiple of 32
+ * (MOE_ERR_UNSUPPORTED), 2^34 elements or more, an unknown format or dtype, a pointer off a
+ * 16-byte boundary, buffers that overlap. */
+moe_status moe_mx_quantize(int32_t format, int32_t dtype, int64_t rows, int32_t cols,
+                           const void *src, void *codes, uint8_t *scales, void *stream);
+moe_status moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_t cols,
+                             const void *codes, const uint8_t *scales, void *dst, void *stream);
+
+/* moe_residual_norm_fwd with x' in 8 bits: x_codes [T, H] and x_scales [T,
+ * moe_mx_scale_cols(H)] are moe_mx_quantize (E4M3) of the x' that x_out would hold, bit for bit;
+ * x_out may be NULL. The backward is moe_residual_norm_bwd. Errors as there, and pre none;
+ * MOE_ERR_UNSUPPORTED: H not a multiple of 32. */
+moe_status moe_residual_norm_mx_fwd(const moe_residual *desc, const void *h, const void *y,
+                                    const moe_residual_params *params, const int64_t *rng,
+                                    int64_t site, void *h_out, void *x_out, uint8_t *x_codes,
+                                    uint8_t *x_scales, float *stats, void *stream);
+
 const char *moe_status_str(moe_status status);
 
 /* Text of the last error raised on the calling thread ("" if none). */
@@ -538,7 +632,9 @@ typedef enum {
   MOE_K_ACCUMULATE = 16, MOE_K_MERGE = 17, MOE_K_DY_GATHER = 18, MOE_K_DW_SUM = 19,
   MOE_K_ROW_SCALE = 20, MOE_K_DROPOUT = 21, MOE_K_RESIDUAL_NORM = 22,
   MOE_K_RESIDUAL_NORM_BWD = 23, MOE_K_LINEAR_FWD = 24, MOE_K_LINEAR_BWD = 25,
-  MOE_K_COUNT = 26
+  MOE_K_MX_QUANTIZE = 26, MOE_K_MX_DEQUANTIZE = 27, MOE_K_MX_LINEAR = 28, MOE_K_GRAD_NORM = 29,
+  MOE_K_GRAD_CLIP = 30,
+  MOE_K_COUNT = 31
 } moe_kernel_id;
 moe_status moe_kernel_timer_enable(int32_t on);
 /* Time only the kernels whose bit (1u << id) is set in mask (all, by default):

@@ -23,9 +23,10 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (ACT_IDS, GATE_IDS, MoeBaseGrads, MoeLinearShape, MoeLoraGrads, MoeResidual,
-                   MoeResidualGrads, MoeResidualParams, MoeSaved, MoeShape, MoeWeights, NORM_IDS,
-                   ROUTER_IDS, check)
+from ._lib import (ACT_IDS, GATE_IDS, MX_IDS, MoeBaseGrads, MoeGrad, MoeGroupedRouter,
+                   MoeLinearShape, MoeLoraGrads, MoeResidual, MoeResidualGrads,
+                   MoeResidualParams, MoeSaved, MoeShape, MoeWeights, NORM_IDS, ROUTER_IDS,
+                   SCORE_IDS, check)
 
 __all__ = [
     "Shape", "moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
@@ -39,7 +40,9 @@ __all__ = [
     "moe_residual_norm_bwd", "moe_dropout", "LinearShape", "moe_linear_workspace_bytes",
     "moe_linear_fwd", "moe_linear_bwd", "kernel_timer", "ROUTER_IDS", "NORM_IDS", "GATE_IDS",
     "ACT_IDS",
-    "library_path",
+    "library_path", "GroupedRouter", "moe_route_grouped", "moe_route_grouped_bwd", "GradList",
+    "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_grad_clip", "SCORE_IDS", "MX_IDS",
+    "mx_scale_cols", "moe_mx_quantize", "moe_mx_dequantize", "moe_residual_norm_mx_fwd",
 ]
 
 _TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
@@ -672,6 +675,168 @@ def moe_linear_bwd(shape: LinearShape, dy, x, w, pre, dx, dw, dbias, ws, rng=Non
             _addr(dbias, (N,), dt, "dbias", True), wsp, wsb)
     dev = _device(dy, x, w, pre, dx, dw, dbias, ws, rng)
     _call(_lib.load().moe_linear_bwd, "moe_linear_bwd", dev, stream, *args)
+
+
+@dataclass(frozen=True)
+class GroupedRouter:
+    """Routing with a bias for balance and groups: the k experts of the largest score + bias within
+    the topk_groups best of `groups` equal runs of experts (a group's score: the sum of its
+    group_top largest); weights scale * score, with renorm divided by the chosen scores' sum.
+    score: "softmax" or "sigmoid" of the logits."""
+    E: int
+    k: int
+    score: str = "sigmoid"
+    groups: int = 1
+    topk_groups: int = 1
+    group_top: int = 2
+    renorm: bool = True
+    scale: float = 1.0
+
+    @functools.cached_property
+    def _c(self) -> tuple:
+        return (self.E, self.k, SCORE_IDS[self.score], self.groups, self.topk_groups,
+                self.group_top, int(self.renorm), float(self.scale))
+
+    def c(self, T: int) -> MoeGroupedRouter:
+        _sizes(self, "E", "k", "groups", "topk_groups", "group_top")
+        if not 0 < T < 1 << 31:
+            raise ValueError(f"T must be in [1, 2^31), got {T}")
+        return MoeGroupedRouter(T, *self._c)
+
+
+def moe_route_grouped(router: GroupedRouter, logits, topk_ids, topk_w, bias=None, stream=None):
+    """topk_ids (int32), topk_w (float32) [T, k] from logits [T, E] and bias [E] (float32, or None)."""
+    T, f32 = logits.shape[0], torch.float32
+    args = (ctypes.byref(router.c(T)), _addr(logits, (T, router.E), f32, "logits"),
+            _addr(bias, (router.E,), f32, "bias", True),
+            _addr(topk_ids, (T, router.k), torch.int32, "topk_ids"),
+            _addr(topk_w, (T, router.k), f32, "topk_w"))
+    dev = _device(logits, bias, topk_ids, topk_w)
+    _call(_lib.load().moe_route_grouped, "moe_route_grouped", dev, stream, *args)
+
+
+def moe_route_grouped_bwd(router: GroupedRouter, logits, topk_ids, d_topk_w, d_logits,
+                          stream=None):
+    """d_logits [T, E] from the gradient of topk_w, the choice held fixed (the bias gets none)."""
+    T, f32 = logits.shape[0], torch.float32
+    args = (ctypes.byref(router.c(T)), _addr(logits, (T, router.E), f32, "logits"),
+            _addr(topk_ids, (T, router.k), torch.int32, "topk_ids"),
+            _addr(d_topk_w, (T, router.k), f32, "d_topk_w"),
+            _addr(d_logits, (T, router.E), f32, "d_logits"))
+    dev = _device(logits, topk_ids, d_topk_w, d_logits)
+    _call(_lib.load().moe_route_grouped_bwd, "moe_route_grouped_bwd", dev, stream, *args)
+
+
+class GradList:
+    """Gradients that are clipped together, each written to its place in `out` (None: in place).
+    The list keeps the tensors and their addresses: a training step's gradients are the same buffers
+    every step, and marshalling them takes longer than scaling a few. A tensor whose memory has
+    moved since is refused."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients, {len(self.out)} outputs")
+        self._c = (MoeGrad * max(len(self.grads), 1))()
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            if not isinstance(g, torch.Tensor):
+                raise TypeError(f"gradient {i} must be a torch.Tensor")
+            key, dt = _dtype_of(g, f"gradient {i}")
+            self._c[i] = MoeGrad(_addr(g, g.shape, dt, f"gradient {i}"),
+                                 _addr(o, g.shape, dt, f"output {i}"), g.numel(), _ABI_DTYPES[key])
+        self._device = _device(*self.grads, *self.out)
+        self._at = [t.data_ptr() for t in self._tensors()]
+        n = ctypes.c_size_t()
+        check(_lib.load().moe_grad_norm_workspace_bytes(len(self.grads), self._c, ctypes.byref(n)),
+              "moe_grad_norm_workspace_bytes")
+        self._ws = n.value
+
+    def _tensors(self):
+        return self.grads if self.out is self.grads else self.grads + self.out
+
+    def _args(self, *others):
+        if [t.data_ptr() for t in self._tensors()] != self._at:
+            raise ValueError("a tensor of the list has moved: make a new GradList")
+        dev = _device(*self.grads[:1], *others)
+        return (len(self.grads), self._c), dev
+
+
+def moe_grad_norm_workspace_bytes(grads: GradList) -> int:
+    return grads._ws
+
+
+def moe_grad_norm(grads: GradList, norm, ws, stream=None):
+    """norm (float32 [1]) = the 2-norm of all the list's gradients together."""
+    wsp, wsb = _ws(ws, grads._ws, "ws")
+    head, dev = grads._args(norm, ws)
+    args = (*head, _addr(norm, (1,), torch.float32, "norm"), wsp, wsb)
+    _call(_lib.load().moe_grad_norm, "moe_grad_norm", dev, stream, *args)
+
+
+def moe_grad_clip(grads: GradList, norm, max_norm: float, eps: float = 1e-6, stream=None):
+    """Scales the list's gradients by min(1, max_norm / (norm + eps)); norm: float32 [1], as
+    moe_grad_norm left it or, with gradients spread over GPUs, the norm over all of them."""
+    head, dev = grads._args(norm)
+    args = (*head, _addr(norm, (1,), torch.float32, "norm"), float(max_norm), float(eps))
+    _call(_lib.load().moe_grad_clip, "moe_grad_clip", dev, stream, *args)
+
+
+def mx_scale_cols(cols: int) -> int:
+    """Scale bytes of a microscaled row of `cols` elements: 16 * ceil(cols / 512)."""
+    return 16 * ((cols + 511) // 512)
+
+
+def _mx_rows(t, name):
+    """(leading shape, rows, cols) of a tensor [.., cols] of microscaled rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    lead, cols = t.shape[:-1], t.shape[-1]
+    if cols >= 1 << 31:
+        raise ValueError(f"{name}: rows of {cols} elements")
+    return lead, lead.numel(), cols
+
+
+def _mx_args(x, codes, scales, fmt, name):
+    key, dt = _dtype_of(x, name)
+    lead, rows, cols = _mx_rows(x, name)
+    u8 = torch.uint8
+    return (MX_IDS[fmt], _ABI_DTYPES[key], rows, cols), _addr(x, x.shape, dt, name), \
+        _addr(codes, (*lead, cols // 2 if fmt == "fp4" else cols), u8, "codes"), \
+        _addr(scales, (*lead, mx_scale_cols(cols)), u8, "scales")
+
+
+def moe_mx_quantize(src, codes, scales, fmt="fp4", stream=None):
+    """Rows src [.., cols] to microscaled codes (uint8 [.., cols] for fmt "fp8", E4M3, or
+    [.., cols / 2] for "fp4", E2M1) and scales (uint8 [.., mx_scale_cols(cols)])."""
+    head, s, c, e = _mx_args(src, codes, scales, fmt, "src")
+    dev = _device(src, codes, scales)
+    _call(_lib.load().moe_mx_quantize, "moe_mx_quantize", dev, stream, *head, s, c, e)
+
+
+def moe_mx_dequantize(codes, scales, dst, fmt="fp4", stream=None):
+    """dst [.., cols] = the values that codes and scales stand for."""
+    head, d, c, e = _mx_args(dst, codes, scales, fmt, "dst")
+    dev = _device(codes, scales, dst)
+    _call(_lib.load().moe_mx_dequantize, "moe_mx_dequantize", dev, stream, *head, c, e, d)
+
+
+def moe_residual_norm_mx_fwd(desc: Residual, h, y, params, h_out, x_codes, x_scales, stats,
+                             x_out=None, rng=None, site=0, stream=None):
+    """moe_residual_norm_fwd with x_out in 8 bits: x_codes uint8 [T, H] and x_scales uint8
+    [T, mx_scale_cols(H)] as moe_mx_quantize makes them of x_out ("fp8"); x_out itself optional."""
+    rows, dt, u8 = (desc.T, desc.H), desc.torch_dtype, torch.uint8
+    q = _residual_params(desc, params)
+    args = (ctypes.byref(desc._c), _addr(h, rows, dt, "h", True), _addr(y, rows, dt, "y", True),
+            ctypes.byref(q), _rng(rng, desc.dropout), site,
+            _addr(h_out, rows, dt, "h_out", y is None), _addr(x_out, rows, dt, "x_out", True),
+            _addr(x_codes, rows, u8, "x_codes"),
+            _addr(x_scales, (desc.T, mx_scale_cols(desc.H)), u8, "x_scales"),
+            _addr(stats, (desc.T, 4), torch.float32, "stats", True))
+    dev = _device(h, y, h_out, x_out, x_codes, x_scales, stats, rng, *(params or {}).values())
+    _call(_lib.load().moe_residual_norm_mx_fwd, "moe_residual_norm_mx_fwd", dev, stream, *args)
 
 
 class kernel_timer:

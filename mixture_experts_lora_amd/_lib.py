@@ -16,9 +16,12 @@ KERNEL_IDS = {"route": 0, "permute": 1, "gather": 2, "gate_up_fwd": 3, "down_fwd
               "lora_side": 10, "lora_wgrad": 11, "unpermute": 12, "base_wgrad": 13,
               "router_fwd": 14, "router_bwd": 15, "accumulate": 16, "merge": 17,
               "dy_gather": 18, "dw_sum": 19, "row_scale": 20, "dropout": 21, "residual_norm": 22,
-              "residual_norm_bwd": 23, "linear_fwd": 24, "linear_bwd": 25}
+              "residual_norm_bwd": 23, "linear_fwd": 24, "linear_bwd": 25, "mx_quantize": 26,
+              "mx_dequantize": 27, "mx_linear": 28, "grad_norm": 29, "grad_clip": 30}
 NORM_IDS = {"none": 0, "rms": 1, "layer": 2}
 ACT_IDS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+SCORE_IDS = {"softmax": 0, "sigmoid": 1}
+MX_IDS = {"fp8": 0, "fp4": 1}
 GATE_IDS = {"none": 0, "channel": 1, "token": 2, "full": 3}
 
 EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
@@ -31,7 +34,9 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
            "moe_grouped_lora_combine_bwd_gather",
            "moe_dropout", "moe_residual_norm_workspace_bytes", "moe_residual_norm_fwd",
            "moe_residual_norm_bwd", "moe_linear_workspace_bytes", "moe_linear_fwd",
-           "moe_linear_bwd",
+           "moe_linear_bwd", "moe_route_grouped", "moe_route_grouped_bwd",
+           "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_grad_clip", "moe_mx_scale_cols",
+           "moe_mx_quantize", "moe_mx_dequantize", "moe_residual_norm_mx_fwd",
            "moe_status_str",
            "moe_last_error",
            "moe_kernel_timer_enable", "moe_kernel_timer_select", "moe_kernel_timer_reset",
@@ -77,6 +82,16 @@ class MoeResidualGrads(ctypes.Structure):
 class MoeLinearShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "dtype", "act")] + \
                [("dropout", ctypes.c_float)]
+
+
+class MoeGroupedRouter(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "score", "groups", "topk_groups",
+                                              "group_top", "renorm")] + [("scale", ctypes.c_float)]
+
+
+class MoeGrad(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -169,6 +184,18 @@ def load() -> ctypes.CDLL:
                                 P, P, ctypes.c_size_t, P]),
         "moe_linear_bwd": (st, [ctypes.POINTER(MoeLinearShape), P, P, P, P, P, ctypes.c_int64, P,
                                 P, P, P, ctypes.c_size_t, P]),
+        "moe_route_grouped": (st, [ctypes.POINTER(MoeGroupedRouter), P, P, P, P, P]),
+        "moe_route_grouped_bwd": (st, [ctypes.POINTER(MoeGroupedRouter), P, P, P, P, P]),
+        "moe_grad_norm_workspace_bytes": (st, [I32, ctypes.POINTER(MoeGrad),
+                                               ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_grad_norm": (st, [I32, ctypes.POINTER(MoeGrad), P, P, ctypes.c_size_t, P]),
+        "moe_grad_clip": (st, [I32, ctypes.POINTER(MoeGrad), P, ctypes.c_float, ctypes.c_float, P]),
+        "moe_mx_scale_cols": (ctypes.c_int64, [ctypes.c_int64]),
+        "moe_mx_quantize": (st, [I32, I32, ctypes.c_int64, I32, P, P, P, P]),
+        "moe_mx_dequantize": (st, [I32, I32, ctypes.c_int64, I32, P, P, P, P]),
+        "moe_residual_norm_mx_fwd": (st, [ctypes.POINTER(MoeResidual), P, P,
+                                          ctypes.POINTER(MoeResidualParams), P, ctypes.c_int64, P,
+                                          P, P, P, P, P]),
         "moe_status_str": (ctypes.c_char_p, [st]),
         "moe_last_error": (ctypes.c_char_p, []),
         "moe_kernel_timer_enable": (st, [I32]),

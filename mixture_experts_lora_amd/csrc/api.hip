@@ -6,36 +6,28 @@
 #include <initializer_list>
 #include <mutex>
 #include <string>
-#include <string_view>
 #include <vector>
 
+#include "api_check.h"
 #include "launch.h"
 
-namespace {
+namespace moe {
 
+namespace {
 thread_local std::string g_last_error;
+}
 
 moe_status fail(moe_status st, const std::string& what) {
   g_last_error = what;
   return st;
 }
 
-moe_status hip_fail(hipError_t e, const char* where) {
-  return fail(MOE_ERR_HIP, std::string(where) + ": " + hipGetErrorString(e));
-}
+}  // namespace moe
 
-#define CHECK_PTR(p)                                                                  \
-  do {                                                                                \
-    if ((p) == nullptr) return fail(MOE_ERR_INVALID_ARG, "null pointer: " #p);        \
-  } while (0)
+using namespace moe::check;
+using moe::fail;
 
-// Token-row buffers that the row kernels (gather, combine and their
-// backwards) move in 16-byte pieces must start on a 16-byte boundary.
-#define CHECK_ROWS(p)                                                                 \
-  do {                                                                                \
-    if ((reinterpret_cast<uintptr_t>(p) & 15) != 0)                                   \
-      return fail(MOE_ERR_INVALID_ARG, #p " does not start on a 16-byte boundary");   \
-  } while (0)
+namespace {
 
 moe_status check_router(int32_t router) {
   if (router < MOE_SOFTMAX_TOPK || router > MOE_SIGMOID_TOPK_RENORM)
@@ -87,8 +79,6 @@ moe::ExpertDims dims_of(const moe_shape* s) {
   d.scale = s->lora_scale;
   return d;
 }
-
-inline hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
 // ---------------------------------------------------------------- kernel timer
 struct TimerRec {
@@ -163,7 +153,7 @@ const char* moe_status_str(moe_status st) {
   return "unknown status";
 }
 
-const char* moe_last_error(void) { return g_last_error.c_str(); }
+const char* moe_last_error(void) { return moe::g_last_error.c_str(); }
 
 moe_status moe_workspace_bytes(const moe_shape* shape, size_t* fwd_ws, size_t* bwd_ws,
                                size_t* permute_ws) {
@@ -214,6 +204,65 @@ moe_status moe_route_bwd(const float* logits, const int32_t* topk_ids, const flo
   hipError_t e = moe::launch_route_bwd(logits, topk_ids, d_topk_w, T, E, k, router, d_logits,
                                        as_stream(stream));
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_route_bwd");
+}
+
+namespace {
+
+moe_status check_grouped_router(const moe_grouped_router* r) {
+  if (!r) return fail(MOE_ERR_INVALID_ARG, "null router");
+  moe_status st = check_routing_dims(r->T, r->E, r->k);
+  if (st != MOE_OK) return st;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARG, "unknown score " + std::to_string(r->score));
+  if (r->groups < 1 || r->E % r->groups != 0)
+    return fail(MOE_ERR_INVALID_ARG, "groups must be >= 1 and divide E");
+  if (r->groups > 64) return fail(MOE_ERR_UNSUPPORTED, "more than 64 groups are not supported");
+  if (r->topk_groups < 1 || r->topk_groups > r->groups)
+    return fail(MOE_ERR_INVALID_ARG, "topk_groups must be in [1, groups]");
+  if (int64_t(r->topk_groups) * (r->E / r->groups) < r->k)
+    return fail(MOE_ERR_INVALID_ARG, "the kept groups hold fewer than k experts");
+  if (r->group_top != 1 && r->group_top != 2)
+    return fail(MOE_ERR_INVALID_ARG, "group_top must be 1 or 2");
+  if (!std::isfinite(r->scale)) return fail(MOE_ERR_INVALID_ARG, "scale must be finite");
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_route_grouped(const moe_grouped_router* router, const float* logits,
+                             const float* bias, int32_t* topk_ids, float* topk_w, void* stream) {
+  moe_status st = check_grouped_router(router);
+  if (st != MOE_OK) return st;
+  CHECK_PTR(logits);
+  CHECK_PTR(topk_ids);
+  CHECK_PTR(topk_w);
+  const int64_t T = router->T, row = int64_t(router->E) * 4, out = T * router->k * 4;
+  st = check_ranges({{topk_ids, out, "topk_ids"}, {topk_w, out, "topk_w"}},
+                    {{logits, T * row, "logits"}, {bias, row, "bias"}});
+  if (st != MOE_OK) return st;
+  moe::TimedScope ts(moe::active_timer(), MOE_K_ROUTE, as_stream(stream));
+  hipError_t e = moe::launch_route_grouped(*router, logits, bias, topk_ids, topk_w,
+                                           as_stream(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_route_grouped");
+}
+
+moe_status moe_route_grouped_bwd(const moe_grouped_router* router, const float* logits,
+                                 const int32_t* topk_ids, const float* d_topk_w, float* d_logits,
+                                 void* stream) {
+  moe_status st = check_grouped_router(router);
+  if (st != MOE_OK) return st;
+  CHECK_PTR(logits);
+  CHECK_PTR(topk_ids);
+  CHECK_PTR(d_topk_w);
+  CHECK_PTR(d_logits);
+  const int64_t rows = int64_t(router->T) * router->E * 4, in = int64_t(router->T) * router->k * 4;
+  st = check_ranges({{d_logits, rows, "d_logits"}},
+                    {{logits, rows, "logits"}, {topk_ids, in, "topk_ids"}, {d_topk_w, in, "d_topk_w"}});
+  if (st != MOE_OK) return st;
+  moe::TimedScope ts(moe::active_timer(), MOE_K_ROUTE_BWD, as_stream(stream));
+  hipError_t e = moe::launch_route_grouped_bwd(*router, logits, topk_ids, d_topk_w, d_logits,
+                                               as_stream(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_route_grouped_bwd");
 }
 
 moe_status moe_permute(const moe_shape* shape, const int32_t* topk_ids, const void* x,
@@ -756,39 +805,6 @@ moe_status moe_accumulate(int32_t dtype, int64_t n, const void* src, void* dst, 
 
 namespace {
 
-struct Range {
-  const void* p;
-  int64_t bytes;
-  const char* name;
-  const char* may_be = nullptr;  // an input: the name of the output that may be this very buffer
-};
-
-bool ranges_overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + static_cast<uintptr_t>(b.bytes) && y < x + static_cast<uintptr_t>(a.bytes);
-}
-
-// No output may overlap an input or another output, apart from the inputs that name one. The name
-// decides, not the address: another input at the same address is read by blocks that the output's
-// own do not wait for.
-moe_status check_ranges(std::initializer_list<Range> outs, std::initializer_list<Range> ins) {
-  for (const Range& o : outs) {
-    for (const Range& i : ins)
-      if (ranges_overlap(o, i) &&
-          !(i.may_be && o.p == i.p && std::string_view(i.may_be) == o.name))
-        return fail(MOE_ERR_INVALID_ARG, std::string(o.name) + " overlaps " + i.name);
-    for (const Range& other : outs)
-      if (&o != &other && ranges_overlap(o, other))
-        return fail(MOE_ERR_INVALID_ARG, std::string(o.name) + " overlaps " + other.name);
-  }
-  return MOE_OK;
-}
-
-bool known_dtype(int32_t dtype) {
-  return dtype == MOE_F32 || dtype == MOE_BF16 || dtype == MOE_F16;
-}
-
 // Fills the threshold and scale of dropout probability p.
 moe_status make_drop(float p, const int64_t* rng, int64_t site, moe::DropArgs* d) {
   if (!(p >= 0.f && p < 1.f))
@@ -823,8 +839,6 @@ moe_status check_residual(const moe_residual* r) {
   if (r->H > 16384) return fail(MOE_ERR_UNSUPPORTED, "H > 16384 is not supported");
   return MOE_OK;
 }
-
-inline int64_t esize(int32_t dtype) { return dtype == MOE_F32 ? 4 : 2; }
 
 int64_t gate_bytes(const moe_residual* r) {
   const int64_t e = esize(r->dtype);
@@ -917,10 +931,13 @@ moe_status moe_residual_norm_workspace_bytes(const moe_residual* desc, size_t* b
   return MOE_OK;
 }
 
-moe_status moe_residual_norm_fwd(const moe_residual* desc, const void* h, const void* y,
-                                 const moe_residual_params* params, const int64_t* rng,
-                                 int64_t site, void* h_out, void* x_out, float* stats,
-                                 void* stream) {
+namespace {
+
+// codes, scales: the normed rows in 8 bits too (both or neither); x_out may then be NULL
+moe_status residual_norm_fwd(const char* name, const moe_residual* desc, const void* h,
+                             const void* y, const moe_residual_params* params, const int64_t* rng,
+                             int64_t site, void* h_out, void* x_out, uint8_t* codes,
+                             uint8_t* scales, float* stats, void* stream) {
   moe_status st = check_residual(desc);
   if (st != MOE_OK) return st;
   if (!h && !y) return fail(MOE_ERR_INVALID_ARG, "h and y are both NULL");
@@ -930,16 +947,20 @@ moe_status moe_residual_norm_fwd(const moe_residual* desc, const void* h, const 
     return fail(MOE_ERR_INVALID_ARG, "a post norm, a gate or dropout needs y");
   if ((st = residual_params(desc, params, &a)) != MOE_OK) return st;
   if (y) CHECK_PTR(h_out);
-  if (desc->pre != MOE_NORM_NONE) CHECK_PTR(x_out);
-  else if (x_out) return fail(MOE_ERR_INVALID_ARG, "x_out without a pre norm");
-  if (!h_out && !x_out) return fail(MOE_ERR_INVALID_ARG, "no output");
+  if (desc->pre != MOE_NORM_NONE && !codes) CHECK_PTR(x_out);
+  else if (x_out && desc->pre == MOE_NORM_NONE) return fail(MOE_ERR_INVALID_ARG, "x_out without a pre norm");
+  if (!h_out && !x_out && !codes) return fail(MOE_ERR_INVALID_ARG, "no output");
   CHECK_ROWS(h);
   CHECK_ROWS(y);
   CHECK_ROWS(h_out);
   CHECK_ROWS(x_out);
+  CHECK_ROWS(codes);
+  CHECK_ROWS(scales);
   CHECK_ROWS(stats);
   const int64_t row = desc->H * esize(desc->dtype), rows = row * desc->T;
-  st = check_ranges({{h_out, rows, "h_out"}, {x_out, rows, "x_out"}, {stats, int64_t(desc->T) * 16, "stats"}},
+  st = check_ranges({{h_out, rows, "h_out"}, {x_out, rows, "x_out"}, {stats, int64_t(desc->T) * 16, "stats"},
+                     {codes, int64_t(desc->T) * desc->H, "codes"},
+                     {scales, int64_t(desc->T) * moe_mx_scale_cols(desc->H), "scales"}},
                     {{h, rows, "h", "h_out"}, {y, rows, "y"}, {a.w_post, row, "w_post"}, {a.b_post, row, "b_post"},
                      {a.gate, gate_bytes(desc), "gate"}, {a.w_pre, row, "w_pre"}, {a.b_pre, row, "b_pre"},
                      {a.drop.thr ? rng : nullptr, 16, "rng"}});
@@ -950,8 +971,37 @@ moe_status moe_residual_norm_fwd(const moe_residual* desc, const void* h, const 
   a.h_out = h_out;
   a.x_out = x_out;
   a.stats = reinterpret_cast<float4*>(stats);
-  hipError_t e = moe::launch_residual_fwd(desc->dtype, a, as_stream(stream), moe::active_timer());
-  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_residual_norm_fwd");
+  a.codes = codes;
+  a.scales = scales;
+  auto* launch = codes ? moe::launch_residual_fwd_mx : moe::launch_residual_fwd;
+  hipError_t e = launch(desc->dtype, a, as_stream(stream), moe::active_timer());
+  return e == hipSuccess ? MOE_OK : hip_fail(e, name);
+}
+
+}  // namespace
+
+moe_status moe_residual_norm_fwd(const moe_residual* desc, const void* h, const void* y,
+                                 const moe_residual_params* params, const int64_t* rng,
+                                 int64_t site, void* h_out, void* x_out, float* stats,
+                                 void* stream) {
+  return residual_norm_fwd("moe_residual_norm_fwd", desc, h, y, params, rng, site, h_out, x_out,
+                           nullptr, nullptr, stats, stream);
+}
+
+moe_status moe_residual_norm_mx_fwd(const moe_residual* desc, const void* h, const void* y,
+                                    const moe_residual_params* params, const int64_t* rng,
+                                    int64_t site, void* h_out, void* x_out, uint8_t* x_codes,
+                                    uint8_t* x_scales, float* stats, void* stream) {
+  moe_status st = check_residual(desc);
+  if (st != MOE_OK) return st;
+  if (desc->pre == MOE_NORM_NONE)
+    return fail(MOE_ERR_INVALID_ARG, "an 8-bit output needs a pre norm");
+  if (desc->H % 32 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "an 8-bit output needs H a multiple of 32");
+  CHECK_PTR(x_codes);
+  CHECK_PTR(x_scales);
+  return residual_norm_fwd("moe_residual_norm_mx_fwd", desc, h, y, params, rng, site, h_out, x_out,
+                           x_codes, x_scales, stats, stream);
 }
 
 moe_status moe_residual_norm_bwd(const moe_residual* desc, const void* dh_out, const void* dx_out,
@@ -1152,6 +1202,119 @@ moe_status moe_linear_bwd(const moe_linear_shape* shape, const void* dy, const v
   hipError_t err = moe::launch_linear_bwd(d, dy, x, w, epi, dx, dw, dbias, ws, as_stream(stream),
                                           moe::active_timer());
   return err == hipSuccess ? MOE_OK : hip_fail(err, "moe_linear_bwd");
+}
+
+namespace {
+
+// clip: every tensor has a dst
+moe_status check_grads(int32_t count, const moe_grad* grads, bool clip) {
+  if (count < 0) return fail(MOE_ERR_INVALID_ARG, "count < 0");
+  if (count > 0) CHECK_PTR(grads);
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_grad& g = grads[i];
+    const std::string at = "gradient " + std::to_string(i);
+    if (!known_dtype(g.dtype)) return fail(MOE_ERR_INVALID_ARG, at + ": unknown dtype");
+    if (g.n < 0 || g.n > (int64_t(1) << 40))
+      return fail(MOE_ERR_INVALID_ARG, at + ": n must be in [0, 2^40]");
+    if (g.n == 0) continue;
+    if (!g.src) return fail(MOE_ERR_INVALID_ARG, at + ": null src");
+    if (reinterpret_cast<uintptr_t>(g.src) % esize(g.dtype))
+      return fail(MOE_ERR_INVALID_ARG, at + ": src is not aligned to its type");
+    if (!clip) continue;
+    if (!g.dst) return fail(MOE_ERR_INVALID_ARG, at + ": null dst");
+    if (reinterpret_cast<uintptr_t>(g.dst) % esize(g.dtype))
+      return fail(MOE_ERR_INVALID_ARG, at + ": dst is not aligned to its type");
+  }
+  return MOE_OK;
+}
+
+// No output of moe_grad_clip may overlap another one, an input other than its own, or the norm:
+// the ranges in order of their addresses, each against those that reach past its start.
+moe_status check_grad_ranges(int32_t count, const moe_grad* grads, const float* norm) {
+  struct Span {
+    uintptr_t lo, hi;
+    int32_t index;
+    bool out;
+  };
+  std::vector<Span> spans;
+  auto add = [&](const void* p, int64_t bytes, int32_t index, bool out) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    spans.push_back({lo, lo + static_cast<uintptr_t>(bytes), index, out});
+  };
+  add(norm, 4, -1, false);
+  for (int32_t i = 0; i < count; ++i) {
+    const moe_grad& g = grads[i];
+    if (g.n == 0) continue;
+    add(g.dst, g.n * esize(g.dtype), i, true);
+    if (g.src != g.dst) add(g.src, g.n * esize(g.dtype), i, false);
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  // the span that reaches furthest so far, among all and among the outputs
+  const Span *all = nullptr, *outs = nullptr;
+  for (const Span& s : spans) {
+    const Span* hit = s.out ? all : outs;
+    if (hit && hit->hi > s.lo) {
+      auto name = [](const Span& x) {
+        return x.index < 0 ? std::string("norm")
+                           : std::string(x.out ? "dst" : "src") + " of gradient " +
+                                 std::to_string(x.index);
+      };
+      return fail(MOE_ERR_INVALID_ARG, name(s) + " overlaps " + name(*hit));
+    }
+    if (!all || s.hi > all->hi) all = &s;
+    if (s.out && (!outs || s.hi > outs->hi)) outs = &s;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_grad_norm_workspace_bytes(int32_t count, const moe_grad* grads, size_t* ws) {
+  moe_status st = check_grads(count, grads, false);
+  if (st != MOE_OK) return st;
+  CHECK_PTR(ws);
+  *ws = moe::grad_norm_ws_bytes(count, grads);
+  return MOE_OK;
+}
+
+moe_status moe_grad_norm(int32_t count, const moe_grad* grads, float* norm, void* ws,
+                         size_t ws_bytes, void* stream) {
+  moe_status st = check_grads(count, grads, false);
+  if (st != MOE_OK) return st;
+  CHECK_PTR(norm);
+  const size_t need = moe::grad_norm_ws_bytes(count, grads);
+  if (need > 0) CHECK_PTR(ws);
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "gradient norm workspace needs " + std::to_string(need) + " bytes");
+  if (reinterpret_cast<uintptr_t>(norm) & 3)
+    return fail(MOE_ERR_INVALID_ARG, "norm does not start on a 4-byte boundary");
+  if (need > 0) CHECK_ROWS(ws);
+  const void* scratch = need ? ws : nullptr;
+  for (int32_t i = 0; i < count; ++i) {
+    st = check_ranges({{norm, 4, "norm"}, {scratch, int64_t(need), "ws"}},
+                      {{grads[i].n ? grads[i].src : nullptr, grads[i].n * esize(grads[i].dtype), "src"}});
+    if (st != MOE_OK) return st;
+  }
+  hipError_t e = moe::launch_grad_norm(count, grads, norm, ws, as_stream(stream),
+                                       moe::active_timer());
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_grad_norm");
+}
+
+moe_status moe_grad_clip(int32_t count, const moe_grad* grads, const float* norm, float max_norm,
+                         float eps, void* stream) {
+  moe_status st = check_grads(count, grads, true);
+  if (st != MOE_OK) return st;
+  CHECK_PTR(norm);
+  if (reinterpret_cast<uintptr_t>(norm) & 3)
+    return fail(MOE_ERR_INVALID_ARG, "norm does not start on a 4-byte boundary");
+  if (!(max_norm >= 0.f) || !std::isfinite(max_norm))
+    return fail(MOE_ERR_INVALID_ARG, "max_norm must be finite and >= 0");
+  if (!(eps > 0.f) || !std::isfinite(eps))
+    return fail(MOE_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if ((st = check_grad_ranges(count, grads, norm)) != MOE_OK) return st;
+  hipError_t e = moe::launch_grad_clip(count, grads, norm, max_norm, eps, as_stream(stream),
+                                       moe::active_timer());
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_grad_clip");
 }
 
 moe_status moe_kernel_timer_enable(int32_t on) {

@@ -37,6 +37,12 @@ hipError_t launch_route(const float* logits, int T, int E, int k, int router, in
 hipError_t launch_route_bwd(const float* logits, const int32_t* ids, const float* dw, int T,
                             int E, int k, int router, float* dlogits, hipStream_t s);
 
+hipError_t launch_route_grouped(const moe_grouped_router& r, const float* logits,
+                                const float* bias, int32_t* ids, float* w, hipStream_t s);
+hipError_t launch_route_grouped_bwd(const moe_grouped_router& r, const float* logits,
+                                    const int32_t* ids, const float* dw, float* dlogits,
+                                    hipStream_t s);
+
 // ---- permutation
 size_t permute_ws_bytes(int64_t N, int E);
 // The current GPU's copy of the moe_permute_noalloc table
@@ -172,6 +178,7 @@ struct ResidualArgs {
   void *h_out, *x_out;
   float4* stats;  // [T]: post mean and rstd, pre mean and rstd
   DropArgs drop;
+  uint8_t *codes, *scales;  // launch_residual_fwd_mx: x' in 8 bits
 };
 
 // f: the forward's vectors, y and statistics (h, h_out and x_out unused).
@@ -188,6 +195,8 @@ struct ResidualBwdArgs {
 
 int64_t residual_bwd_groups(int T, int H);
 hipError_t launch_residual_fwd(int dtype, const ResidualArgs& a, hipStream_t s, KernelTimer* tm);
+hipError_t launch_residual_fwd_mx(int dtype, const ResidualArgs& a, hipStream_t s,
+                                  KernelTimer* tm);
 hipError_t launch_residual_bwd(int dtype, const ResidualBwdArgs& a, hipStream_t s,
                                KernelTimer* tm);
 hipError_t launch_residual_bwd_bf16(const ResidualBwdArgs& a, hipStream_t s);
@@ -207,5 +216,18 @@ hipError_t launch_linear_fwd(const LinearDims& d, const void* x, const void* w,
 hipError_t launch_linear_bwd(const LinearDims& d, const void* dy, const void* x, const void* w,
                              const LinearEpi& epi, void* dx, void* dw, void* db, void* ws,
                              hipStream_t s, KernelTimer* tm);
+
+// ---- gradients of many tensors
+size_t grad_norm_ws_bytes(int count, const moe_grad* grads);
+hipError_t launch_grad_norm(int count, const moe_grad* grads, float* norm, void* ws, hipStream_t s,
+                            KernelTimer* tm);
+hipError_t launch_grad_clip(int count, const moe_grad* grads, const float* norm, float max_norm,
+                            float eps, hipStream_t s, KernelTimer* tm);
+
+// ---- microscaled formats
+hipError_t launch_mx_quantize(int fmt, int dtype, int64_t rows, int cols, const void* src,
+                              void* codes, uint8_t* scales, hipStream_t s, KernelTimer* tm);
+hipError_t launch_mx_dequantize(int fmt, int dtype, int64_t rows, int cols, const void* codes,
+                                const uint8_t* scales, void* dst, hipStream_t s, KernelTimer* tm);
 
 }  // namespace moe

@@ -1,0 +1,14 @@
+// The residual operator's forward with its normed rows in 8 bits and scales: the same kernel, which
+// rounds a row to its type and encodes it from there while it is in registers. It writes half the
+// bytes of a 16-bit row.
+#include "residual_fwd.h"
+
+namespace moe {
+
+hipError_t launch_residual_fwd_mx(int dtype, const ResidualArgs& a, hipStream_t s,
+                                  KernelTimer* tm) {
+  TimedScope ts(tm, MOE_K_RESIDUAL_NORM, s);
+  return launch_residual_rows<true>(dtype, a, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,375 @@
+// Routing with a bias for balance and groups of experts, and its backward.
+//
+//   s_i = softmax(l)_i or sigmoid(l_i)      v_i = s_i + b_i        (b only decides the choice)
+//   a group's score: the sum of its one or two largest v; the best groups stay
+//   the k largest v of those are chosen, in order; ties go to the lower index
+//   w_j = c s_j, or c s_j / sum of the chosen s
+//
+// Choice. v is formed in 64 bits: two scores that differ in float32's last bits decide which expert
+// a token goes to, and sigmoid saturates in float32. A candidate is one positive double, its key:
+// v's bits in an order-preserving form, the lowest ten replaced by 1023 - index. The largest key is
+// then the largest v (to 2^-41 of it) with the lower index first, and a maximum is one v_max_f64.
+// Without a bias, and where no two scores are added, the logits order the experts as the scores do
+// and stand in for them.
+//
+// L lanes work on a token, 16 where a row has no more than 256 experts, so that a wave's rounds of
+// the top-k serve four tokens; expert i belongs to lane i % L. The kernel is bound by instructions
+// (64-bit exponentials and k rounds over the keys), not by its 4 E + 8 k bytes a token.
+#include "device_common.h"
+#include "launch.h"
+
+#include <float.h>
+
+namespace moe {
+
+namespace {
+
+constexpr int kRouteBlock = 256;
+constexpr int kMaxGroups = 64;
+
+// ---- reductions over the L lanes of a token (16: a DPP row; 64: the wave); every lane gets the result
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = dpp_i32<CTRL>(static_cast<int>(static_cast<uint32_t>(b)));
+  const uint32_t hi = dpp_i32<CTRL>(static_cast<int>(static_cast<uint32_t>(b >> 32)));
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+__device__ __forceinline__ double readlane_f64(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(b)), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(b >> 32)), lane);
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+template <int L, typename T, typename Op>
+__device__ __forceinline__ T lanes_reduce(T v, Op op) {
+  if constexpr (sizeof(T) == 8) {
+    v = op(v, dpp_f64<kDppSwap1>(v));
+    v = op(v, dpp_f64<kDppSwap2>(v));
+    v = op(v, dpp_f64<kDppHalfMirror>(v));
+    v = op(v, dpp_f64<kDppMirror>(v));
+    if constexpr (L == 64)
+      v = op(op(readlane_f64(v, 0), readlane_f64(v, 16)), op(readlane_f64(v, 32), readlane_f64(v, 48)));
+  } else {
+    v = op(v, dpp_f32<kDppSwap1>(v));
+    v = op(v, dpp_f32<kDppSwap2>(v));
+    v = op(v, dpp_f32<kDppHalfMirror>(v));
+    v = op(v, dpp_f32<kDppMirror>(v));
+    if constexpr (L == 64)
+      v = op(op(readlane_f32(v, 0), readlane_f32(v, 16)), op(readlane_f32(v, 32), readlane_f32(v, 48)));
+  }
+  return v;
+}
+template <int L, typename T>
+__device__ __forceinline__ T lanes_max(T v) {
+  return lanes_reduce<L>(v, [](T a, T b) __attribute__((always_inline)) {
+    if constexpr (sizeof(T) == 8) return __builtin_fmax(a, b);
+    else return fmaxf(a, b);
+  });
+}
+template <int L, typename T>
+__device__ __forceinline__ T lanes_sum(T v) {
+  return lanes_reduce<L>(v, [](T a, T b) __attribute__((always_inline)) { return a + b; });
+}
+
+// The key of candidate idx with value v: positive, finite, larger for a larger v and, where v is the
+// same, for a lower idx. NaN ranks below -infinity. |v| < 2^1023 (float32 sums are).
+__device__ __forceinline__ double route_key(double v, int idx) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 as 0
+  uint64_t o = (b >> 63) ? ~b : (b | (uint64_t{1} << 63));
+  // an infinite v gives the largest finite key
+  o = min(o, uint64_t{0xFFBFFFFFFFFFFFFFull});
+  if (v != v) o = 0;
+  o = (o >> 1) + (uint64_t{1} << 52);  // above every taken candidate's key, which has no exponent
+  return __builtin_bit_cast(double, (o & ~uint64_t{1023}) | static_cast<uint64_t>(1023 - idx));
+}
+__device__ __forceinline__ int key_index(double key) {
+  return 1023 - static_cast<int>(__builtin_bit_cast(uint64_t, key) & 1023);
+}
+
+// ---- weights of the chosen. Lane j < k of a token holds slot j's logit l; the others hold
+// -infinity. Ratios are formed so that neither a large negative row nor an
+// overflowing exponential turns them into 0 / 0: with m the largest chosen logit,
+//   sigmoid(l) / sigmoid(m) = e^(l-m) (1 + e^m) / (1 + e^l)   for m <= 0,  sigmoid itself above.
+// A row whose chosen logits are all -infinity gets weights 0.
+__device__ __forceinline__ float sigmoid_precise(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+template <int L>
+__device__ __forceinline__ float renorm_weight(float l, bool act, int sigmoid, float c) {
+  const float m = lanes_max<L>(l);
+  if (m == -INFINITY) return 0.f;
+  float e;
+  if (!sigmoid) {
+    e = act ? expf(l - m) : 0.f;
+  } else if (m > 0.f) {
+    e = act ? sigmoid_precise(l) : 0.f;
+  } else {
+    e = act ? expf(l - m) * (1.0f + expf(m)) / (1.0f + expf(l)) : 0.f;
+  }
+  return c * e / lanes_sum<L>(e);
+}
+
+template <int L, int NV>
+__global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
+    moe_grouped_router r, const float* __restrict__ logits, const float* __restrict__ bias,
+    int32_t* __restrict__ ids, float* __restrict__ w) {
+  constexpr int TPB = kRouteBlock / L;  // tokens a block
+  // a token's values with a gap after each group, so that the lanes that scan the groups of a token
+  // do not meet in a bank
+  constexpr int ROW = L * NV + kMaxGroups;
+  __shared__ double vals[TPB * ROW];
+  __shared__ double gscore[TPB * (L == 16 ? 16 : kMaxGroups)];
+  const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * TPB + slot;
+  const bool there = t < r.T;
+  const int E = r.E;
+  const float* l = logits + (there ? t : 0) * E;  // lanes past the last token repeat the first
+  float lg[NV];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + L * i;
+    lg[i] = e < E ? l[e] : -INFINITY;
+    mx = fmaxf(mx, lg[i]);
+  }
+  mx = lanes_max<L>(mx);
+  const bool sigmoid = r.score == MOE_SCORE_SIGMOID;
+  const bool by_logit = !bias && (r.groups == 1 || r.group_top == 1);
+  double v[NV];
+  if (by_logit) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = static_cast<double>(lg[i]);
+  } else {
+    // a row of -infinity: every score 0
+    const double shift = sigmoid || mx == -INFINITY ? 0.0 : static_cast<double>(mx);
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const double x = static_cast<double>(lg[i]) - shift;
+      v[i] = exp(sigmoid ? -x : x);
+      if (sigmoid) v[i] = 1.0 / (1.0 + v[i]);
+      else sum += v[i];  // exp(-infinity) past the row
+    }
+    if (!sigmoid) {
+      sum = lanes_sum<L>(sum);
+      const double inv = sum > 0.0 ? 1.0 / sum : (sum == 0.0 ? 0.0 : sum);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[i] *= inv;
+    }
+    if (bias) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = lane + L * i;
+        if (e < E) v[i] += static_cast<double>(bias[e]);
+      }
+    }
+  }
+  double key[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + L * i;
+    key[i] = e < E ? route_key(v[i], e) : 0.0;
+  }
+  if (r.groups > 1) {
+    const int gs = E / r.groups;
+    double* row = vals + slot * ROW;
+    double* sc = gscore + slot * (L == 16 ? 16 : kMaxGroups);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + L * i;
+      if (e < E) row[e + e / gs] = v[i];
+    }
+    __syncthreads();
+    double mine = -INFINITY;
+    if (lane < r.groups) {
+      const double* g = row + lane * (gs + 1);
+      double a = -INFINITY, b = -INFINITY;  // the largest and the second
+      for (int i = 0; i < gs; ++i) {
+        const double x = g[i] != g[i] ? -INFINITY : g[i];
+        b = __builtin_fmax(b, __builtin_fmin(a, x));
+        a = __builtin_fmax(a, x);
+      }
+      mine = r.group_top == 2 && gs > 1 ? a + b : a;
+      if (mine != mine) mine = -INFINITY;
+      sc[lane] = mine;
+    }
+    __syncthreads();
+    bool keep = false;
+    if (lane < r.groups) {
+      int rank = 0;
+      for (int h = 0; h < r.groups; ++h) {
+        const double o = sc[h];
+        rank += o > mine || (o == mine && h < lane);
+      }
+      keep = rank < r.topk_groups;
+    }
+    // bit g of this token's lanes: group g stays
+    uint64_t kept = __ballot(keep);
+    if (L < 64) kept = (kept >> (threadIdx.x % kWave / L * L)) & ((uint64_t{1} << (L & 63)) - 1);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + L * i;
+      if (e < E && !((kept >> (e / gs)) & 1)) key[i] = 0.0;
+    }
+  }
+  int id = 0;
+  for (int j = 0; j < r.k; ++j) {
+    double best = key[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) best = __builtin_fmax(best, key[i]);
+    best = lanes_max<L>(best);
+    const int idx = key_index(best);
+    if (lane == j) id = idx;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (idx == lane + L * i) key[i] = 0.0;
+  }
+  const bool act = lane < r.k;
+  const float chosen = act ? l[id] : -INFINITY;
+  float wj;
+  if (r.renorm) {
+    wj = renorm_weight<L>(chosen, act, sigmoid, r.scale);
+  } else if (sigmoid) {
+    wj = r.scale * sigmoid_precise(chosen);
+  } else {
+    float s = 0.f;
+    const float m = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s += expf(lg[i] - m);
+    s = lanes_sum<L>(s);
+    wj = s == 0.f ? 0.f : r.scale * (expf(chosen - m) / s);
+  }
+  if (there && act) {
+    ids[t * r.k + lane] = id;
+    w[t * r.k + lane] = wj;
+  }
+}
+
+// d logits from the gradient D at the weights, which reaches the scores of the chosen alone:
+//   renormalised, p_j = s_j / sum of the chosen s
+//     softmax   dl_j = c p_j (D_j - sum_i D_i p_i)
+//     sigmoid   the same times 1 - s_j = sigmoid(-l_j)
+//   as they are, p = s
+//     softmax   dl_i = c p_i (D_i - sum_j D_j p_j) for every expert i (D_i = 0 where not chosen)
+//     sigmoid   dl_j = c D_j s_j (1 - s_j)
+// A token's row is put together in LDS: zeros, the chosen over them, and out in whole lines. Only
+// softmax as it is reads the row of logits; the others read the chosen k alone. Bound by the row
+// written.
+template <int L, int NV>
+__global__ __launch_bounds__(kRouteBlock) void route_grouped_bwd_kernel(
+    moe_grouped_router r, const float* __restrict__ logits, const int32_t* __restrict__ ids,
+    const float* __restrict__ dw, float* __restrict__ dlogits) {
+  constexpr int TPB = kRouteBlock / L, ROW = L * NV;
+  __shared__ float rows[TPB * ROW];
+  const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * TPB + slot;
+  const bool there = t < r.T;
+  const int E = r.E, k = r.k;
+  const int64_t tt = there ? t : 0;
+  const float* l = logits + tt * E;
+  const bool sigmoid = r.score == MOE_SCORE_SIGMOID, act = lane < k;
+  int id = 0;
+  float chosen = -INFINITY, d = 0.f;
+  if (act) {
+    id = ids[tt * k + lane];
+    // ids come from the forward; one out of range (a caller's error) stays in bounds
+    if (id < 0 || id >= E) id = 0;
+    chosen = l[id];
+    d = dw[tt * k + lane];
+  }
+  float* row = rows + slot * ROW;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) row[lane + L * i] = 0.f;
+  const bool full = !sigmoid && !r.renorm;
+  float lg[NV];
+  if (full) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) lg[i] = lane + L * i < E ? l[lane + L * i] : -INFINITY;
+  }
+  __syncthreads();
+  float u = r.scale * d;
+  if (r.renorm) {
+    const float p = renorm_weight<L>(chosen, act, sigmoid, 1.0f);
+    const float mean = lanes_sum<L>(act ? u * p : 0.f);
+    u = p * (u - mean);
+    // a chosen logit of -infinity has the weight 0 and no gradient
+    if (sigmoid) u *= sigmoid_precise(-chosen);
+    if (p == 0.f) u = 0.f;
+  } else if (sigmoid) {
+    u *= sigmoid_precise(chosen) * sigmoid_precise(-chosen);
+  }
+  if (act) row[id] = u;
+  __syncthreads();
+  float out[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) out[i] = row[lane + L * i];
+  if (full) {
+    float m = lg[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) m = fmaxf(m, lg[i]);
+    m = lanes_max<L>(m);
+    if (m == -INFINITY) m = 0.f;
+    float s = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      lg[i] = expf(lg[i] - m);
+      s += lg[i];
+      dot = fmaf(lg[i], out[i], dot);
+    }
+    s = lanes_sum<L>(s);
+    const float inv = s == 0.f ? 0.f : 1.0f / s;
+    dot = lanes_sum<L>(dot) * inv;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) out[i] = lg[i] * inv * (out[i] - dot);
+  }
+  if (there) {
+    float* o = dlogits + t * E;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lane + L * i < E) o[lane + L * i] = out[i];
+  }
+}
+
+// Calls go with the lanes a token takes and the experts a lane holds.
+template <typename F>
+hipError_t by_experts(const moe_grouped_router& r, F&& go) {
+  using std::integral_constant;
+  typedef integral_constant<int, 16> L16;
+  typedef integral_constant<int, 64> L64;
+  // a slot a lane, and a group a lane
+  if (r.E <= 256 && r.k <= 16 && r.groups <= 16) {
+    if (r.E <= 32) return go(L16(), integral_constant<int, 2>());
+    if (r.E <= 64) return go(L16(), integral_constant<int, 4>());
+    if (r.E <= 128) return go(L16(), integral_constant<int, 8>());
+    return go(L16(), integral_constant<int, 16>());
+  }
+  if (r.E <= 256) return go(L64(), integral_constant<int, 4>());
+  return go(L64(), integral_constant<int, 16>());
+}
+
+}  // namespace
+
+hipError_t launch_route_grouped(const moe_grouped_router& r, const float* logits,
+                                const float* bias, int32_t* ids, float* w, hipStream_t s) {
+  return by_experts(r, [&](auto lanes, auto nv) {
+    constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value, TPB = kRouteBlock / L;
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(r.T) + TPB - 1) / TPB));
+    hipLaunchKernelGGL((route_grouped_kernel<L, NV>), grid, dim3(kRouteBlock), 0, s, r, logits,
+                       bias, ids, w);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_route_grouped_bwd(const moe_grouped_router& r, const float* logits,
+                                    const int32_t* ids, const float* dw, float* dlogits,
+                                    hipStream_t s) {
+  return by_experts(r, [&](auto lanes, auto nv) {
+    constexpr int L = decltype(lanes)::value, NV = decltype(nv)::value, TPB = kRouteBlock / L;
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(r.T) + TPB - 1) / TPB));
+    hipLaunchKernelGGL((route_grouped_bwd_kernel<L, NV>), grid, dim3(kRouteBlock), 0, s, r, logits,
+                       ids, dw, dlogits);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace moe
