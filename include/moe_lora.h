@@ -604,6 +604,37 @@ moe_status moe_mx_quantize(int32_t format, int32_t dtype, int64_t rows, int32_t 
 moe_status moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_t cols,
                              const void *codes, const uint8_t *scales, void *dst, void *stream);
 
+/* Products of microscaled operands, the forward of an exported layer's projections:
+ *   z = a w^T                         a E4M3 or E2M1, w E2M1
+ *   y = z, or with swiglu y = silu(z[:, :N]) * z[:, N:]
+ * Products are exact; the matrix cores sum them in float32, in 8 bits with an alignment of each 64
+ * or 128 products that costs a few 1e-6 of the result (so there is no float32 output).
+ *   E = 0   one weight matrix: k = 1, gather = 0, M = T rows; w [Nw, K], Nw = N or with swiglu 2N
+ *   E > 0   one per expert, w [E, Nw, K]: M = T * k rows in expert order, rows
+ *           [offsets[e], offsets[e + 1]) with expert e's weights (moe_permute's offsets); rows
+ *           behind offsets[E] and rows of no expert are left as they were
+ *   gather  nonzero: a holds the T token rows and row i of the products reads a's row rows[i] / k
+ *           (rows [M] = moe_permute's sorted_pair); else a holds the M rows, rows is not read
+ *   out     MOE_BF16 or MOE_F16: y [M, N]; MOE_MX_OUT_FP8: y [M, N] E4M3 codes and y_scales
+ *           [M, moe_mx_scale_cols(N)], quantised from the float32 result (the a of the next product)
+ * a, a_scales, w, w_scales as moe_mx_quantize gives them. ws: moe_mx_linear_workspace_bytes (0: may
+ * be NULL). Results repeat bit for bit. Errors: T, K, N or k < 1, E < 0 or > 1024, k > E or k > 32
+ * with experts, an unknown format or out, T * k >= 2^31, T * k * max(K, N) above 2^34, codes of one
+ * weight matrix, or of a gathered a, of 2 GiB or more, a pointer off a 16-byte boundary (rows, offsets: 4), an output that
+ * overlaps another buffer; MOE_ERR_UNSUPPORTED: K not a multiple of 32, N not a multiple of 8 (of
+ * 32 with MOE_MX_OUT_FP8), K or N above 2^20. */
+enum { MOE_MX_OUT_FP8 = 3 /* beside moe_dtype's values */ };
+typedef struct {
+  int32_t T, K, N, E, k;
+  int32_t a_format; /* moe_mx_format */
+  int32_t gather, swiglu, out;
+} moe_mx_linear_shape;
+moe_status moe_mx_linear_workspace_bytes(const moe_mx_linear_shape *shape, size_t *ws);
+moe_status moe_mx_linear(const moe_mx_linear_shape *shape, const void *a, const uint8_t *a_scales,
+                         const int32_t *rows, const int32_t *offsets, const void *w,
+                         const uint8_t *w_scales, void *y, uint8_t *y_scales, void *ws,
+                         size_t ws_bytes, void *stream);
+
 /* moe_residual_norm_fwd with x' in 8 bits: x_codes [T, H] and x_scales [T,
  * moe_mx_scale_cols(H)] are moe_mx_quantize (E4M3) of the x' that x_out would hold, bit for bit;
  * x_out may be NULL. The backward is moe_residual_norm_bwd. Errors as there, and pre none;

@@ -23,8 +23,8 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import (ACT_IDS, GATE_IDS, MX_IDS, MoeBaseGrads, MoeGrad, MoeGroupedRouter,
-                   MoeLinearShape, MoeLoraGrads, MoeResidual, MoeResidualGrads,
+from ._lib import (ACT_IDS, GATE_IDS, MX_IDS, MX_OUT_IDS, MoeBaseGrads, MoeGrad, MoeGroupedRouter,
+                   MoeLinearShape, MoeLoraGrads, MoeMxLinearShape, MoeResidual, MoeResidualGrads,
                    MoeResidualParams, MoeSaved, MoeShape, MoeWeights, NORM_IDS, ROUTER_IDS,
                    SCORE_IDS, check)
 
@@ -43,6 +43,7 @@ __all__ = [
     "library_path", "GroupedRouter", "moe_route_grouped", "moe_route_grouped_bwd", "GradList",
     "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_grad_clip", "SCORE_IDS", "MX_IDS",
     "mx_scale_cols", "moe_mx_quantize", "moe_mx_dequantize", "moe_residual_norm_mx_fwd",
+    "MXLinear", "moe_mx_linear_workspace_bytes", "moe_mx_linear", "MX_OUT_IDS",
 ]
 
 _TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
@@ -837,6 +838,77 @@ def moe_residual_norm_mx_fwd(desc: Residual, h, y, params, h_out, x_codes, x_sca
             _addr(stats, (desc.T, 4), torch.float32, "stats", True))
     dev = _device(h, y, h_out, x_out, x_codes, x_scales, stats, rng, *(params or {}).values())
     _call(_lib.load().moe_residual_norm_mx_fwd, "moe_residual_norm_mx_fwd", dev, stream, *args)
+
+
+@dataclass(frozen=True)
+class MXLinear:
+    """A product of microscaled operands: y = a w^T, or with act "swiglu" silu of its first N
+    columns times the others. a_format: "fp8" or "fp4"; w is "fp4". E = 0: one w [Nw, K] for T
+    rows (Nw = N, or 2N with swiglu). E > 0: w [E, Nw, K] and T * k rows in expert order; gather:
+    a holds the T token rows. out: "bf16", "f16" or "mx8" (codes and scales as "fp8")."""
+    T: int
+    K: int
+    N: int
+    a_format: str = "fp8"
+    out: str = "bf16"
+    act: str = "none"
+    E: int = 0
+    k: int = 1
+    gather: bool = False
+
+    @property
+    def M(self) -> int:
+        return self.T * self.k
+
+    def c(self) -> MoeMxLinearShape:
+        _sizes(self, "T", "K", "N", "k")
+        if self.act not in ("none", "swiglu"):
+            raise ValueError(f"act must be \"none\" or \"swiglu\", got {self.act!r}")
+        if not 0 <= self.E < 1 << 31:
+            raise ValueError(f"E must be in [0, 2^31), got {self.E}")
+        return MoeMxLinearShape(self.T, self.K, self.N, self.E, self.k, MX_IDS[self.a_format],
+                                int(self.gather), int(self.act == "swiglu"), MX_OUT_IDS[self.out])
+
+    @functools.cached_property
+    def _c(self) -> MoeMxLinearShape:
+        return self.c()
+
+    @functools.cached_property
+    def _shapes(self) -> tuple:
+        """Shapes of a, a_scales, w, w_scales, y, y_scales."""
+        rows, half = self.T if self.gather else self.M, self.K // 2
+        n_w, e = self.N * (2 if self.act == "swiglu" else 1), (self.E,) if self.E else ()
+        return ((rows, half if self.a_format == "fp4" else self.K), (rows, mx_scale_cols(self.K)),
+                (*e, n_w, half), (*e, n_w, mx_scale_cols(self.K)), (self.M, self.N),
+                (self.M, mx_scale_cols(self.N)))
+
+    @functools.cached_property
+    def _ws(self) -> int:
+        n = ctypes.c_size_t()
+        check(_lib.load().moe_mx_linear_workspace_bytes(ctypes.byref(self._c), ctypes.byref(n)),
+              "moe_mx_linear_workspace_bytes")
+        return n.value
+
+
+def moe_mx_linear_workspace_bytes(shape: MXLinear) -> int:
+    return shape._ws
+
+
+def moe_mx_linear(shape: MXLinear, a, a_scales, w, w_scales, y, ws=None, y_scales=None, rows=None,
+                  offsets=None, stream=None):
+    """y from codes a, w and their scales (moe_mx_quantize's). rows: moe_permute's sorted_pair, with
+    gather; offsets: its offsets, with experts; y_scales: with out "mx8" (y then holds codes)."""
+    wsp, wsb = _ws(ws, shape._ws, "ws")
+    sa, ssa, sw, ssw, sy, ssy = shape._shapes
+    u8, mx = torch.uint8, shape.out == "mx8"
+    args = (ctypes.byref(shape._c), _addr(a, sa, u8, "a"), _addr(a_scales, ssa, u8, "a_scales"),
+            _addr(rows, (shape.M,), torch.int32, "rows") if shape.gather else None,
+            _addr(offsets, (shape.E + 1,), torch.int32, "offsets") if shape.E else None,
+            _addr(w, sw, u8, "w"), _addr(w_scales, ssw, u8, "w_scales"),
+            _addr(y, sy, u8 if mx else _TORCH_DTYPES[shape.out], "y"),
+            _addr(y_scales, ssy, u8, "y_scales", not mx), wsp, wsb)
+    dev = _device(a, a_scales, w, w_scales, y, y_scales, rows, offsets, ws)
+    _call(_lib.load().moe_mx_linear, "moe_mx_linear", dev, stream, *args)
 
 
 class kernel_timer:

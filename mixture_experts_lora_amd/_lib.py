@@ -22,6 +22,7 @@ NORM_IDS = {"none": 0, "rms": 1, "layer": 2}
 ACT_IDS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 SCORE_IDS = {"softmax": 0, "sigmoid": 1}
 MX_IDS = {"fp8": 0, "fp4": 1}
+MX_OUT_IDS = {"bf16": MOE_BF16, "f16": MOE_F16, "mx8": 3}
 GATE_IDS = {"none": 0, "channel": 1, "token": 2, "full": 3}
 
 EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
@@ -37,6 +38,7 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_bwd", "moe_permute",
            "moe_linear_bwd", "moe_route_grouped", "moe_route_grouped_bwd",
            "moe_grad_norm_workspace_bytes", "moe_grad_norm", "moe_grad_clip", "moe_mx_scale_cols",
            "moe_mx_quantize", "moe_mx_dequantize", "moe_residual_norm_mx_fwd",
+           "moe_mx_linear_workspace_bytes", "moe_mx_linear",
            "moe_status_str",
            "moe_last_error",
            "moe_kernel_timer_enable", "moe_kernel_timer_select", "moe_kernel_timer_reset",
@@ -87,6 +89,11 @@ class MoeLinearShape(ctypes.Structure):
 class MoeGroupedRouter(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "score", "groups", "topk_groups",
                                               "group_top", "renorm")] + [("scale", ctypes.c_float)]
+
+
+class MoeMxLinearShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "E", "k", "a_format", "gather",
+                                              "swiglu", "out")]
 
 
 class MoeGrad(ctypes.Structure):
@@ -196,6 +203,10 @@ def load() -> ctypes.CDLL:
         "moe_residual_norm_mx_fwd": (st, [ctypes.POINTER(MoeResidual), P, P,
                                           ctypes.POINTER(MoeResidualParams), P, ctypes.c_int64, P,
                                           P, P, P, P, P]),
+        "moe_mx_linear_workspace_bytes": (st, [ctypes.POINTER(MoeMxLinearShape),
+                                               ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_mx_linear": (st, [ctypes.POINTER(MoeMxLinearShape), P, P, P, P, P, P, P, P, P,
+                               ctypes.c_size_t, P]),
         "moe_status_str": (ctypes.c_char_p, [st]),
         "moe_last_error": (ctypes.c_char_p, []),
         "moe_kernel_timer_enable": (st, [I32]),

@@ -24,6 +24,21 @@ def scale_cols(cols):
     return 16 * -(-cols // 512)
 
 
+def nearest(q, fmt):
+    """Codes of the values nearest to q >= 0, ties to the even code, at most the largest."""
+    t = TABLE[fmt]
+    hi = np.clip(np.searchsorted(t, q), 0, len(t) - 1)  # first value >= q
+    lo = np.maximum(hi - 1, 0)
+    a, c = q - t[lo], t[hi] - q
+    code = np.where(a < c, lo, np.where(a > c, hi, np.where(lo % 2 == 0, lo, hi)))
+    return np.where(q >= t[-1], len(t) - 1, code)
+
+
+def rounded(q, fmt):
+    """q (any sign) rounded to the format's values."""
+    return np.copysign(TABLE[fmt][nearest(np.abs(q), fmt)], q)
+
+
 def quantize(x, fmt):
     """(codes as one number an element, scales [rows, scale_cols]) of rows x [rows, cols]."""
     x = np.asarray(x, np.float64)
@@ -36,12 +51,7 @@ def quantize(x, fmt):
     e = np.where(amax > 0, np.frexp(amax)[1] - 1 + 127 - TOP[fmt], 0)
     s = np.maximum(e, 0)
     q = np.where(bad[..., None], 0.0, b) * np.exp2(127.0 - s)[..., None]
-    t = TABLE[fmt]
-    hi = np.clip(np.searchsorted(t, np.abs(q)), 0, len(t) - 1)  # first value >= |q|
-    lo = np.maximum(hi - 1, 0)
-    a, c = np.abs(q) - t[lo], t[hi] - np.abs(q)
-    code = np.where(a < c, lo, np.where(a > c, hi, np.where(lo % 2 == 0, lo, hi)))
-    code = np.where(np.abs(q) >= t[-1], len(t) - 1, code)
+    code = nearest(np.abs(q), fmt)
     sign = np.signbit(q) << (3 if fmt == "fp4" else 7)
     scales = np.zeros((rows, scale_cols(cols)), np.uint8)
     scales[:, :cols // 32] = np.where(bad, 255, s)
