@@ -31,8 +31,11 @@ constexpr int kMaxGroups = 64;
 template <int CTRL>
 __device__ __forceinline__ double dpp_f64(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = dpp_i32<CTRL>(static_cast<int>(static_cast<uint32_t>(b)));
-  const uint32_t hi = dpp_i32<CTRL>(static_cast<int>(static_cast<uint32_t>(b >> 32)));
+  // every lane of the row is active: nothing else is left in the result
+  const uint32_t lo = __builtin_amdgcn_mov_dpp(static_cast<int>(static_cast<uint32_t>(b)), CTRL, 0xF,
+                                               0xF, false);
+  const uint32_t hi = __builtin_amdgcn_mov_dpp(static_cast<int>(static_cast<uint32_t>(b >> 32)), CTRL,
+                                               0xF, 0xF, false);
   return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
 __device__ __forceinline__ double readlane_f64(double v, int lane) {
@@ -40,6 +43,18 @@ __device__ __forceinline__ double readlane_f64(double v, int lane) {
   const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(b)), lane);
   const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(b >> 32)), lane);
   return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+// Largest and smallest of two numbers of which neither is NaN (the builtins would put both operands
+// through an instruction of its own that quiets NaNs).
+__device__ __forceinline__ double max_f64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min_f64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
 }
 template <int L, typename T, typename Op>
 __device__ __forceinline__ T lanes_reduce(T v, Op op) {
@@ -63,7 +78,7 @@ __device__ __forceinline__ T lanes_reduce(T v, Op op) {
 template <int L, typename T>
 __device__ __forceinline__ T lanes_max(T v) {
   return lanes_reduce<L>(v, [](T a, T b) __attribute__((always_inline)) {
-    if constexpr (sizeof(T) == 8) return __builtin_fmax(a, b);
+    if constexpr (sizeof(T) == 8) return max_f64(a, b);
     else return fmaxf(a, b);
   });
 }
@@ -85,6 +100,31 @@ __device__ __forceinline__ double route_key(double v, int idx) {
 }
 __device__ __forceinline__ int key_index(double key) {
   return 1023 - static_cast<int>(__builtin_bit_cast(uint64_t, key) & 1023);
+}
+
+// e^x to 2^-45 for |x| <= 708, larger |x| taken as 708 (e^-708 is 0 beside any other score): x is cut
+// at a multiple of ln 2, taken off in two parts, and the rest (at most ln 2 / 2) goes
+// through the Taylor polynomial of degree 12, whose next term is below 2^-52. Equal arguments give
+// equal values, so ties stay ties.
+__device__ __forceinline__ double route_exp(double x) {
+  x = __builtin_fmin(__builtin_fmax(x, -708.0), 708.0);
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  // ln 2 to 20 bits, so that n times it is exact, and what is left of ln 2
+  double r = __builtin_fma(n, -0.693145751953125, x);
+  r = __builtin_fma(n, -1.4286068203094172321e-06, r);
+  constexpr double c[] = {1.0 / 479001600, 1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320,
+                          1.0 / 5040,      1.0 / 720,      1.0 / 120,     1.0 / 24,     1.0 / 6,
+                          0.5,             1.0,            1.0};
+  double y = c[0];
+#pragma unroll
+  for (int i = 1; i < 13; ++i) y = __builtin_fma(y, r, c[i]);
+  return __builtin_ldexp(y, static_cast<int>(n));
+}
+// 1 / x for x in [1, 2^1023): the hardware's estimate and two steps of Newton's method.
+__device__ __forceinline__ double route_rcp(double x) {
+  double y = __builtin_amdgcn_rcp(x);
+  y = __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
+  return __builtin_fma(__builtin_fma(-x, y, 1.0), y, y);
 }
 
 // ---- weights of the chosen. Lane j < k of a token holds slot j's logit l; the others hold
@@ -116,7 +156,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
   constexpr int TPB = kRouteBlock / L;  // tokens a block
   // a token's values with a gap after each group, so that the lanes that scan the groups of a token
   // do not meet in a bank
-  constexpr int ROW = L * NV + kMaxGroups;
+  constexpr int ROW = L * NV + kMaxGroups + 1;  // the last place is written and not read
   __shared__ double vals[TPB * ROW];
   __shared__ double gscore[TPB * (L == 16 ? 16 : kMaxGroups)];
   const int lane = threadIdx.x % L, slot = threadIdx.x / L;
@@ -129,7 +169,8 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = lane + L * i;
-    lg[i] = e < E ? l[e] : -INFINITY;
+    lg[i] = l[min(e, E - 1)];  // loads without branches; what lies past the row is put aside
+    if (e >= E) lg[i] = -INFINITY;
     mx = fmaxf(mx, lg[i]);
   }
   mx = lanes_max<L>(mx);
@@ -140,27 +181,36 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = static_cast<double>(lg[i]);
   } else {
-    // a row of -infinity: every score 0
+    // sigmoid(l) = 1 / (1 + e^-l); softmax from l - max. -infinity scores 0 (as every expert of a
+    // row of nothing else), NaN stays NaN.
     const double shift = sigmoid || mx == -INFINITY ? 0.0 : static_cast<double>(mx);
+    const double sign = sigmoid ? -1.0 : 1.0, one = sigmoid ? 1.0 : 0.0;
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const double x = static_cast<double>(lg[i]) - shift;
-      v[i] = exp(sigmoid ? -x : x);
-      if (sigmoid) v[i] = 1.0 / (1.0 + v[i]);
-      else sum += v[i];  // exp(-infinity) past the row
+      v[i] = one + route_exp((static_cast<double>(lg[i]) - shift) * sign);
+      if (lg[i] == -INFINITY && !sigmoid) v[i] = 0.0;
+      sum += v[i];
     }
-    if (!sigmoid) {
+    if (sigmoid) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        v[i] = route_rcp(v[i]);
+        if (lg[i] == -INFINITY) v[i] = 0.0;
+      }
+    } else {
       sum = lanes_sum<L>(sum);
-      const double inv = sum > 0.0 ? 1.0 / sum : (sum == 0.0 ? 0.0 : sum);
+      const double inv = sum > 0.0 ? route_rcp(sum) : 0.0;  // sum >= 1 or 0
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] *= inv;
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lg[i] != lg[i]) v[i] = static_cast<double>(lg[i]);
     if (bias) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = lane + L * i;
-        if (e < E) v[i] += static_cast<double>(bias[e]);
+        v[i] += static_cast<double>(bias[min(lane + L * i, E - 1)]);
       }
     }
   }
@@ -168,61 +218,82 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = lane + L * i;
-    key[i] = e < E ? route_key(v[i], e) : 0.0;
+    key[i] = route_key(v[i], e);
+    if (e >= E) key[i] = 0.0;
   }
   if (r.groups > 1) {
     const int gs = E / r.groups;
+    const float inv_gs = 1.0f / static_cast<float>(gs);
+    // e / gs: half an expert keeps the product off the borders by far more than its rounding
+    auto group_of = [&](int e) __attribute__((always_inline)) {
+      return static_cast<int>((static_cast<float>(e) + 0.5f) * inv_gs);
+    };
     double* row = vals + slot * ROW;
     double* sc = gscore + slot * (L == 16 ? 16 : kMaxGroups);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + L * i;
-      if (e < E) row[e + e / gs] = v[i];
+      row[e < E ? e + group_of(e) : ROW - 1] = v[i];
     }
     __syncthreads();
-    double mine = -INFINITY;
-    if (lane < r.groups) {
-      const double* g = row + lane * (gs + 1);
-      double a = -INFINITY, b = -INFINITY;  // the largest and the second
-      for (int i = 0; i < gs; ++i) {
+    // a group's experts are looked through by S lanes (1, 2, 4 or 8), which then merge their two best
+    const int S = r.groups * 8 <= L ? 8 : r.groups * 4 <= L ? 4 : r.groups * 2 <= L ? 2 : 1;
+    const int group = lane / S;
+    double a = -INFINITY, b = -INFINITY;  // the largest and the second
+    if (group < r.groups) {
+      const double* g = row + group * (gs + 1);
+#pragma unroll 4
+      for (int i = lane & (S - 1); i < gs; i += S) {
         const double x = g[i] != g[i] ? -INFINITY : g[i];
-        b = __builtin_fmax(b, __builtin_fmin(a, x));
-        a = __builtin_fmax(a, x);
+        b = max_f64(b, min_f64(a, x));
+        a = max_f64(a, x);
       }
-      mine = r.group_top == 2 && gs > 1 ? a + b : a;
-      if (mine != mine) mine = -INFINITY;
-      sc[lane] = mine;
     }
+    auto merge = [&](double oa, double ob) __attribute__((always_inline)) {
+      b = max_f64(min_f64(a, oa), max_f64(b, ob));
+      a = max_f64(a, oa);
+    };
+    if (S >= 2) merge(dpp_f64<kDppSwap1>(a), dpp_f64<kDppSwap1>(b));
+    if (S >= 4) merge(dpp_f64<kDppSwap2>(a), dpp_f64<kDppSwap2>(b));
+    if (S >= 8) merge(dpp_f64<kDppHalfMirror>(a), dpp_f64<kDppHalfMirror>(b));
+    double mine = r.group_top == 2 && gs > 1 ? a + b : a;
+    if (mine != mine) mine = -INFINITY;
+    const bool head = group < r.groups && (lane & (S - 1)) == 0;
+    if (head) sc[group] = mine;
     __syncthreads();
-    bool keep = false;
-    if (lane < r.groups) {
-      int rank = 0;
-      for (int h = 0; h < r.groups; ++h) {
-        const double o = sc[h];
-        rank += o > mine || (o == mine && h < lane);
-      }
-      keep = rank < r.topk_groups;
+    int rank = 0;
+#pragma unroll 8
+    for (int h = 0; h < r.groups; ++h) {
+      const double o = sc[h];
+      rank += o > mine || (o == mine && h < group);
     }
-    // bit g of this token's lanes: group g stays
-    uint64_t kept = __ballot(keep);
-    if (L < 64) kept = (kept >> (threadIdx.x % kWave / L * L)) & ((uint64_t{1} << (L & 63)) - 1);
+    // bit g S of this token's lanes: group g stays
+    uint64_t kept = __ballot(head && rank < r.topk_groups);
+    if (L < 64) kept >>= threadIdx.x % kWave / L * L;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + L * i;
-      if (e < E && !((kept >> (e / gs)) & 1)) key[i] = 0.0;
+      if (!((kept >> (group_of(min(e, E - 1)) * S)) & 1)) key[i] = 0.0;
     }
   }
   int id = 0;
   for (int j = 0; j < r.k; ++j) {
-    double best = key[0];
+    double m[NV];
 #pragma unroll
-    for (int i = 1; i < NV; ++i) best = __builtin_fmax(best, key[i]);
-    best = lanes_max<L>(best);
-    const int idx = key_index(best);
+    for (int i = 0; i < NV; ++i) m[i] = key[i];
+#pragma unroll
+    for (int n = NV; n > 1; n >>= 1)
+#pragma unroll
+      for (int i = 0; i < n / 2; ++i) m[i] = max_f64(m[i], m[i + n / 2]);
+    const int idx = key_index(lanes_max<L>(m[0]));
     if (lane == j) id = idx;
+    // taken: without its upper half a key is below every other
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (idx == lane + L * i) key[i] = 0.0;
+    for (int i = 0; i < NV; ++i) {
+      uint64_t b = __builtin_bit_cast(uint64_t, key[i]);
+      if (idx == lane + L * i) b &= 0xffffffffu;
+      key[i] = __builtin_bit_cast(double, b);
+    }
   }
   const bool act = lane < r.k;
   const float chosen = act ? l[id] : -INFINITY;
@@ -284,7 +355,10 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_bwd_kernel(
   float lg[NV];
   if (full) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) lg[i] = lane + L * i < E ? l[lane + L * i] : -INFINITY;
+    for (int i = 0; i < NV; ++i) {
+      lg[i] = l[min(lane + L * i, E - 1)];
+      if (lane + L * i >= E) lg[i] = -INFINITY;
+    }
   }
   __syncthreads();
   float u = r.scale * d;
@@ -336,13 +410,16 @@ hipError_t by_experts(const moe_grouped_router& r, F&& go) {
   using std::integral_constant;
   typedef integral_constant<int, 16> L16;
   typedef integral_constant<int, 64> L64;
-  // a slot a lane, and a group a lane
-  if (r.E <= 256 && r.k <= 16 && r.groups <= 16) {
+  // 16 lanes hold up to 16 slots and 16 groups. Up to 4096 tokens leave lanes idle either way, and a
+  // token's chain of steps is shorter with a wave of its own (256 experts in 8 groups, 2048 tokens:
+  // 7.0 us against 8.7 with 16 lanes; 4096: 9.0 against 8.9; 8192: 15.2 against 12.1).
+  if (r.E <= 256 && r.k <= 16 && r.groups <= 16 && r.T > 4096) {
     if (r.E <= 32) return go(L16(), integral_constant<int, 2>());
     if (r.E <= 64) return go(L16(), integral_constant<int, 4>());
     if (r.E <= 128) return go(L16(), integral_constant<int, 8>());
     return go(L16(), integral_constant<int, 16>());
   }
+  if (r.E <= 64) return go(L64(), integral_constant<int, 1>());
   if (r.E <= 256) return go(L64(), integral_constant<int, 4>());
   return go(L64(), integral_constant<int, 16>());
 }
