@@ -698,11 +698,20 @@ class GroupedRouter:
         return (self.E, self.k, SCORE_IDS[self.score], self.groups, self.topk_groups,
                 self.group_top, int(self.renorm), float(self.scale))
 
+    @functools.cached_property
+    def _by_T(self) -> dict:
+        return {}
+
     def c(self, T: int) -> MoeGroupedRouter:
-        _sizes(self, "E", "k", "groups", "topk_groups", "group_top")
-        if not 0 < T < 1 << 31:
-            raise ValueError(f"T must be in [1, 2^31), got {T}")
-        return MoeGroupedRouter(T, *self._c)
+        got = self._by_T.get(T)
+        if got is None:
+            _sizes(self, "E", "k", "groups", "topk_groups", "group_top")
+            if not 0 < T < 1 << 31:
+                raise ValueError(f"T must be in [1, 2^31), got {T}")
+            if len(self._by_T) >= 64:  # token counts that vary are not kept for good
+                self._by_T.clear()
+            got = self._by_T[T] = MoeGroupedRouter(T, *self._c)
+        return got
 
 
 def moe_route_grouped(router: GroupedRouter, logits, topk_ids, topk_w, bias=None, stream=None):
@@ -788,25 +797,24 @@ def mx_scale_cols(cols: int) -> int:
     return 16 * ((cols + 511) // 512)
 
 
-def _mx_rows(t, name):
-    """(leading shape, rows, cols) of a tensor [.., cols] of microscaled rows."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() < 1:
-        raise ValueError(f"{name} must have at least one dimension")
-    lead, cols = t.shape[:-1], t.shape[-1]
+@functools.lru_cache(maxsize=256)
+def _mx_shapes(shape, fmt: str):
+    """(rows, cols), and the shapes of codes and scales, of microscaled rows of `shape`."""
+    if len(shape) < 1:
+        raise ValueError("microscaled rows need at least one dimension")
+    lead, cols = shape[:-1], shape[-1]
     if cols >= 1 << 31:
-        raise ValueError(f"{name}: rows of {cols} elements")
-    return lead, lead.numel(), cols
+        raise ValueError(f"rows of {cols} elements")
+    return (lead.numel(), cols), (*lead, cols // 2 if fmt == "fp4" else cols), \
+        (*lead, mx_scale_cols(cols))
 
 
 def _mx_args(x, codes, scales, fmt, name):
     key, dt = _dtype_of(x, name)
-    lead, rows, cols = _mx_rows(x, name)
+    rows, cs, ss = _mx_shapes(x.shape, fmt)
     u8 = torch.uint8
-    return (MX_IDS[fmt], _ABI_DTYPES[key], rows, cols), _addr(x, x.shape, dt, name), \
-        _addr(codes, (*lead, cols // 2 if fmt == "fp4" else cols), u8, "codes"), \
-        _addr(scales, (*lead, mx_scale_cols(cols)), u8, "scales")
+    return (MX_IDS[fmt], _ABI_DTYPES[key], *rows), _addr(x, x.shape, dt, name), \
+        _addr(codes, cs, u8, "codes"), _addr(scales, ss, u8, "scales")
 
 
 def moe_mx_quantize(src, codes, scales, fmt="fp4", stream=None):

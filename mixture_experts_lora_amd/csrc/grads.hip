@@ -20,6 +20,9 @@ namespace {
 constexpr int kGradTensors = 80;
 constexpr int kGradPiece = 16384;
 constexpr int kGradBlock = 256;
+// Up to so many elements one block of kGradOne threads sums and roots in a single launch.
+constexpr int kGradOne = 1024;
+constexpr int64_t kGradOneMost = 131072;
 constexpr int kGradBlocks = 2048;  // most partials a launch leaves
 
 struct GradTable {
@@ -45,7 +48,7 @@ __device__ __forceinline__ void for_pieces(const GradTable& t, F&& go) {
   }
 }
 
-template <typename Elem>
+template <int BLOCK, typename Elem>
 __device__ __forceinline__ double squares(const Elem* g, int n, bool vec) {
   double s[2] = {0.0, 0.0};
   auto add = [&](int j, float x) __attribute__((always_inline)) {
@@ -55,7 +58,7 @@ __device__ __forceinline__ double squares(const Elem* g, int n, bool vec) {
   int done = 0;
   if (vec) {
     done = n & ~7;
-    constexpr int STEP = kGradBlock * 8;
+    constexpr int STEP = BLOCK * 8;
     int i = threadIdx.x * 8;
     for (; i + 3 * STEP < done; i += 4 * STEP) {
       Row8<Elem> r[4];
@@ -78,36 +81,39 @@ __device__ __forceinline__ double squares(const Elem* g, int n, bool vec) {
       for (int j = 0; j < 8; ++j) add(j, v[j]);
     }
   }
-  for (int i = done + threadIdx.x; i < n; i += kGradBlock) add(0, to_f32<Elem>(g[i]));
+  for (int i = done + threadIdx.x; i < n; i += BLOCK) add(0, to_f32<Elem>(g[i]));
   return s[0] + s[1];
 }
 
 // The block's sum, in thread 0: lanes by halves, then the waves in order.
+template <int BLOCK>
 __device__ __forceinline__ double block_sum(double s) {
-  __shared__ double part[kGradBlock / kWave];
+  __shared__ double part[BLOCK / kWave];
 #pragma unroll
   for (int d = kWave / 2; d > 0; d >>= 1) s += __shfl_xor(s, d, kWave);
   if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = s;
   __syncthreads();
   s = part[0];
 #pragma unroll
-  for (int w = 1; w < kGradBlock / kWave; ++w) s += part[w];
+  for (int w = 1; w < BLOCK / kWave; ++w) s += part[w];
   return s;
 }
 
 template <bool ONE>
-__global__ __launch_bounds__(kGradBlock) void grad_squares_kernel(GradTable t, double* part,
-                                                                  float* norm) {
+__global__ __launch_bounds__(ONE ? kGradOne : kGradBlock) void grad_squares_kernel(GradTable t,
+                                                                                   double* part,
+                                                                                   float* norm) {
+  constexpr int BLOCK = ONE ? kGradOne : kGradBlock;
   double s = 0.0;
   for_pieces(t, [&](int i, int64_t at, int n) __attribute__((always_inline)) {
     if (t.dtype[i] == MOE_F32)
-      s += squares(static_cast<const float*>(t.src[i]) + at, n, t.vec[i]);
+      s += squares<BLOCK>(static_cast<const float*>(t.src[i]) + at, n, t.vec[i]);
     else if (t.dtype[i] == MOE_BF16)
-      s += squares(static_cast<const bf16_t*>(t.src[i]) + at, n, t.vec[i]);
+      s += squares<BLOCK>(static_cast<const bf16_t*>(t.src[i]) + at, n, t.vec[i]);
     else
-      s += squares(static_cast<const f16_t*>(t.src[i]) + at, n, t.vec[i]);
+      s += squares<BLOCK>(static_cast<const f16_t*>(t.src[i]) + at, n, t.vec[i]);
   });
-  s = block_sum(s);
+  s = block_sum<BLOCK>(s);
   if (threadIdx.x == 0) {
     if (ONE) *norm = static_cast<float>(sqrt(s));
     else part[blockIdx.x] = s;
@@ -118,7 +124,7 @@ __global__ __launch_bounds__(kGradBlock) void grad_norm_kernel(const double* par
                                                                float* norm) {
   double s = 0.0;
   for (int i = threadIdx.x; i < n; i += kGradBlock) s += part[i];
-  s = block_sum(s);
+  s = block_sum<kGradBlock>(s);
   if (threadIdx.x == 0) *norm = static_cast<float>(sqrt(s));
 }
 
@@ -185,39 +191,54 @@ int64_t blocks_of(const GradTable& t) {
   return std::min<int64_t>(t.first[t.count], kGradBlocks);
 }
 
+// Whether one block sums the whole list: it fits a launch, and adding partials up would cost more.
+bool one_block(int count, const moe_grad* grads) {
+  int64_t n = 0;
+  int tensors = 0;
+  for (int i = 0; i < count; ++i) {
+    n += grads[i].n;
+    tensors += grads[i].n > 0;
+    if (n > kGradOneMost || tensors > kGradTensors) return false;
+  }
+  return tensors > 0;
+}
+
 }  // namespace
 
 size_t grad_norm_ws_bytes(int count, const moe_grad* grads) {
+  if (one_block(count, grads)) return 0;
   int64_t parts = 0;
   for (int at = 0; at < count;) {
     GradTable t;
     at += fill_table(grads + at, count - at, &t);
     parts += blocks_of(t);
   }
-  return parts <= 1 ? 0 : static_cast<size_t>(parts) * sizeof(double);
+  return static_cast<size_t>(parts) * sizeof(double);
 }
 
 hipError_t launch_grad_norm(int count, const moe_grad* grads, float* norm, void* ws, hipStream_t s,
                             KernelTimer* tm) {
   TimedScope ts(tm, MOE_K_GRAD_NORM, s);
-  // a single piece in all: its block has the sum
-  const bool one = grad_norm_ws_bytes(count, grads) == 0;
   double* part = static_cast<double*>(ws);
+  if (one_block(count, grads)) {
+    GradTable t;
+    fill_table(grads, count, &t);
+    hipLaunchKernelGGL(grad_squares_kernel<true>, dim3(1), dim3(kGradOne), 0, s, t, part, norm);
+    return hipGetLastError();
+  }
   int64_t parts = 0;
   for (int at = 0; at < count;) {
     GradTable t;
     at += fill_table(grads + at, count - at, &t);
     const int64_t blocks = blocks_of(t);
     if (blocks == 0) continue;
-    auto* kern = one ? grad_squares_kernel<true> : grad_squares_kernel<false>;
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(blocks)), dim3(kGradBlock), 0, s, t,
-                       part + parts, norm);
+    hipLaunchKernelGGL(grad_squares_kernel<false>, dim3(static_cast<unsigned>(blocks)),
+                       dim3(kGradBlock), 0, s, t, part + parts, norm);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     parts += blocks;
   }
-  if (one && parts == 1) return hipSuccess;
-  // no elements at all: the sum of no partials
+  // (of no elements at all: the sum of no partials)
   hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(kGradBlock), 0, s, part,
                      static_cast<int>(parts), norm);
   return hipGetLastError();
