@@ -30,6 +30,9 @@ CFLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     f"-I{os.path.join(PKG, os.pardir, 'include')}",
 ]
+# accumulators stay in vector registers where a block's LDS leaves one block a CU: in accumulation
+# registers they would be copied out and back around every statement that holds a product in place
+FILE_CFLAGS = {"mx_linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def _run(cmd, verbose):
@@ -50,7 +53,8 @@ def build(verbose: bool = False) -> str:
     objs = [os.path.join(BUILD, os.path.basename(s)[:-4] + ".o") for s in srcs]
     jobs = min(len(srcs), max(1, min(16, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(jobs) as ex:
-        futs = [ex.submit(_run, [HIPCC, *CFLAGS, "-c", s, "-o", o], verbose)
+        futs = [ex.submit(_run, [HIPCC, *CFLAGS, *FILE_CFLAGS.get(os.path.basename(s), ()),
+                                "-c", s, "-o", o], verbose)
                 for s, o in zip(srcs, objs)]
         for f in futs:
             f.result()

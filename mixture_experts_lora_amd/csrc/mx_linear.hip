@@ -120,186 +120,231 @@ __device__ __forceinline__ constexpr int row_bytes_of(int k) {
 }
 
 // ------------------------------------------------------------------ many rows: tiles through LDS
-// LDS rows hold 128 elements, 16-byte chunk c of row r at c ^ swizzle(r), so that 16 lanes of a
-// fragment read (16 rows, one chunk) touch every bank once.
-template <int RB>  // bytes a row: 128 or 64
+// A stage is 128 elements of every row; NST stages have places in LDS. 16-byte chunk c of row r is
+// kept at c ^ swizzle(r), so that 16 lanes of a fragment read (16 rows, one chunk) touch every bank
+// once.
+template <int RB>  // bytes a row: 128 (8 bits) or 64 (4 bits)
 __device__ __forceinline__ int mx_swz(int r) {
   return RB == 128 ? (r >> 1) & 7 : (r >> 2) & 3;
 }
 
-// Rows of one operand's tile as DMA instructions of 1 KB: the lane's source offset, without the
-// stage's.
-template <int RB, int N>
-struct MxFill {
-  uint32_t vo[N];
-};
-
+// Row and byte within the stage that lane `lane` of an operand's 1 KB DMA instruction j brings.
 template <int RB>
 __device__ __forceinline__ int fill_row(int j, int lane) { return j * (1024 / RB) + lane / (RB / 16); }
 template <int RB>
-__device__ __forceinline__ int fill_chunk(int j, int lane) {
-  return (lane % (RB / 16)) ^ mx_swz<RB>(fill_row<RB>(j, lane));
+__device__ __forceinline__ int fill_byte(int j, int lane) {
+  return ((lane % (RB / 16)) ^ mx_swz<RB>(fill_row<RB>(j, lane))) * 16;
+}
+
+// The instruction's operand: 16 bytes of 4-bit codes (the upper half is not read), or 32 of 8-bit.
+__device__ __forceinline__ i32x8 mx_operand(const i32x4& lo, const i32x4& hi, bool fp4) {
+  return fp4 ? __builtin_shufflevector(lo, lo, 0, 1, 2, 3, -1, -1, -1, -1)
+             : __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// 16 bytes per lane, global -> LDS at byte `lds` of the block's memory (dma16 of gemm16.h, whose
+// generic pointers cost a check for null each); rs and soff are uniform.
+__device__ __forceinline__ void dma16_at(uint32_t lds, const u32x4& rs, uint32_t vo, uint32_t soff) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds);
+  u32x4 srs;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) srs[i] = __builtin_amdgcn_readfirstlane(rs[i]);
+  const uint32_t ssoff = __builtin_amdgcn_readfirstlane(soff);
+  asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"{m0}"(m0), "v"(vo),
+               "s"(srs), "s"(ssoff)
+               : "memory");
 }
 
 // Columns of the output that a block of BN weight rows gives.
 template <int BN, bool SWIGLU>
 constexpr int out_cols() { return SWIGLU ? BN / 2 : BN; }
 
-template <int AF, int OUT, bool SWIGLU, int BM, int BN, int WM, int WN, int MINB>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void mx_gemm_kernel(MxGemm p) {
+template <int AF, int OUT, bool SWIGLU, int BM, int BN, int WM, int WN, int NST>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
+    __attribute__((amdgpu_waves_per_eu(2, 2))) void mx_gemm_kernel(MxGemm p) {
   constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
   constexpr int MF = WM / 32, NF = WN / 32;
   constexpr int AB = row_bytes_of<AF>(128), WB = 64;
   constexpr int A_BYTES = BM * AB, W_BYTES = BN * WB, STAGE = A_BYTES + W_BYTES;
-  constexpr int S_BYTES = (BM + BN) * 16;  // scales of 512 elements
+  constexpr int S_BYTES = (BM + BN) * 16;  // scales of 512 elements, in two places
   constexpr int AI = A_BYTES / 1024 / NW, WI = W_BYTES / 1024 / NW;
   static_assert(AI * NW * 1024 == A_BYTES && WI * NW * 1024 == W_BYTES, "whole instructions a wave");
-  static_assert((BM + BN) % 64 == 0 && BM % 64 == 0, "whole scale instructions");
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE + 2 * S_BYTES];
-  char* const sscale = smem + 2 * STAGE;
+  static_assert(NW * (1024 / AB) % 16 == 0 && NW * (1024 / WB) % 16 == 0,
+                "whole swizzle periods between a wave's instructions");
+  static_assert(BN % 64 == 0 && BM % 64 == 0, "whole scale instructions");
+  static_assert(NST >= 2 && NST <= 4, "scales: one place is read, the other filled");
+  constexpr int S_AT = NST * STAGE;
+  __shared__ __attribute__((aligned(1024))) char smem[S_AT + 2 * S_BYTES];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   MxTile t;
   if (!find_tile<BM, true>(p, blockIdx.x, t)) return;
-  const int n0 = t.n * out_cols<BN, SWIGLU>();
+
   const int n_w = SWIGLU ? 2 * p.N : p.N;
   const int a_row = row_bytes_of<AF>(p.K), w_row = p.K / 2;
   const int sc = static_cast<int>(mx_scale_cols(p.K));
+  const int stages = (p.K + 127) / 128;
 
-  // Weight row of the tile's row r. SwiGLU: each wave's rows are half gate, half up.
-  auto weight_row = [&](int r, bool& ok) __attribute__((always_inline)) {
-    if (!SWIGLU) {
-      ok = n0 + r < p.N;
-      return n0 + r;
-    }
-    const int w = r / WN, in = r % WN, f = n0 + w * (WN / 2) + in % (WN / 2);
-    ok = f < p.N;
-    return in < WN / 2 ? f : p.N + f;
+  // Weight row of a tile's row r, from the tile's first on. SwiGLU: each wave's rows are half gate,
+  // half up. A row past the last reads zeros (past the matrix) or a row whose column is not stored.
+  auto weight_row = [&](int r) __attribute__((always_inline)) {
+    if (!SWIGLU) return r;
+    const int in = r % WN;
+    return r / WN * (WN / 2) + in % (WN / 2) + (in < WN / 2 ? 0 : p.N);
   };
-  // Row of a: gathered rows as they are in a, the others from the tile's first on.
-  const int64_t a_first = p.rows ? 0 : t.row0;
-  auto act_row = [&](int r, bool& ok) __attribute__((always_inline)) {
-    ok = r < t.rows;
-    if (!p.rows) return r;
-    const int pair = p.rows[t.row0 + (ok ? r : 0)];
-    const int row = static_cast<int>(static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.k));
-    ok = ok && row < p.a_rows;
-    return row;
-  };
-  const u32x4 ra = buffer_rsrc(p.a + a_first * a_row, clamp_records((p.a_rows - a_first) * a_row));
-  const u32x4 rw = buffer_rsrc(p.w + static_cast<int64_t>(t.e) * n_w * w_row,
-                               clamp_records(static_cast<int64_t>(n_w) * w_row));
-  const u32x4 rsa = buffer_rsrc(p.a_scales + a_first * sc, clamp_records((p.a_rows - a_first) * sc));
-  const u32x4 rsw = buffer_rsrc(p.w_scales + static_cast<int64_t>(t.e) * n_w * sc,
-                                clamp_records(static_cast<int64_t>(n_w) * sc));
-  uint32_t voa[AI], vow[WI];
-#pragma unroll
-  for (int i = 0; i < AI; ++i) {
-    const int j = wave + NW * i;
-    bool ok;
-    const int row = act_row(fill_row<AB>(j, lane), ok);
-    voa[i] = ok ? static_cast<uint32_t>(row) * a_row + fill_chunk<AB>(j, lane) * 16 : kOOB;
-  }
-#pragma unroll
-  for (int i = 0; i < WI; ++i) {
-    const int j = wave + NW * i;
-    bool ok;
-    const int row = weight_row(fill_row<WB>(j, lane), ok);
-    vow[i] = ok ? static_cast<uint32_t>(row) * w_row + fill_chunk<WB>(j, lane) * 16 : kOOB;
-  }
-  // scale rows: instruction q covers 64 rows of the tile, a's first
+  static_assert(!SWIGLU || NW * (1024 / WB) == WN / 2 || NW * (1024 / WB) % WN == 0,
+                "rows an instruction's step apart are so in w");
+  // the byte a lane brings is the same in all of its wave's instructions
+  const int byte_a = fill_byte<AB>(wave, lane), byte_w = fill_byte<WB>(wave, lane);
+  // scale rows: instruction q covers 64 rows of a tile, a's first
   constexpr int SI = (S_BYTES / 1024 + NW - 1) / NW;
-  uint32_t vos[SI];
+  // row of a gathered or, from the tile's first on, of its own
+  auto act = [&](int r, int bytes, uint32_t byte) __attribute__((always_inline)) {
+    if (!p.rows) return r < t.rows ? r * bytes + byte : kOOB;
+    const int pair = p.rows[t.row0 + min(r, t.rows - 1)];
+    const uint32_t row = static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.k);
+    return r < t.rows && row < p.a_rows ? row * bytes + byte : kOOB;
+  };
+  const int64_t a_first = p.rows ? 0 : t.row0, w_first = static_cast<int64_t>(t.e) * n_w;
+  const u32x4 ra = buffer_rsrc(p.a + a_first * a_row, clamp_records((p.a_rows - a_first) * a_row));
+  const u32x4 rsa = buffer_rsrc(p.a_scales + a_first * sc, clamp_records((p.a_rows - a_first) * sc));
+  const u32x4 rw = buffer_rsrc(p.w + w_first * w_row, clamp_records(static_cast<int64_t>(n_w) * w_row));
+  const u32x4 rsw = buffer_rsrc(p.w_scales + w_first * sc, clamp_records(static_cast<int64_t>(n_w) * sc));
+  const int n0 = t.n * out_cols<BN, SWIGLU>();
+  uint32_t voa[AI], vos[SI];
+#pragma unroll
+  for (int i = 0; i < AI; ++i) voa[i] = act(fill_row<AB>(wave + NW * i, lane), a_row, byte_a);
+  const uint32_t vow = static_cast<uint32_t>(n0 + weight_row(fill_row<WB>(wave, lane))) * w_row + byte_w;
 #pragma unroll
   for (int i = 0; i < SI; ++i) {
     const int q = wave + NW * i;
-    bool ok = false;
-    int row = 0;
-    if (q < BM / 64) row = act_row(q * 64 + lane, ok);
-    else if (q < (BM + BN) / 64) row = weight_row((q - BM / 64) * 64 + lane, ok);
-    vos[i] = ok ? static_cast<uint32_t>(row) * sc : kOOB;
+    vos[i] = q < BM / 64 ? act(q * 64 + lane, sc, 0)
+                         : static_cast<uint32_t>(n0 + weight_row((q - BM / 64) * 64 + lane)) * sc;
   }
 
-  const int stages = (p.K + 127) / 128;
-  auto issue = [&](int s) __attribute__((always_inline)) {
-    char* st = smem + (s & 1) * STAGE;
-    const int left = p.K - s * 128;  // elements; a multiple of 32
-    const int a_left = row_bytes_of<AF>(left), w_left = left / 2;
-#pragma unroll
-    for (int i = 0; i < AI; ++i) {
-      const int j = wave + NW * i;
-      const uint32_t vo = fill_chunk<AB>(j, lane) * 16 < a_left ? voa[i] : kOOB;
-      dma16(st + j * 1024, ra, vo, static_cast<uint32_t>(s) * AB);
+  const uint32_t lds = static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(smem)));
+  // Instruction i of this wave's share of stage s into place `at`; what lies past the rows' end is
+  // filled with zeros.
+  auto issue = [&](int s, int at, int i) __attribute__((always_inline)) {
+    const uint32_t st = lds + at * STAGE;
+    if (i < AI) {
+      const uint32_t end = a_row - s * AB > byte_a ? 0u : kOOB;
+      dma16_at(st + (wave + NW * i) * 1024, ra, voa[i < AI ? i : 0] | end, static_cast<uint32_t>(s) * AB);
+    } else {
+      i -= AI;
+      const uint32_t end = w_row - s * WB > byte_w ? 0u : kOOB;
+      dma16_at(st + A_BYTES + (wave + NW * i) * 1024, rw,
+               (vow + static_cast<uint32_t>(weight_row(NW * (1024 / WB) * i)) * w_row) | end,
+               static_cast<uint32_t>(s) * WB);
     }
+  };
+  // The scales of four stages, with the first of them.
+  auto issue_scales = [&](int s) __attribute__((always_inline)) {
+    if ((s & 3) != 0) return;
 #pragma unroll
-    for (int i = 0; i < WI; ++i) {
-      const int j = wave + NW * i;
-      const uint32_t vo = fill_chunk<WB>(j, lane) * 16 < w_left ? vow[i] : kOOB;
-      dma16(st + A_BYTES + j * 1024, rw, vo, static_cast<uint32_t>(s) * WB);
-    }
-    if ((s & 3) == 0) {
-      char* ss = sscale + ((s >> 2) & 1) * S_BYTES;
-#pragma unroll
-      for (int i = 0; i < SI; ++i) {
-        const int q = wave + NW * i;
-        if (q < (BM + BN) / 64)
-          dma16(ss + q * 1024, q < BM / 64 ? rsa : rsw, vos[i], static_cast<uint32_t>(s) * 4);
-      }
+    for (int i = 0; i < SI; ++i) {
+      const int q = wave + NW * i;
+      if (q < (BM + BN) / 64)
+        dma16_at(lds + S_AT + (s >> 2 & 1) * S_BYTES + q * 1024, q < BM / 64 ? rsa : rsw,
+                 vos[i] | (s * 4 < sc ? 0u : kOOB), static_cast<uint32_t>(s) * 4);
     }
   };
 
+  // A stage is two steps of 64 elements, each with its own fragment registers: the second step's are
+  // read while the first is multiplied and the next stage's first while the second is. The barrier
+  // stands between the two, when a wave has read all of the stage and the next one has arrived; the
+  // place it frees is filled during the second step, a few instructions beside each product (all
+  // before the products: 32 experts, 8192 tokens of 4, 550 us against 518; dense 73.8 / 69.0).
   f32x16 acc[NF][MF] = {};
   const int r = lane & 31, g = lane >> 5;
-  issue(0);
-  for (int s = 0; s < stages; ++s) {
-    // this stage has arrived for every wave, and nobody reads the one before any more
-    wait_vmcnt<0>();
-    barrier_lds();
-    if (s + 1 < stages) issue(s + 1);
-    const char* sa = smem + (s & 1) * STAGE + wm * WM * AB;
-    const char* sw = smem + (s & 1) * STAGE + A_BYTES + wn * WN * WB;
-    const char* ss = sscale + ((s >> 2) & 1) * S_BYTES + (s & 3) * 4;
-    int sca[MF], scw[NF];
+  struct Frags {
+    i32x4 a[MF][AB / 64], w[NF];  // as loaded; widened to the instruction's operand at its use
+  };
+  struct Scales {
+    int a[MF], w[NF];
+  };
+  auto load_scales = [&](int s, Scales& c) __attribute__((always_inline)) {
+    const char* ss = smem + S_AT + (s >> 2 & 1) * S_BYTES + (s & 3) * 4;
 #pragma unroll
     for (int f = 0; f < MF; ++f)
-      sca[f] = *reinterpret_cast<const int*>(ss + (wm * WM + f * 32 + r) * 16) >> (8 * g);
+      c.a[f] = *reinterpret_cast<const int*>(ss + (wm * WM + f * 32 + r) * 16) >> (8 * g);
 #pragma unroll
     for (int f = 0; f < NF; ++f)
-      scw[f] = *reinterpret_cast<const int*>(ss + (BM + wn * WN + f * 32 + r) * 16) >> (8 * g);
-    auto step = [&](auto jc) __attribute__((always_inline)) {
-      constexpr int j = decltype(jc)::value;
-      i32x8 fa[MF], fw[NF];
+      c.w[f] = *reinterpret_cast<const int*>(ss + (BM + wn * WN + f * 32 + r) * 16) >> (8 * g);
+  };
+  // Piece i of a step's fragments: 16 bytes of a weight fragment, or of one of a's.
+  constexpr int PIECES = NF + MF * (AB / 64), PRODUCTS = NF * MF;
+  auto load = [&](int at, auto jc, int i, Frags& x) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value;
+    if (i < NF) {
+      x.w[i < NF ? i : 0] = *reinterpret_cast<const i32x4*>(
+          smem + at * STAGE + A_BYTES + (wn * WN + i * 32 + r) * WB + (((2 * j + g) ^ mx_swz<WB>(r)) << 4));
+    } else if (i < PIECES) {
+      const int f = (i - NF) / (AB / 64), h = (i - NF) % (AB / 64);
+      x.a[f][h] = *reinterpret_cast<const i32x4*>(
+          smem + at * STAGE + (wm * WM + f * 32 + r) * AB +
+          (((AB / 32 * j + 2 * h + g) ^ mx_swz<AB>(r)) << 4));
+    }
+  };
+  // Product i of a step. The empty statement holds it in place: neither it nor what stands beside it
+  // moves across, so that the wave's other instructions go out while the matrix core is busy.
+  auto multiply = [&](auto jc, int i, const Frags& x, const Scales& c) __attribute__((always_inline)) {
+    constexpr int j = decltype(jc)::value;
+    const int f = i / MF, m = i % MF;
+    acc[f][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+        mx_operand(x.w[f], x.w[f], true), mx_operand(x.a[m][0], x.a[m][AB / 64 - 1], AB == 64),
+        acc[f][m], 4, AF == MOE_MX_FP4 ? 4 : 0, 2 * j, c.w[f], 2 * j, c.a[m]);
+    asm volatile("" : "+v"(acc[f][m])::"memory");
+  };
+  const std::integral_constant<int, 0> first;
+  const std::integral_constant<int, 1> second;
+  constexpr int EACH = (PIECES + PRODUCTS - 1) / PRODUCTS;       // pieces read beside a product
+  constexpr int FILL = (AI + WI + PRODUCTS - 1) / PRODUCTS;      // DMA instructions beside one
+  Frags x0, x1;
+  Scales c0, c1;
+  // Loads of a wave complete in order: with at most so many left, the stage before the last NST - 2
+  // has arrived (scales among them only make the wait stricter).
+  constexpr int IN_FLIGHT = (NST - 2) * (AI + WI);
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const i32x4 v = *reinterpret_cast<const i32x4*>(
-            sw + (f * 32 + r) * WB + (((2 * j + g) ^ mx_swz<WB>(r)) << 4));
-        fw[f] = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-      }
+  for (int s = 0; s < NST; ++s) {
+    issue_scales(s);
 #pragma unroll
-      for (int f = 0; f < MF; ++f) {
-        const char* row = sa + (f * 32 + r) * AB;
-        if constexpr (AF == MOE_MX_FP4) {
-          const i32x4 v = *reinterpret_cast<const i32x4*>(row + (((2 * j + g) ^ mx_swz<AB>(r)) << 4));
-          fa[f] = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-        } else {
-          const i32x4 lo = *reinterpret_cast<const i32x4*>(row + (((4 * j + g) ^ mx_swz<AB>(r)) << 4));
-          const i32x4 hi =
-              *reinterpret_cast<const i32x4*>(row + (((4 * j + 2 + g) ^ mx_swz<AB>(r)) << 4));
-          fa[f] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < NF; ++f)
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
-          acc[f][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              fw[f], fa[m], acc[f][m], 4, AF == MOE_MX_FP4 ? 4 : 0, 2 * j, scw[f], 2 * j, sca[m]);
-    };
-    step(std::integral_constant<int, 0>());
-    step(std::integral_constant<int, 1>());
+    for (int i = 0; i < AI + WI; ++i) issue(s, s, i);
   }
+  wait_vmcnt<IN_FLIGHT + AI + WI>();
+  barrier_lds();
+  load_scales(0, c0);
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) load(0, first, i, x0);
+  int at = 0;  // the place of stage s
+  for (int s = 0; s < stages; ++s) {
+#pragma unroll
+    for (int i = 0; i < PRODUCTS; ++i) {
+#pragma unroll
+      for (int n = 0; n < EACH; ++n) load(at, second, EACH * i + n, x1);
+      multiply(first, i, x0, c0);
+    }
+    wait_vmcnt<IN_FLIGHT>();
+    barrier_lds();
+    const int next = at + 1 == NST ? 0 : at + 1;
+    c1 = c0;
+    load_scales(s + 1, c0);  // past the last stage: not used
+    issue_scales(s + NST);
+#pragma unroll
+    for (int i = 0; i < PRODUCTS; ++i) {
+      multiply(second, i, x1, c1);
+#pragma unroll
+      for (int n = 0; n < EACH; ++n) load(next, first, EACH * i + n, x0);
+#pragma unroll
+      for (int n = 0; n < FILL; ++n)
+        if (FILL * i + n < AI + WI) issue(s + NST, at, FILL * i + n);
+    }
+    at = next;
+  }
+  wait_vmcnt<0>();
 
   // Lane (r, g) holds row r's columns 8 q + 4 g + i at register 4 q + i; after swapping halves with
   // its partner it holds the 16 columns from 16 g on.
@@ -308,13 +353,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void mx_gemm_kern
     for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[4 * q + i]),
                                                         __float_as_uint(c[4 * (q + 2) + i]), false, false);
         v[8 * q + i] = __uint_as_float(x[0]);
         v[8 * q + 4 + i] = __uint_as_float(x[1]);
       }
   };
+
   constexpr int OF = SWIGLU ? NF / 2 : NF;  // fragments of output columns
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
@@ -374,100 +419,139 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, MINB) void mx_gemm_kern
 }
 
 // ------------------------------------------------------------------ few rows: weights streamed
-// A block takes up to 16 rows and 32 output columns; its four waves split the reduction and meet in
-// LDS, adding in order. Weights come straight from HBM into the matrix cores' registers, each byte
-// once for 16 rows; steps of 128 elements are loaded kAhead at a time.
-constexpr int kSmallRows = 16, kSmallCols = 32, kSmallWaves = 4, kAhead = 4;
+// A block takes up to 16 rows and 16 or 32 output columns; its waves split the reduction and meet in
+// LDS, adding in order. Weights come straight from HBM into the matrix cores' registers, each byte once
+// for 16 rows, in batches of four steps of 128 elements with the next batch on its way: a row's four
+// steps are 256 bytes of codes and 16 of scales. Loads go by buffer resources, whose bounds make
+// zeros of steps past the operand; what a batch reads behind its own steps is not multiplied.
+constexpr int kSmallRows = 16, kSmallWaves = 4, kBatch = 4;
+
+// Output columns of a block: as few as there can be, so that even one token's experts give every CU
+// several blocks; 32 where they share a scale. (32 columns for 16-bit results: 64 tokens of 4 of 32
+// experts, 2880 x 2880 gate and up, 92 us against 76; one token 10.3 against 10.2.)
+template <int OUT>
+constexpr int small_cols() { return OUT == kMxOut8 ? 32 : 16; }
 
 template <int AF, int OUT, bool SWIGLU>
 __global__ __launch_bounds__(kSmallWaves * 64) void mx_rows_kernel(MxGemm p) {
-  constexpr int NF = SWIGLU ? 4 : 2;
+  constexpr int COLS = small_cols<OUT>(), OF = COLS / 16, NF = SWIGLU ? 2 * OF : OF;
   constexpr int AB = row_bytes_of<AF>(128), AC = AB / 64;  // bytes a step; 16-byte pieces a lane
   constexpr int LD = 20;  // floats between a row's fragments' columns, off the banks' period
   __shared__ float red[kSmallWaves][NF][16][LD];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   MxTile t;
   if (!find_tile<kSmallRows, false>(p, blockIdx.x, t)) return;
-  const int n0 = t.n * kSmallCols, n_w = SWIGLU ? 2 * p.N : p.N;
+  const int n0 = t.n * COLS, n_w = SWIGLU ? 2 * p.N : p.N;
   const int a_row = row_bytes_of<AF>(p.K), w_row = p.K / 2;
   const int sc = static_cast<int>(mx_scale_cols(p.K));
   const int r = lane & 15, g = lane >> 4;
-
-  // a's row of this lane
   const bool act = r < t.rows;
-  int64_t arow = t.row0 + (act ? r : 0);
-  if (p.rows)
-    arow = static_cast<uint32_t>(p.rows[arow]) / static_cast<uint32_t>(p.k);
-  const bool a_ok = act && arow < p.a_rows;
-  if (!a_ok) arow = 0;
-  const uint8_t* ap = p.a + arow * a_row;
-  const uint8_t* asp = p.a_scales + arow * sc;
-  const uint8_t *wp[NF], *wsp[NF];
-  bool w_ok[NF];
+  int64_t arow = t.row0 + (act ? r : 0);  // a's row of this lane
+  int pair = 0;
+  if (p.rows) pair = p.rows[arow];
+
+  auto resource = [](const uint8_t* base, int64_t bytes) __attribute__((always_inline)) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), static_cast<short>(0),
+                                             clamp_records(bytes), 0x00020000);
+  };
+  const int64_t w_first = static_cast<int64_t>(t.e) * n_w;
+  const auto rw = resource(p.w + w_first * w_row, static_cast<int64_t>(n_w) * w_row);
+  const auto rsw = resource(p.w_scales + w_first * sc, static_cast<int64_t>(n_w) * sc);
+  uint32_t vw[NF], vsw[NF];
 #pragma unroll
   for (int f = 0; f < NF; ++f) {
-    const int half = SWIGLU ? f & 1 : f, n = n0 + 16 * half + r;
-    w_ok[f] = n < p.N;
-    const int64_t row = static_cast<int64_t>(t.e) * n_w + (w_ok[f] ? n : 0) + (SWIGLU && f >= 2 ? p.N : 0);
-    wp[f] = p.w + row * w_row;
-    wsp[f] = p.w_scales + row * sc;
+    const int n = n0 + 16 * (f % OF) + r;  // SwiGLU: the gate's fragments, then those of up
+    const uint32_t row = n + f / OF * p.N;
+    vw[f] = n < p.N ? row * w_row + g * 16 : kOOB;
+    vsw[f] = n < p.N ? row * sc : kOOB;
   }
   const int steps = (p.K + 127) / 128, each = (steps + kSmallWaves - 1) / kSmallWaves;
   const int first = wave * each, last = min(steps, first + each);
-  f32x4 acc[NF] = {};
-  const i32x4 zero = {};
-  for (int s0 = first; s0 < last; s0 += kAhead) {
-    i32x4 w[kAhead][NF], a[kAhead][AC];
-    int sw[kAhead][NF], sa[kAhead];
+  struct Batch {
+    i32x4 w[kBatch][NF], sw[NF], a[kBatch][AC], sa;
+  };
+  auto load_w = [&](int s0, Batch& x) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int s = s0 + u;
-      const bool in = s < last;
-      const int at = in ? s : first;
-      // elements of this lane's pieces that are within the row
-      const int left = in ? p.K - s * 128 : 0;
+    for (int u = 0; u < kBatch; ++u) {
+      // pieces past the row's end are zeros
+      const uint32_t end = (s0 + u) * 64 + g * 16 < w_row ? 0u : kOOB;
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const bool ok = w_ok[f] && g * 32 < left;
-        w[u][f] = ok ? __builtin_nontemporal_load(reinterpret_cast<const i32x4*>(wp[f] + at * 64 + g * 16)) : zero;
-        sw[u][f] = *reinterpret_cast<const int*>(wsp[f] + at * 4) >> (8 * g);
-      }
-#pragma unroll
-      for (int c = 0; c < AC; ++c) {
-        const int byte = c * 64 + g * 16;
-        const bool ok = a_ok && byte < row_bytes_of<AF>(left);
-        a[u][c] = ok ? *reinterpret_cast<const i32x4*>(ap + at * AB + byte) : zero;
-      }
-      sa[u] = *reinterpret_cast<const int*>(asp + at * 4) >> (8 * g);
+      for (int f = 0; f < NF; ++f)
+        x.w[u][f] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, vw[f] | end, (s0 + u) * 64, 0));
     }
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const i32x8 fa = AC == 2 ? __builtin_shufflevector(a[u][0], a[u][AC - 1], 0, 1, 2, 3, 4, 5, 6, 7)
-                               : __builtin_shufflevector(a[u][0], a[u][0], 0, 1, 2, 3, -1, -1, -1, -1);
+    for (int f = 0; f < NF; ++f)
+      x.sw[f] = __builtin_bit_cast(
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsw, vsw[f], s0 * 4, 0));
+  };
+  Batch x0, x1;
+  if (first < last) load_w(first, x0);
+  if (p.rows) arow = static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.k);
+  // a tile's rows lie together, or are anywhere in a gathered a (below 2 GiB)
+  const int64_t a_first = p.rows ? 0 : t.row0;
+  const auto ra = resource(p.a + a_first * a_row, (p.a_rows - a_first) * a_row);
+  const auto rsa = resource(p.a_scales + a_first * sc, (p.a_rows - a_first) * sc);
+  const bool a_ok = act && arow < p.a_rows;
+  const uint32_t va = a_ok ? static_cast<uint32_t>(arow - a_first) * a_row + g * 16 : kOOB;
+  const uint32_t vsa = a_ok ? static_cast<uint32_t>(arow - a_first) * sc : kOOB;
+  auto load_a = [&](int s0, Batch& x) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+      for (int c = 0; c < AC; ++c) {
+        const int byte = (s0 + u) * AB + c * 64;
+        const uint32_t end = byte + g * 16 < a_row ? 0u : kOOB;
+        x.a[u][c] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, va | end, byte, 0));
+      }
+    x.sa = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rsa, vsa, s0 * 4, 0));
+  };
+  f32x4 acc[NF] = {};
+  auto multiply = [&](int s0, const Batch& x) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (s0 + u >= last) break;
+      const i32x8 fa = mx_operand(x.a[u][0], x.a[u][AC - 1], AC == 1);
 #pragma unroll
       for (int f = 0; f < NF; ++f)
         acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            __builtin_shufflevector(w[u][f], w[u][f], 0, 1, 2, 3, -1, -1, -1, -1), fa, acc[f], 4,
-            AF == MOE_MX_FP4 ? 4 : 0, 0, sw[u][f], 0, sa[u]);
+            mx_operand(x.w[u][f], x.w[u][f], true), fa, acc[f], 4, AF == MOE_MX_FP4 ? 4 : 0, 0,
+            x.sw[f][u] >> (8 * g), 0, x.sa[u] >> (8 * g));
     }
+  };
+  if (first < last) load_a(first, x0);
+  for (int s0 = first; s0 < last; s0 += 2 * kBatch) {
+    if (s0 + kBatch < last) {
+      load_w(s0 + kBatch, x1);
+      load_a(s0 + kBatch, x1);
+    }
+    multiply(s0, x0);
+    if (s0 + 2 * kBatch < last) {
+      load_w(s0 + 2 * kBatch, x0);
+      load_a(s0 + 2 * kBatch, x0);
+    }
+    multiply(s0 + kBatch, x1);
   }
   // lane (r, g) has row r, columns 4 g .. 4 g + 3
 #pragma unroll
   for (int f = 0; f < NF; ++f)
     *reinterpret_cast<f32x4*>(&red[wave][f][r][4 * g]) = acc[f];
   __syncthreads();
-  const int m = threadIdx.x >> 4, c = (threadIdx.x & 15) * 2, col = n0 + c;
+  // CPT columns a thread
+  constexpr int CPT = COLS / 16;
+  const int m = threadIdx.x >> 4, c = (threadIdx.x & 15) * CPT, col = n0 + c;
   auto total = [&](int f, int at) __attribute__((always_inline)) {
     float v = red[0][f][m][at];
 #pragma unroll
     for (int w = 1; w < kSmallWaves; ++w) v += red[w][f][m][at];
     return v;
   };
-  float v[2];
+  float v[CPT];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < CPT; ++i) {
     v[i] = total(c >> 4, (c & 15) + i);
-    if constexpr (SWIGLU) v[i] = swiglu(v[i], total(2 + (c >> 4), (c & 15) + i));
+    if constexpr (SWIGLU) v[i] = swiglu(v[i], total(OF + (c >> 4), (c & 15) + i));
   }
   const bool there = m < t.rows && col < p.N;
   const int64_t row = t.row0 + m;
@@ -492,11 +576,29 @@ __global__ __launch_bounds__(kSmallWaves * 64) void mx_rows_kernel(MxGemm p) {
       }
     }
   } else if (there) {
+    Out16<OUT>* y = static_cast<Out16<OUT>*>(p.y) + row * p.N + col;
     const uint32_t lo = __builtin_bit_cast(uint16_t, from_f32<Out16<OUT>>(v[0]));
-    const uint32_t hi = __builtin_bit_cast(uint16_t, from_f32<Out16<OUT>>(v[1]));
-    *reinterpret_cast<uint32_t*>(static_cast<Out16<OUT>*>(p.y) + row * p.N + col) = lo | (hi << 16);
+    if constexpr (CPT == 2) {  // N and the column are even
+      const uint32_t hi = __builtin_bit_cast(uint16_t, from_f32<Out16<OUT>>(v[1]));
+      *reinterpret_cast<uint32_t*>(y) = lo | (hi << 16);
+    } else {
+      *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(lo);
+    }
   }
 }
+
+// Which kernel takes a call, measured on both sides of each line.
+//  Few rows: while its blocks (in units of 16 output columns) are at most three a CU, since weights
+//  are read again for every 16 rows. 4096 -> 2880, 64 rows 11.9 us against 14.5 of the smallest
+//  tiles, 96 rows 18.3 against 14.7; 8192 -> 8192, 16 rows 15.3 / 25.3, 32 rows 27.5 / 24.9; SwiGLU
+//  2880 -> 2880 of 4 of 32 experts, one token 10.5 / 13.2, 8 tokens 41.9 / 36.7.
+//  Larger tiles, which read less from L2 for a product: where they give three quarters of the CUs a
+//  tile, and experts on average rows for half of one. 4096 -> 2880, 256 x 256 against 128 x 128:
+//  4096 rows (192 tiles) 51.6 / 54.8 us, 2048 rows 43.4 / 31.4; the experts above, 1024 tokens (128
+//  rows each) 122.6 / 143.0, 768 tokens 114.7 / 103.5. 128 x 128 against 64 x 128: 1024 rows (184
+//  tiles) 20.1 / 21.4, 512 rows 17.8 / 15.6; the experts, 512 tokens (64 rows each) 93.5 / 111.8,
+//  256 tokens 81 / 75. (128 x 256 lies within 7 % of one of the others everywhere.)
+constexpr int kRowsBlocks = 768, kTilesToFill = 192;
 
 // Calls go with the format of a, the output and SwiGLU as constants.
 template <typename F>
@@ -541,20 +643,37 @@ hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const u
   return by_product(s, [&](auto af, auto out, auto glu) {
     constexpr int AF = decltype(af)::value, OUT = decltype(out)::value;
     constexpr bool GLU = decltype(glu)::value;
-    // at most this many M tiles of bm rows, whatever the experts' counts are
-    auto tiles = [&](int bm) {
-      return s.E > 0 ? p.M / bm + experts : (p.M + bm - 1) / bm;
+    // at most this many tiles of bm rows and bn weight rows, whatever the experts' counts are
+    auto tiles = [&](int bm, int cols) {
+      p.ntn = (s.N + cols - 1) / cols;
+      return static_cast<int64_t>(s.E > 0 ? p.M / bm + experts : (p.M + bm - 1) / bm) * p.ntn;
     };
-    if (p.M <= 16 * experts) {
-      p.ntn = (s.N + kSmallCols - 1) / kSmallCols;
+    auto tiled = [&](auto bm, auto bn, auto wm, auto wn, auto nst) {
+      constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
+      constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
+      hipLaunchKernelGGL((mx_gemm_kernel<AF, OUT, GLU, BM, BN, WM, WN, decltype(nst)::value>),
+                         dim3(static_cast<unsigned>(tiles(BM, out_cols<BN, GLU>()))),
+                         dim3((BM / WM) * (BN / WN) * 64), 0, st, p);
+    };
+    auto fills = [&](int bm, int bn) {
+      const int cols = GLU ? bn / 2 : bn;
+      return p.M >= bm / 2 * static_cast<int64_t>(experts) &&
+             p.M / bm * static_cast<int64_t>((s.N + cols - 1) / cols) >= kTilesToFill;
+    };
+    using std::integral_constant;
+    if (tiles(kSmallRows, small_cols<OUT>()) * (small_cols<OUT>() / 16) <= kRowsBlocks) {
       hipLaunchKernelGGL((mx_rows_kernel<AF, OUT, GLU>),
-                         dim3(static_cast<unsigned>(tiles(kSmallRows) * p.ntn)),
+                         dim3(static_cast<unsigned>(tiles(kSmallRows, small_cols<OUT>()))),
                          dim3(kSmallWaves * 64), 0, st, p);
+    } else if (fills(256, 256)) {
+      tiled(integral_constant<int, 256>(), integral_constant<int, 256>(), integral_constant<int, 64>(),
+            integral_constant<int, 128>(), integral_constant<int, 3>());
+    } else if (fills(128, 128)) {
+      tiled(integral_constant<int, 128>(), integral_constant<int, 128>(), integral_constant<int, 64>(),
+            integral_constant<int, 64>(), integral_constant<int, 3>());
     } else {
-      constexpr int BM = 128, BN = 256, C = out_cols<BN, GLU>();
-      p.ntn = (s.N + C - 1) / C;
-      hipLaunchKernelGGL((mx_gemm_kernel<AF, OUT, GLU, BM, BN, 64, 128, 2>),
-                         dim3(static_cast<unsigned>(tiles(BM) * p.ntn)), dim3(256), 0, st, p);
+      tiled(integral_constant<int, 64>(), integral_constant<int, 128>(), integral_constant<int, 32>(),
+            integral_constant<int, 64>(), integral_constant<int, 4>());
     }
     return hipGetLastError();
   });
