@@ -1,9 +1,11 @@
 """GPU parity of the microscaled products against float64 products of the dequantised operands.
 
-Tolerances. The products of two codes with their scales are exact; the matrix cores add those of one
-instruction after an alignment that is measured at below 2^-17 of the sum of their magnitudes (one
-128-product instruction with 8-bit operands), and the instructions' sums in float32. Allowed:
-d = 2^-16 sum_k |a w| for a product. With SwiGLU, d comes in through both factors, the slope of
+Tolerances. The products of two codes with their scales are exact. The matrix cores add them eight
+neighbours at a time, aligned to the largest of the eight: what of a product lies below 2^-13 of the
+power of two at or under that largest is cut off towards zero (measured; 256 beside 1.75 * 2^-5 gives
+2^-5, and 2^-6 nothing, at the places 0 to 7 and no further). So a product's error is at most the sum
+of what is cut, |a w| mod that unit, which `cut` forms product by product, and that of the float32 sums
+of the eights, for which 2^-16 sum_k |a w| is allowed: d is the sum of the two. With SwiGLU, d comes in through both factors, the slope of
 silu is at most 1.1, and its exponential and reciprocal add 16 roundings of float32. A 16-bit result
 is rounded once: u = eps / 2 of the type. An 8-bit result is the code of some value within d of the
 exact one, under the scale of some largest magnitude within d: both are checked as intervals.
@@ -44,6 +46,19 @@ def _routing(rng, T, E, k, skew=False):
     return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32), order.astype(np.int32)
 
 
+def cut(a, w):
+    """[M, n] sums over k of what the alignment of eight products cuts off."""
+    a, w = (torch.from_numpy(np.ascontiguousarray(v)).cuda().view(len(v), -1, 8) for v in (a, w))
+    out = torch.zeros(len(a), len(w), device="cuda", dtype=torch.float64)
+    step = max(1, (1 << 25) // w.numel())
+    for lo in range(0, len(a), step):
+        p = (a[lo:lo + step, None] * w[None]).abs()
+        # frexp's mantissa is in [0.5, 1)
+        unit = torch.exp2(torch.frexp(p.amax(-1))[1].double() - 14)[..., None]
+        out[lo:lo + step] = (p - (p / unit).floor() * unit).sum((-1, -2))
+    return out.cpu().numpy()
+
+
 def reference(a, w, offsets, M, swiglu):
     """(y, d) in float64 for rows in expert order (offsets None: one matrix)."""
     spans = [(0, M, w)] if offsets is None else [
@@ -52,7 +67,8 @@ def reference(a, w, offsets, M, swiglu):
     z, d = np.zeros((M, n_w)), np.zeros((M, n_w))
     for lo, hi, we in spans:
         z[lo:hi] = a[lo:hi] @ we.T
-        d[lo:hi] = 2.0 ** -16 * (np.abs(a[lo:hi]) @ np.abs(we).T)
+        if hi > lo:
+            d[lo:hi] = 2.0 ** -16 * (np.abs(a[lo:hi]) @ np.abs(we).T) + cut(a[lo:hi], we)
     if not swiglu:
         return z, d
     n = n_w // 2
