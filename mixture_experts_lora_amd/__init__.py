@@ -966,7 +966,7 @@ except RuntimeError:
     pass
 
 from .layer import (LayerScratch, MoELoRABlock, MoELoRAChunkedLayer, MoELoRAFunction,  # noqa: E402
-                    MoELoRALayer, MoELoRASublayer)
+                    MoELoRALayer, MoELoRASublayer, MoEMXLayer, MoEMXSublayer, mx_weights)
 
 __all__ += ["LayerScratch", "MoELoRABlock", "MoELoRAChunkedLayer", "MoELoRALayer",
-            "MoELoRAFunction", "MoELoRASublayer"]
+            "MoELoRAFunction", "MoELoRASublayer", "MoEMXLayer", "MoEMXSublayer", "mx_weights"]

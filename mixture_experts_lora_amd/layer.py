@@ -16,6 +16,11 @@ so nothing is allocated inside a step) and issues, on torch's current stream:
   (on x_perm), which read the expert outputs y_exp, so those are then kept
   from the forward.
 
+  router is the name of a moe_route mode, or a GroupedRouter: moe_route_grouped
+  and its backward then take their places, with the balance bias of the call's
+  route_bias. clip_grads() clips the layer's gradients together (moe_grad_norm
+  -> moe_grad_clip).
+
 MoELoRAFunction wraps the same calls as a torch.autograd.Function whose
 gradients are dX, d logits and the four LoRA gradients (base weights frozen).
 
@@ -35,16 +40,27 @@ layer once attention has run: attention's heads projected into the stream
 (moe_linear_fwd), the norm before the block, the block, and its output through
 a norm, a gate, a residual scale and dropout added to the stream
 (moe_residual_norm_fwd); and the backward of all of it.
+
+MoEMXLayer is the forward of an exported layer: the merged weights in 4 bits
+(mx_weights, from moe_merge_lora's), the activations in 8:
+  moe_mx_quantize -> the routing -> moe_permute (indices only) -> moe_mx_linear
+  (gate and up with SwiGLU, reading the tokens' rows through sorted_pair, its
+  result in 8 bits) -> moe_mx_linear -> moe_unpermute_combine
+MoEMXSublayer is that layer on the residual stream: the norm before it writes
+its 8-bit rows beside those that the router reads (moe_residual_norm_mx_fwd).
 """
 from __future__ import annotations
 
 import torch
 
-from . import (LinearShape, Residual, Shape, moe_accumulate, moe_grouped_full_bwd,
+from . import (GradList, GroupedRouter, LinearShape, MXLinear, Residual, Shape, moe_accumulate,
+               moe_grad_clip, moe_grad_norm, moe_grad_norm_workspace_bytes, moe_grouped_full_bwd,
                moe_grouped_lora_bwd, moe_linear_bwd, moe_linear_fwd, moe_linear_workspace_bytes,
                moe_residual_norm_bwd, moe_residual_norm_fwd, moe_residual_norm_workspace_bytes,
                moe_grouped_lora_combine_bwd, moe_grouped_lora_combine_bwd_gather,
-               moe_grouped_lora_fwd_gather,
+               moe_grouped_lora_fwd_gather, moe_mx_linear, moe_mx_linear_workspace_bytes,
+               moe_mx_quantize, moe_residual_norm_mx_fwd, moe_route_grouped,
+               moe_route_grouped_bwd, mx_scale_cols,
                moe_grouped_lora_bwd_recompute, moe_grouped_lora_fwd, moe_grouped_lora_fwd_lean,
                moe_permute, moe_route, moe_route_bwd, moe_router_bwd, moe_router_fwd,
                moe_router_workspace_bytes, moe_unpermute_combine, moe_unpermute_combine_bwd,
@@ -52,6 +68,45 @@ from . import (LinearShape, Residual, Shape, moe_accumulate, moe_grouped_full_bw
 
 WEIGHT_NAMES = ("w_gu", "a_gu", "b_gu", "w_d", "a_d", "b_d")
 GRAD_NAMES = ("da_gu", "db_gu", "da_d", "db_d")
+
+
+def _check_router(router, shape: Shape):
+    if isinstance(router, GroupedRouter) and (router.E, router.k) != (shape.E, shape.k):
+        raise ValueError(f"router of {router.k} of {router.E} experts, layer of {shape.k} of "
+                         f"{shape.E}")
+
+
+def _route(router, logits, topk_ids, topk_w, bias, stream):
+    if isinstance(router, GroupedRouter):
+        moe_route_grouped(router, logits, topk_ids, topk_w, bias, stream)
+    elif bias is not None:
+        raise ValueError("route_bias is a GroupedRouter's")
+    else:
+        moe_route(logits, topk_ids.shape[1], router, topk_ids, topk_w, stream)
+
+
+def _route_bwd(router, logits, topk_ids, d_topk_w, d_logits, stream):
+    if isinstance(router, GroupedRouter):
+        moe_route_grouped_bwd(router, logits, topk_ids, d_topk_w, d_logits, stream)
+    else:
+        moe_route_bwd(logits, topk_ids, d_topk_w, topk_ids.shape[1], router, d_logits, stream)
+
+
+class _Clipped:
+    """clip_grads() of a layer that owns its gradients' buffers (_grad_buffers())."""
+
+    def clip_grads(self, max_norm: float, eps: float = 1e-6, stream=None):
+        """Scales the layer's gradients in place by min(1, max_norm / (norm + eps)); returns norm
+        (float32 [1], on the device), the 2-norm of all of them before."""
+        if not hasattr(self, "_clip"):
+            grads = GradList(self._grad_buffers())
+            u8, dev = torch.uint8, grads.grads[0].device
+            ws = torch.empty(max(moe_grad_norm_workspace_bytes(grads), 1), device=dev, dtype=u8)
+            self._clip = grads, torch.empty(1, device=dev), ws
+        grads, norm, ws = self._clip
+        moe_grad_norm(grads, norm, ws, stream)
+        moe_grad_clip(grads, norm, max_norm, eps, stream)
+        return norm
 
 
 class LayerScratch:
@@ -97,7 +152,7 @@ def _gatherable(shape: Shape) -> bool:
     return shape.T * shape.H * shape.torch_dtype.itemsize < (1 << 31)
 
 
-class MoELoRALayer:
+class MoELoRALayer(_Clipped):
     """full_ft=True also computes the base-weight gradients (full fine-tuning).
     recompute=True is the activation-lean mode: h and act are not kept between
     forward and backward (they live in the forward workspace and are recomputed
@@ -124,11 +179,12 @@ class MoELoRALayer:
     outputs into (a chunk writes its rows of the whole layer's outputs).
     grads, base_grads: optional gradient buffers to write into."""
 
-    def __init__(self, shape: Shape, router: str, device="cuda", full_ft: bool = False,
-                 recompute: bool = False, scratch: LayerScratch | None = None,
+    def __init__(self, shape: Shape, router: str | GroupedRouter, device="cuda",
+                 full_ft: bool = False, recompute: bool = False, scratch: LayerScratch | None = None,
                  out: dict | None = None, grads: dict | None = None,
                  base_grads: dict | None = None, fold_combine_bwd: bool = True,
                  gather_x: bool | None = None, gather_dy: bool = True):
+        _check_router(router, shape)
         self.shape, self.router, self.full_ft, self.recompute = shape, router, full_ft, recompute
         self.fold = fold_combine_bwd
         if gather_x is None:
@@ -182,14 +238,17 @@ class MoELoRALayer:
         t = list(self.saved.values()) + ([] if self.recompute or self.gather else [self.x_perm])
         return sum(v.numel() * v.element_size() for v in t)
 
+    def _grad_buffers(self):
+        return [*self.grads.values(), *(self.base_grads or {}).values()]
+
     def _permute(self, x, stream):
         s = self.shape
         moe_permute(s, self.topk_ids, x, self.counts, self.offsets, self.sorted_pair,
                     self.inv_pos, self.x_perm, self.ws_perm, stream)
 
-    def forward(self, x, logits, weights: dict, stream=None):
+    def forward(self, x, logits, weights: dict, stream=None, route_bias=None):
         s = self.shape
-        moe_route(logits, s.k, self.router, self.topk_ids, self.topk_w, stream)
+        _route(self.router, logits, self.topk_ids, self.topk_w, route_bias, stream)
         self._permute(x, stream)
         saved = {**self.saved, "y_exp": self.y_exp}
         if self.gather:
@@ -216,14 +275,12 @@ class MoELoRALayer:
                 x if self.gather else self.x_perm, self.offsets, weights, self.saved,
                 self.dy_perm, self.dx_perm, self.grads, self.d_topk_w, self.ws_bwd,
                 base_grads=self.base_grads, recompute=self.recompute, stream=stream)
-            moe_route_bwd(logits, self.topk_ids, self.d_topk_w, s.k, self.router, self.d_logits,
-                          stream)
+            _route_bwd(self.router, logits, self.topk_ids, self.d_topk_w, self.d_logits, stream)
             moe_unpermute_combine(s, self.dx_perm, self.inv_pos, None, self.dx, stream)
             return self.dx, self.d_logits, self.grads
         moe_unpermute_combine_bwd(s, dy, self.y_exp, self.inv_pos, self.topk_w,
                                   self.dy_perm, self.d_topk_w, stream)
-        moe_route_bwd(logits, self.topk_ids, self.d_topk_w, s.k, self.router, self.d_logits,
-                      stream)
+        _route_bwd(self.router, logits, self.topk_ids, self.d_topk_w, self.d_logits, stream)
         if self.recompute:
             moe_grouped_lora_bwd_recompute(s, self.dy_perm, self.x_perm, self.offsets, weights,
                                            self.saved, self.dx_perm, self.grads, self.ws_bwd,
@@ -237,13 +294,13 @@ class MoELoRALayer:
         moe_unpermute_combine(s, self.dx_perm, self.inv_pos, None, self.dx, stream)
         return self.dx, self.d_logits, self.grads
 
-    def step(self, x, logits, dy, weights: dict, stream=None):
+    def step(self, x, logits, dy, weights: dict, stream=None, route_bias=None):
         """One forward and backward pass."""
-        self.forward(x, logits, weights, stream)
+        self.forward(x, logits, weights, stream, route_bias)
         return self.backward(dy, logits, weights, stream, x=x)
 
 
-class MoELoRAChunkedLayer:
+class MoELoRAChunkedLayer(_Clipped):
     """The layer over its T tokens in `chunks` consecutive chunks, for long
     contexts: every output row depends only on its own token, so each chunk
     runs the same calls on its rows (writing its rows of Y, dX and d logits,
@@ -253,7 +310,7 @@ class MoELoRAChunkedLayer:
     and the permuted gradient rows are sized for one chunk and shared, which
     is what lowers the peak."""
 
-    def __init__(self, shape: Shape, router: str, chunks: int, device="cuda",
+    def __init__(self, shape: Shape, router: str | GroupedRouter, chunks: int, device="cuda",
                  full_ft: bool = False, recompute: bool = False, gather_x: bool | None = None,
                  gather_dy: bool = True):
         if chunks < 1 or chunks > shape.T:
@@ -293,9 +350,12 @@ class MoELoRAChunkedLayer:
     def saved_bytes(self) -> int:
         return sum(p.saved_bytes() for p in self.parts)
 
-    def forward(self, x, logits, weights: dict, stream=None):
+    def _grad_buffers(self):
+        return self.parts[0]._grad_buffers()
+
+    def forward(self, x, logits, weights: dict, stream=None, route_bias=None):
         for (lo, hi), p in zip(self.bounds, self.parts):
-            p.forward(x[lo:hi], logits[lo:hi], weights, stream)
+            p.forward(x[lo:hi], logits[lo:hi], weights, stream, route_bias)
         return self.y
 
     def backward(self, dy, logits, weights: dict, stream=None, x=None):
@@ -310,8 +370,8 @@ class MoELoRAChunkedLayer:
                         moe_accumulate(g, self.base_grads[n], stream)
         return self.dx, self.d_logits, self.grads
 
-    def step(self, x, logits, dy, weights: dict, stream=None):
-        self.forward(x, logits, weights, stream)
+    def step(self, x, logits, dy, weights: dict, stream=None, route_bias=None):
+        self.forward(x, logits, weights, stream, route_bias)
         return self.backward(dy, logits, weights, stream, x=x)
 
 
@@ -341,7 +401,7 @@ class _DenseExpertBuffers:
                                                 dtype=torch.uint8)
 
 
-class MoELoRABlock:
+class MoELoRABlock(_Clipped):
     """Router projection + routed MoE-LoRA layer + optional shared expert.
 
     shared_I: intermediate width of the shared expert (None: no shared expert).
@@ -350,8 +410,8 @@ class MoELoRABlock:
     a_gu, b_gu, w_d [H, shared_I], a_d, b_d. full_ft and recompute apply to
     the routed and the shared experts alike."""
 
-    def __init__(self, shape: Shape, router: str, shared_I: int | None = None, device="cuda",
-                 full_ft: bool = False, recompute: bool = False):
+    def __init__(self, shape: Shape, router: str | GroupedRouter, shared_I: int | None = None,
+                 device="cuda", full_ft: bool = False, recompute: bool = False):
         self.shape, self.shared_I = shape, shared_I
         self.routed = MoELoRALayer(shape, router, device, full_ft, recompute)
         T, H, E = shape.T, shape.H, shape.E
@@ -367,9 +427,15 @@ class MoELoRABlock:
             self.shared_offsets = torch.tensor([0, T], device=device, dtype=torch.int32)
             self.shared_dx = torch.empty(T, H, device=device, dtype=shape.torch_dtype)
 
-    def forward(self, x, w_r, weights: dict, shared_weights: dict | None = None, stream=None):
+    def _grad_buffers(self):
+        shared = [] if self.shared is None else [*self.shared.grads.values(),
+                                                 *(self.shared.base_grads or {}).values()]
+        return self.routed._grad_buffers() + shared
+
+    def forward(self, x, w_r, weights: dict, shared_weights: dict | None = None, stream=None,
+                route_bias=None):
         moe_router_fwd(x, w_r, self.logits, self.ws_router, stream)
-        y = self.routed.forward(x, self.logits, weights, stream)
+        y = self.routed.forward(x, self.logits, weights, stream, route_bias)
         if self.shared is not None:
             L, sh = self.shared, self.shared_shape
             fwd = moe_grouped_lora_fwd_lean if L.recompute else moe_grouped_lora_fwd
@@ -400,12 +466,13 @@ class MoELoRABlock:
         moe_accumulate(self.shared_dx, dx, stream)
         return dx, dl, g, {n: v[0] for n, v in L.grads.items()}
 
-    def step(self, x, w_r, dy, weights: dict, shared_weights: dict | None = None, stream=None):
-        self.forward(x, w_r, weights, shared_weights, stream)
+    def step(self, x, w_r, dy, weights: dict, shared_weights: dict | None = None, stream=None,
+             route_bias=None):
+        self.forward(x, w_r, weights, shared_weights, stream, route_bias)
         return self.backward(dy, x, w_r, weights, shared_weights, stream)
 
 
-class MoELoRASublayer:
+class MoELoRASublayer(_Clipped):
     """A MoE block on the residual stream h [T, H]:
 
         h1 = h + dropout(attn w_o^T + b_o)        (attn_width: columns of attn; None: h1 = h)
@@ -418,7 +485,7 @@ class MoELoRASublayer:
     `train`, the names to differentiate (None: all). The two dropouts draw the masks of
     offset + site and offset + site + 1, so a step's sublayers take every second site."""
 
-    def __init__(self, shape: Shape, router: str, shared_I: int | None = None,
+    def __init__(self, shape: Shape, router: str | GroupedRouter, shared_I: int | None = None,
                  attn_width: int | None = None, attn_bias: bool = False, norm: str = "rms",
                  post: str = "none", gate: str = "none", gate_sigmoid: bool = False,
                  alpha: float = 1.0, eps: float = 1e-5, weight_shift: float = 0.0,
@@ -455,12 +522,15 @@ class MoELoRASublayer:
                 s["b_o"] = (self.proj.N,)
         return s
 
+    def _grad_buffers(self):
+        return [*self.grads.values(), *self.block._grad_buffers()]
+
     def _sub(self, d: dict, desc: Residual, prefix="") -> dict:
         """The entries of d (vectors, or with prefix "d" gradients) that desc's call takes."""
         return {prefix + n: d[prefix + n] for n in desc.param_shapes() if prefix + n in d}
 
     def forward(self, h, params: dict, w_r, weights: dict, shared_weights: dict | None = None,
-                attn=None, rng=None, site: int = 0, stream=None):
+                attn=None, rng=None, site: int = 0, stream=None, route_bias=None):
         """h2; h and attn are kept by the caller for the backward."""
         self.stream_in = h
         if self.proj is not None:
@@ -472,7 +542,7 @@ class MoELoRASublayer:
             self.stream_in = self.h1
         moe_residual_norm_fwd(self.before, self.stream_in, None, self._sub(params, self.before),
                               None, self.x, self.stats_before, stream=stream)
-        self.y = self.block.forward(self.x, w_r, weights, shared_weights, stream)
+        self.y = self.block.forward(self.x, w_r, weights, shared_weights, stream, route_bias)
         moe_residual_norm_fwd(self.after, self.stream_in, self.y, self._sub(params, self.after),
                               self.h2, None, self.stats_after, rng=rng, site=site + 1,
                               stream=stream)
@@ -506,9 +576,132 @@ class MoELoRASublayer:
         return self.dh, dattn, lora, shared
 
     def step(self, h, dh2, params: dict, w_r, weights: dict, shared_weights: dict | None = None,
-             attn=None, rng=None, site: int = 0, stream=None):
-        self.forward(h, params, w_r, weights, shared_weights, attn, rng, site, stream)
+             attn=None, rng=None, site: int = 0, stream=None, route_bias=None):
+        self.forward(h, params, w_r, weights, shared_weights, attn, rng, site, stream, route_bias)
         return self.backward(dh2, params, w_r, weights, shared_weights, attn, rng, site, stream)
+
+
+def mx_weights(w_gu, w_d, stream=None) -> dict:
+    """Merged expert weights w_gu [E, 2I, H] and w_d [E, H, I] (or one expert's, without E) in 4
+    bits: {"w_gu", "s_gu", "w_d", "s_d"}, codes and scales, for MoEMXLayer."""
+    out = {}
+    for n, w in (("gu", w_gu), ("d", w_d)):
+        u8 = dict(device=w.device, dtype=torch.uint8)
+        out["w_" + n] = torch.empty(*w.shape[:-1], w.shape[-1] // 2, **u8)
+        out["s_" + n] = torch.empty(*w.shape[:-1], mx_scale_cols(w.shape[-1]), **u8)
+        moe_mx_quantize(w, out["w_" + n], out["s_" + n], "fp4", stream)
+    return out
+
+
+class _MXExperts:
+    """gate, up and down of one expert or of E, over T tokens' 8-bit rows in token order."""
+
+    def __init__(self, T, H, I, dtype, E, k, device):
+        self.up = MXLinear(T, H, I, "fp8", "mx8", "swiglu", E, k, gather=E > 0)
+        self.down = MXLinear(T, I, H, "fp8", dtype, E=E, k=k)
+        u8 = dict(device=device, dtype=torch.uint8)
+        self.act = torch.empty(T * k, I, **u8)
+        self.act_scales = torch.empty(T * k, mx_scale_cols(I), **u8)
+        ws = max(moe_mx_linear_workspace_bytes(s) for s in (self.up, self.down))
+        self.ws = torch.empty(max(ws, 1), **u8)
+
+    def __call__(self, x, x_scales, w, y, rows, offsets, stream):
+        moe_mx_linear(self.up, x, x_scales, w["w_gu"], w["s_gu"], self.act, self.ws,
+                      y_scales=self.act_scales, rows=rows, offsets=offsets, stream=stream)
+        moe_mx_linear(self.down, self.act, self.act_scales, w["w_d"], w["s_d"], y, self.ws,
+                      offsets=offsets, stream=stream)
+
+
+class MoEMXLayer:
+    """Forward of an exported layer: weights in 4 bits, activations in 8, both microscaled, sums in
+    float32. shape.dtype ("bf16" or "f16") is that of x and y; shape.r is not used. H and I are
+    multiples of 32. Layers of other T share the weights; the buffers are the layer's own.
+
+    shared_I: width of an always-on shared expert, whose weights are mx_weights of its own."""
+
+    def __init__(self, shape: Shape, router: str | GroupedRouter, shared_I: int | None = None,
+                 device="cuda"):
+        if shape.dtype not in ("bf16", "f16"):
+            raise ValueError(f"results have 16 bits: dtype bf16 or f16, got {shape.dtype}")
+        _check_router(router, shape)
+        T, H, E, k, N, dt = shape.T, shape.H, shape.E, shape.k, shape.N, shape.torch_dtype
+        self.shape, self.router = shape, router
+        z = lambda *s, dtype=dt: torch.empty(s, device=device, dtype=dtype)  # noqa: E731
+        i32, u8 = torch.int32, torch.uint8
+        self.experts = _MXExperts(T, H, shape.I, shape.dtype, E, k, device)
+        self.shared = None
+        if shared_I:
+            self.shared = _MXExperts(T, H, int(shared_I), shape.dtype, 0, 1, device)
+            self.shared_y = z(T, H)
+        self.x_codes, self.x_scales = z(T, H, dtype=u8), z(T, mx_scale_cols(H), dtype=u8)
+        self.topk_ids, self.topk_w = z(T, k, dtype=i32), z(T, k, dtype=torch.float32)
+        self.counts, self.offsets = z(E, dtype=i32), z(E + 1, dtype=i32)
+        self.sorted_pair, self.inv_pos = z(N, dtype=i32), z(N, dtype=i32)
+        self.ws_perm = z(max(moe_workspace_bytes(shape)[2], 1), dtype=u8)
+        self.y_exp, self.y = z(N, H), z(T, H)
+
+    def forward(self, x, logits, weights: dict, shared_weights: dict | None = None, stream=None,
+                route_bias=None):
+        """y from the rows x [T, H]; x None: from x_codes and x_scales, which the caller has filled
+        (moe_residual_norm_mx_fwd)."""
+        s = self.shape
+        if x is not None:
+            moe_mx_quantize(x, self.x_codes, self.x_scales, "fp8", stream)
+        _route(self.router, logits, self.topk_ids, self.topk_w, route_bias, stream)
+        moe_permute(s, self.topk_ids, None, self.counts, self.offsets, self.sorted_pair,
+                    self.inv_pos, None, self.ws_perm, stream)
+        self.experts(self.x_codes, self.x_scales, weights, self.y_exp, self.sorted_pair,
+                     self.offsets, stream)
+        moe_unpermute_combine(s, self.y_exp, self.inv_pos, self.topk_w, self.y, stream)
+        if self.shared is not None:
+            self.shared(self.x_codes, self.x_scales, shared_weights, self.shared_y, None, None,
+                        stream)
+            moe_accumulate(self.shared_y, self.y, stream)
+        return self.y
+
+
+class MoEMXSublayer:
+    """An exported layer on the residual stream h [T, H]:
+
+        h2 = h + alpha * g * post(layer(norm(h)))
+
+    norm, post, gate, gate_sigmoid, alpha, eps and weight_shift as in MoELoRASublayer, shared_I as
+    in MoEMXLayer; param_shapes() names the vectors in `params`. w_r [E, H] is the router's
+    projection, of the stream's dtype."""
+
+    def __init__(self, shape: Shape, router: str | GroupedRouter, shared_I: int | None = None,
+                 norm: str = "rms", post: str = "none", gate: str = "none",
+                 gate_sigmoid: bool = False, alpha: float = 1.0, eps: float = 1e-5,
+                 weight_shift: float = 0.0, device="cuda"):
+        if norm == "none":
+            raise ValueError("the layer's input needs a norm: \"rms\" or \"layer\"")
+        T, H, E, dt = shape.T, shape.H, shape.E, shape.torch_dtype
+        self.shape = shape
+        self.layer = MoEMXLayer(shape, router, shared_I, device)
+        common = dict(eps=eps, weight_shift=weight_shift)
+        self.before = Residual(T, H, shape.dtype, pre=norm, **common)
+        self.after = Residual(T, H, shape.dtype, post=post, pre="none", gate=gate,
+                              gate_sigmoid=gate_sigmoid, alpha=alpha, **common)
+        z = lambda *s, dtype=dt: torch.empty(s, device=device, dtype=dtype)  # noqa: E731
+        self.x, self.h2 = z(T, H), z(T, H)
+        self.logits = z(T, E, dtype=torch.float32)
+        self.ws_router = z(max(moe_router_workspace_bytes(T, H, E, shape.dtype), 1),
+                           dtype=torch.uint8)
+
+    def param_shapes(self) -> dict:
+        return {**self.before.param_shapes(), **self.after.param_shapes()}
+
+    def forward(self, h, params: dict, w_r, weights: dict, shared_weights: dict | None = None,
+                stream=None, route_bias=None):
+        layer = self.layer
+        sub = lambda d: {n: params[n] for n in d.param_shapes()}  # noqa: E731
+        moe_residual_norm_mx_fwd(self.before, h, None, sub(self.before), None, layer.x_codes,
+                                 layer.x_scales, None, x_out=self.x, stream=stream)
+        moe_router_fwd(self.x, w_r, self.logits, self.ws_router, stream)
+        y = layer.forward(None, self.logits, weights, shared_weights, stream, route_bias)
+        moe_residual_norm_fwd(self.after, h, y, sub(self.after), self.h2, None, None,
+                              stream=stream)
+        return self.h2
 
 
 class MoELoRAFunction(torch.autograd.Function):
@@ -517,7 +710,8 @@ class MoELoRAFunction(torch.autograd.Function):
     which case their gradients are computed too."""
 
     @staticmethod
-    def forward(ctx, x, logits, w_gu, a_gu, b_gu, w_d, a_d, b_d, router, k, lora_scale=1.0):
+    def forward(ctx, x, logits, w_gu, a_gu, b_gu, w_d, a_d, b_d, router, k, lora_scale=1.0,
+                route_bias=None):
         T, H = x.shape
         E, r = logits.shape[1], a_gu.shape[1]
         I = w_gu.shape[1] // 2
@@ -527,7 +721,7 @@ class MoELoRAFunction(torch.autograd.Function):
         layer = MoELoRALayer(shape, router, device=x.device, full_ft=full)
         weights = dict(zip(WEIGHT_NAMES, (w_gu, a_gu, b_gu, w_d, a_d, b_d)))
         x = x.contiguous()
-        y = layer.forward(x, logits.contiguous(), weights).clone()
+        y = layer.forward(x, logits.contiguous(), weights, route_bias=route_bias).clone()
         ctx.layer, ctx.weights, ctx.logits, ctx.x = layer, weights, logits.contiguous(), x
         return y
 
@@ -539,4 +733,4 @@ class MoELoRAFunction(torch.autograd.Function):
         dw_gu = bg["dw_gu"].clone() if bg is not None and ctx.needs_input_grad[2] else None
         dw_d = bg["dw_d"].clone() if bg is not None and ctx.needs_input_grad[5] else None
         return (dx.clone(), dl.clone(), dw_gu, g["da_gu"].clone(), g["db_gu"].clone(), dw_d,
-                g["da_d"].clone(), g["db_d"].clone(), None, None, None)
+                g["da_d"].clone(), g["db_d"].clone(), None, None, None, None)
