@@ -318,6 +318,18 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
   }
   wait_vmcnt<IN_FLIGHT + AI + WI>();
   barrier_lds();
+  // a wave whose rows or columns lie past the end (an expert's last tile) only brings its share
+  if (wm * WM >= t.rows || n0 + wn * out_cols<WN, SWIGLU>() >= p.N) {
+    for (int s = 0, at = 0; s < stages; ++s, at = at + 1 == NST ? 0 : at + 1) {
+      wait_vmcnt<IN_FLIGHT>();
+      barrier_lds();
+      issue_scales(s + NST);
+#pragma unroll
+      for (int i = 0; i < AI + WI; ++i) issue(s + NST, at, i);
+    }
+    wait_vmcnt<0>();
+    return;
+  }
   load_scales(0, c0);
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) load(0, first, i, x0);
