@@ -564,7 +564,8 @@ moe_status moe_linear_bwd(const moe_linear_shape *shape, const void *dy, const v
  * the call returns.
  * Errors: an unknown dtype, n outside [0, 2^40], a tensor not aligned to its type, max_norm < 0
  * or not finite, eps <= 0 or not finite, a dst that overlaps another dst, another tensor's src or
- * the norm; norm or ws (16-byte boundary) overlapping a src. */
+ * the norm; norm or ws (16-byte boundary) overlapping a src; MOE_ERR_UNSUPPORTED: more than 2^20
+ * tensors. */
 typedef struct {
   const void *src;
   void *dst;

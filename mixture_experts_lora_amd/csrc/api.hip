@@ -1209,6 +1209,7 @@ namespace {
 // clip: every tensor has a dst
 moe_status check_grads(int32_t count, const moe_grad* grads, bool clip) {
   if (count < 0) return fail(MOE_ERR_INVALID_ARG, "count < 0");
+  if (count > (1 << 20)) return fail(MOE_ERR_UNSUPPORTED, "more than 2^20 gradients");
   if (count > 0) CHECK_PTR(grads);
   for (int32_t i = 0; i < count; ++i) {
     const moe_grad& g = grads[i];
