@@ -560,8 +560,8 @@ moe_status moe_linear_bwd(const moe_linear_shape *shape, const void *dy, const v
  * norm over all of them. src and dst (may be src; not read by moe_grad_norm) hold n elements of
  * dtype; n may be 0. A NaN norm makes every gradient NaN; an infinite one, zeros (NaN where the
  * gradient is not finite). dst = src is left untouched where nothing is clipped. Sums have an
- * order that depends on the sizes alone, so results repeat bit for bit. The list is read before
- * the call returns.
+ * order that depends on the sizes and on which addresses are multiples of 16 alone, so results
+ * repeat bit for bit. The list is read before the call returns.
  * Errors: an unknown dtype, n outside [0, 2^40], a tensor not aligned to its type, max_norm < 0
  * or not finite, eps <= 0 or not finite, a dst that overlaps another dst, another tensor's src or
  * the norm; norm or ws (16-byte boundary) overlapping a src; MOE_ERR_UNSUPPORTED: more than 2^20

@@ -122,6 +122,11 @@ __device__ __forceinline__ constexpr int row_bytes_of(int k) {
 }
 
 // ------------------------------------------------------------------ many rows: tiles through LDS
+// Bound by power and by what stands outside the loop: 32 experts, 8192 tokens of 4, 2880 -> 2 x 2880,
+// 8-bit result, 521 us in all (2.1 PFLOP/s), of which 9.5 us a tile, 13 tiles a CU, are the tile's
+// lookup, its first stages and its epilogue; the loop runs at 2.7 PFLOP/s, where products of such
+// data from registers alone reach 3.6 to 4.1. Dense, 4 bits by 4, 8192 x 4096 x 2880: 64 to 70 us.
+//
 // A stage is 128 elements of every row; NST stages have places in LDS. 16-byte chunk c of row r is
 // kept at c ^ swizzle(r), so that 16 lanes of a fragment read (16 rows, one chunk) touch every bank
 // once.
@@ -437,7 +442,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
 // LDS, adding in order. Weights come straight from HBM into the matrix cores' registers, each byte once
 // for 16 rows, in batches of four steps of 128 elements with the next batch on its way: a row's four
 // steps are 256 bytes of codes and 16 of scales. Loads go by buffer resources, whose bounds make
-// zeros of steps past the operand; what a batch reads behind its own steps is not multiplied.
+// zeros of steps past the operand; what a batch reads behind its own steps is not multiplied. One
+// token of 4 of 32 experts, 2880 -> 2 x 2880, 10 us, 3.5 TB/s: bound by the latency of 23 steps.
 constexpr int kSmallRows = 16, kSmallWaves = 4, kBatch = 4;
 
 // Output columns of a block: as few as there can be, so that even one token's experts give every CU
