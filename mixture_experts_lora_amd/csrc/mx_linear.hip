@@ -365,18 +365,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
   }
   wait_vmcnt<0>();
 
-  // Lane (r, g) holds row r's columns 8 q + 4 g + i at register 4 q + i; after swapping halves with
-  // its partner it holds the 16 columns from 16 g on.
-  auto columns = [&](const f32x16& c, float (&v)[16]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[4 * q + i]),
-                                                        __float_as_uint(c[4 * (q + 2) + i]), false, false);
-        v[8 * q + i] = __uint_as_float(x[0]);
-        v[8 * q + 4 + i] = __uint_as_float(x[1]);
-      }
+  // Lane (r, g) holds row r's columns 8 q + 4 g + i at register 4 q + i. Rounded to the output's type
+  // these are words of two or four columns; after swapping halves of them with its partner it holds
+  // the 16 columns from 16 g on. (Swapped before
+  // the rounding and SwiGLU, as many words more: the experts above 517 us against 513.)
+  auto swap = [](uint32_t a, uint32_t b, uint32_t& lo, uint32_t& hi) __attribute__((always_inline)) {
+    const auto x = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    lo = x[0];
+    hi = x[1];
   };
 
   constexpr int OF = SWIGLU ? NF / 2 : NF;  // fragments of output columns
@@ -387,32 +383,31 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
     const int64_t row = t.row0 + local;
 #pragma unroll
     for (int f = 0; f < OF; ++f) {
-      float v[16];
-      columns(acc[f][m], v);
-      if constexpr (SWIGLU) {
-        float u[16];
-        columns(acc[f + NF / 2][m], u);
+      float lo[8], hi[8];  // q = 0 and 1, q = 2 and 3
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = swiglu(v[i], u[i]);
+      for (int i = 0; i < 8; ++i) {
+        lo[i] = acc[f][m][i];
+        hi[i] = acc[f][m][8 + i];
+        if constexpr (SWIGLU) {
+          lo[i] = swiglu(lo[i], acc[f + NF / 2][m][i]);
+          hi[i] = swiglu(hi[i], acc[f + NF / 2][m][8 + i]);
+        }
       }
       const int base = n0 + wn * (OF * 32) + f * 32, col = base + 16 * g;
       if constexpr (OUT == kMxOut8) {
         uint32_t amax = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
-        const auto x = __builtin_amdgcn_permlane32_swap(amax, amax, false, false);
-        amax = max(static_cast<uint32_t>(x[0]), static_cast<uint32_t>(x[1]));
-        const uint32_t sb = mx_scale_of<MOE_MX_FP8>(amax);
-        float lo[8], hi[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          lo[i] = v[i];
-          hi[i] = v[8 + i];
-        }
+        for (int i = 0; i < 8; ++i)
+          amax = max(amax, max(__float_as_uint(lo[i]) & 0x7fffffffu, __float_as_uint(hi[i]) & 0x7fffffffu));
+        uint32_t a0, a1;
+        swap(amax, amax, a0, a1);
+        const uint32_t sb = mx_scale_of<MOE_MX_FP8>(max(a0, a1));
         const uint2 c0 = mx_encode8<MOE_MX_FP8>(lo, sb), c1 = mx_encode8<MOE_MX_FP8>(hi, sb);
+        uint4 out;
+        swap(c0.x, c1.x, out.x, out.y);
+        swap(c0.y, c1.y, out.z, out.w);
         if (there && base < p.N) {
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + row * p.N + col) =
-              make_uint4(c0.x, c0.y, c1.x, c1.y);
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + row * p.N + col) = out;
           if (g == 0) {
             const int cols = static_cast<int>(mx_scale_cols(p.N));
             uint8_t* s = p.y_scales + row * cols;
@@ -422,16 +417,18 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
           }
         }
       } else {
+        Row8<Out16<OUT>> w0, w1;
+        w0.set(lo);
+        w1.set(hi);
+        uint4 out[2];
+        swap(w0.a.x, w1.a.x, out[0].x, out[0].z);
+        swap(w0.a.y, w1.a.y, out[0].y, out[0].w);
+        swap(w0.a.z, w1.a.z, out[1].x, out[1].z);
+        swap(w0.a.w, w1.a.w, out[1].y, out[1].w);
         Out16<OUT>* y = static_cast<Out16<OUT>*>(p.y) + row * p.N + col;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float o[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = v[8 * h + i];
-          Row8<Out16<OUT>> r8;
-          r8.set(o);
-          if (there && col + 8 * h < p.N) r8.store(y + 8 * h);
-        }
+        for (int h = 0; h < 2; ++h)
+          if (there && col + 8 * h < p.N) *reinterpret_cast<uint4*>(y + 8 * h) = out[h];
       }
     }
   }
