@@ -123,7 +123,7 @@ __device__ __forceinline__ constexpr int row_bytes_of(int k) {
 
 // ------------------------------------------------------------------ many rows: tiles through LDS
 // Bound by power and by what stands outside the loop: 32 experts, 8192 tokens of 4, 2880 -> 2 x 2880,
-// 8-bit result, 521 us in all (2.1 PFLOP/s), of which 9.5 us a tile, 13 tiles a CU, are the tile's
+// 8-bit result, 513 us in all (2.1 PFLOP/s), of which 9.5 us a tile, 13 tiles a CU, are the tile's
 // lookup, its first stages and its epilogue; the loop runs at 2.7 PFLOP/s, where products of such
 // data from registers alone reach 3.6 to 4.1. Dense, 4 bits by 4, 8192 x 4096 x 2880: 64 to 70 us.
 //
@@ -172,7 +172,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
   constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
   constexpr int MF = WM / 32, NF = WN / 32;
   constexpr int AB = row_bytes_of<AF>(128), WB = 64;
-  constexpr int A_BYTES = BM * AB, W_BYTES = BN * WB, STAGE = A_BYTES + W_BYTES;
+  // places for w's rows in whole instructions a wave; those past BN are not filled
+  constexpr int BNL = (BN + NW * (1024 / WB) - 1) / (NW * (1024 / WB)) * (NW * (1024 / WB));
+  constexpr int A_BYTES = BM * AB, W_BYTES = BNL * WB, STAGE = A_BYTES + W_BYTES;
   constexpr int S_BYTES = (BM + BN) * 16;  // scales of 512 elements, in two places
   constexpr int AI = A_BYTES / 1024 / NW, WI = W_BYTES / 1024 / NW;
   static_assert(AI * NW * 1024 == A_BYTES && WI * NW * 1024 == W_BYTES, "whole instructions a wave");
@@ -242,7 +244,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
       dma16_at(st + (wave + NW * i) * 1024, ra, voa[i < AI ? i : 0] | end, static_cast<uint32_t>(s) * AB);
     } else {
       i -= AI;
-      const uint32_t end = w_row - s * WB > byte_w ? 0u : kOOB;
+      uint32_t end = w_row - s * WB > byte_w ? 0u : kOOB;
+      if (BN != BNL && (wave + NW * i) * (1024 / WB) >= BN) end = kOOB;
       dma16_at(st + A_BYTES + (wave + NW * i) * 1024, rw,
                (vow + static_cast<uint32_t>(weight_row(NW * (1024 / WB) * i)) * w_row) | end,
                static_cast<uint32_t>(s) * WB);
@@ -367,8 +370,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
 
   // Lane (r, g) holds row r's columns 8 q + 4 g + i at register 4 q + i. Rounded to the output's type
   // these are words of two or four columns; after swapping halves of them with its partner it holds
-  // the 16 columns from 16 g on. (Swapped before
-  // the rounding and SwiGLU, as many words more: the experts above 517 us against 513.)
+  // the 16 columns from 16 g on. (Swapped before the rounding and SwiGLU, two or four times the words:
+  // the experts above 517 us against 513.)
   auto swap = [](uint32_t a, uint32_t b, uint32_t& lo, uint32_t& hi) __attribute__((always_inline)) {
     const auto x = __builtin_amdgcn_permlane32_swap(a, b, false, false);
     lo = x[0];
@@ -615,7 +618,11 @@ __global__ __launch_bounds__(kSmallWaves * 64) void mx_rows_kernel(MxGemm p) {
 //  rows each) 122.6 / 143.0, 768 tokens 114.7 / 103.5. 128 x 128 against 64 x 128: 1024 rows (184
 //  tiles) 20.1 / 21.4, 512 rows 17.8 / 15.6; the experts, 512 tokens (64 rows each) 93.5 / 111.8,
 //  256 tokens 81 / 75. (128 x 256 lies within 7 % of one of the others everywhere.)
-constexpr int kRowsBlocks = 768, kTilesToFill = 192;
+//  256 x 192 in the place of 256 x 256 where the last round of tiles would leave many CUs idle, so
+//  that rounds times columns fall by a tenth or more (without SwiGLU, whose halves of 96 rows no
+//  instruction's step divides): 8192 rows of 4096 -> 2880 (480 tiles for 384) 87.3 us against 97.6,
+//  in 4 bits 69.5 / 74.2; 2048 tokens of 4 of 32 experts, 2880 -> 2880, 94.4 / 106.3.
+constexpr int kCUs = 256, kRowsBlocks = 3 * kCUs, kTilesToFill = kCUs * 3 / 4;
 
 // Calls go with the format of a, the output and SwiGLU as constants.
 template <typename F>
@@ -672,6 +679,11 @@ hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const u
                          dim3(static_cast<unsigned>(tiles(BM, out_cols<BN, GLU>()))),
                          dim3((BM / WM) * (BN / WN) * 64), 0, st, p);
     };
+    // rounds of a tile a CU that 256 x bn tiles take, in columns
+    auto rounds = [&](int bn) {
+      const int64_t n = (p.M + 255) / 256 * static_cast<int64_t>((s.N + bn - 1) / bn);
+      return (n + kCUs - 1) / kCUs * bn;
+    };
     auto fills = [&](int bm, int bn) {
       const int cols = GLU ? bn / 2 : bn;
       return p.M >= bm / 2 * static_cast<int64_t>(experts) &&
@@ -682,6 +694,10 @@ hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const u
       hipLaunchKernelGGL((mx_rows_kernel<AF, OUT, GLU>),
                          dim3(static_cast<unsigned>(tiles(kSmallRows, small_cols<OUT>()))),
                          dim3(kSmallWaves * 64), 0, st, p);
+    } else if (!GLU && fills(256, 256) && rounds(192) * 10 < rounds(256) * 9) {
+      if constexpr (!GLU)
+        tiled(integral_constant<int, 256>(), integral_constant<int, 192>(), integral_constant<int, 64>(),
+              integral_constant<int, 96>(), integral_constant<int, 3>());
     } else if (fills(256, 256)) {
       tiled(integral_constant<int, 256>(), integral_constant<int, 256>(), integral_constant<int, 64>(),
             integral_constant<int, 128>(), integral_constant<int, 3>());

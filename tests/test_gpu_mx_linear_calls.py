@@ -33,6 +33,15 @@ def test_large_tiles_of_experts(T, K, N, E, k, skew, fmt, gather):
     check(T, K, N // 64 * 32, fmt, "mx8", "swiglu", E, k, gather, skew=skew)
 
 
+@pytest.mark.parametrize("T,K,N,E,k", [(2300, 160, 8352, 0, 1), (2300, 416, 8360, 0, 1),
+                                       (1500, 544, 6496, 5, 2)])
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("out", ["bf16", "mx8"])
+def test_tiles_of_192_columns(T, K, N, E, k, fmt, out):
+    """Sizes whose last round of tiles of 256 columns would be mostly empty."""
+    check(T, K, N // 32 * 32 if out == "mx8" else N, fmt, out, "none", E, k, gather=E > 0)
+
+
 def _product(mel, T, K, N, E=0, k=1, out="bf16", act="none", gather=False, fmt="fp8", seed=0):
     """(run, y, y_scales, tensors) of a product with its own buffers."""
     rng = np.random.default_rng(seed + T + N)
