@@ -167,8 +167,10 @@ moe_status moe_route_bwd(const float *logits, const int32_t *topk_ids, const flo
  *   topk_ids: the k largest v within them, descending; ties, of groups too, to the lower index
  *   topk_w_j = scale * s_j, or with renorm scale * s_j / (sum of the chosen s)
  * The bias decides the choice only. v is formed in float64 and compared to 2^-41 of its value; NaN
- * ranks below -infinity. Experts masked by a logit of -infinity are chosen only where the others
- * do not suffice and weigh 0, as does every expert of a row of nothing else. */
+ * ranks below -infinity. An expert masked by a logit of -infinity has v = -infinity whatever its
+ * bias: it is chosen only where the others in the kept groups do not suffice, and weighs 0, as does
+ * every expert of a row of nothing else. Groups whose sum is -infinity come after the others, by
+ * their largest v. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
 typedef struct {

@@ -1,6 +1,7 @@
 // Routing with a bias for balance and groups of experts, and its backward.
 //
 //   s_i = softmax(l)_i or sigmoid(l_i)      v_i = s_i + b_i        (b only decides the choice)
+//   v_i = -infinity where l_i is: a masked expert stays behind the others whatever its bias
 //   a group's score: the sum of its one or two largest v; the best groups stay
 //   the k largest v of those are chosen, in order; ties go to the lower index
 //   w_j = c s_j, or c s_j / sum of the chosen s
@@ -183,8 +184,8 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = static_cast<double>(lg[i]);
   } else {
-    // sigmoid(l) = 1 / (1 + e^-l); softmax from l - max. -infinity scores 0 (as every expert of a
-    // row of nothing else), NaN stays NaN.
+    // sigmoid(l) = 1 / (1 + e^-l); softmax from l - max. A logit of -infinity adds nothing to the sum
+    // and gives v = -infinity after the bias, NaN stays NaN.
     const double shift = sigmoid || mx == -INFINITY ? 0.0 : static_cast<double>(mx);
     const double sign = sigmoid ? -1.0 : 1.0, one = sigmoid ? 1.0 : 0.0;
     double sum = 0.0;
@@ -196,10 +197,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
     }
     if (sigmoid) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        v[i] = route_rcp(v[i]);
-        if (lg[i] == -INFINITY) v[i] = 0.0;
-      }
+      for (int i = 0; i < NV; ++i) v[i] = route_rcp(v[i]);
     } else {
       sum = lanes_sum<L>(sum);
       const double inv = sum > 0.0 ? route_rcp(sum) : 0.0;  // sum >= 1 or 0
@@ -215,6 +213,9 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
         v[i] += static_cast<double>(bias[min(lane + L * i, E - 1)]);
       }
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (lg[i] == -INFINITY) v[i] = -INFINITY;
   }
   double key[NV];
 #pragma unroll
@@ -268,6 +269,17 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
     for (int h = 0; h < r.groups; ++h) {
       const double o = sc[h];
       rank += o > mine || (o == mine && h < group);
+    }
+    // Sums of -infinity (fewer than two free experts): the largest v decides between those. Lanes of a
+    // token are in one wave, and rows without masks skip this.
+    if (r.group_top == 2 && __any(head && mine == -INFINITY)) {
+      const int first = threadIdx.x % kWave / L * L;
+      rank = 0;
+      for (int h = 0; h < r.groups; ++h) {
+        const double o = sc[h], oa = __shfl(a, first + h * S, kWave);
+        const bool tie = o == mine, best = tie && o == -INFINITY && oa != a;
+        rank += best ? oa > a : o > mine || (tie && h < group);
+      }
     }
     // bit g S of this token's lanes: group g stays
     uint64_t kept = __ballot(head && rank < r.topk_groups);

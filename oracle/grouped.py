@@ -17,16 +17,19 @@ def scores(logits, score):
 
 
 def choose(logits, k, score, groups=1, topk_groups=1, group_top=2, bias=None):
-    """[T, k] experts, one token and one pick at a time."""
+    """[T, k] experts, one token and one pick at a time. A logit of -inf stays behind the others
+    whatever its bias; groups whose sum such experts make -inf go by their best."""
     v = scores(logits, score)
     if bias is not None:
         v = v + np.asarray(bias, np.float64)
+    v = np.where(np.isneginf(logits), -np.inf, v)
     T, E = v.shape
     size = E // groups
     ids = np.empty((T, k), np.int64)
     for t in range(T):
-        best = [sum(sorted(v[t, g * size:(g + 1) * size])[::-1][:group_top]) for g in range(groups)]
-        stay = sorted(range(groups), key=lambda g: (-best[g], g))[:topk_groups]
+        top = [sorted(v[t, g * size:(g + 1) * size])[::-1][:group_top] for g in range(groups)]
+        best = [(sum(x), x[0] if sum(x) == -np.inf else 0.0) for x in top]
+        stay = sorted(range(groups), key=lambda g: (-best[g][0], -best[g][1], g))[:topk_groups]
         free = [e for e in range(E) if e // size in stay]
         ids[t] = sorted(free, key=lambda e: (-v[t, e], e))[:k]
     return ids
