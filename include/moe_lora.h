@@ -167,10 +167,13 @@ moe_status moe_route_bwd(const float *logits, const int32_t *topk_ids, const flo
  *   topk_ids: the k largest v within them, descending; ties, of groups too, to the lower index
  *   topk_w_j = scale * s_j, or with renorm scale * s_j / (sum of the chosen s)
  * The bias decides the choice only. v is formed in float64 and compared to 2^-41 of its value; NaN
- * ranks below -infinity. An expert masked by a logit of -infinity has v = -infinity whatever its
- * bias: it is chosen only where the others in the kept groups do not suffice, and weighs 0, as does
- * every expert of a row of nothing else. Groups whose sum is -infinity come after the others, by
- * their largest v. */
+ * ranks below -infinity, and exponentials below e^-708 count as that. With bias NULL and groups = 1
+ * or group_top = 1 experts and groups go by their logits instead, which order them as v does and
+ * differ where scores saturate: a sigmoid of 45 comes before one of 40, whose v is the same (so a
+ * bias of zeros may choose otherwise than NULL).
+ * An expert masked by a logit of -infinity has v = -infinity whatever its bias: it is chosen only
+ * where the others in the kept groups do not suffice, and weighs 0, as does every expert of a row of
+ * nothing else. Groups whose sum is -infinity come after the others, by their largest v. */
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
 typedef struct {

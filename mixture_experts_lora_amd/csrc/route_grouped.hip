@@ -10,8 +10,9 @@
 // a token goes to, and sigmoid saturates in float32. A candidate is one positive double, its key:
 // v's bits in an order-preserving form, the lowest ten replaced by 1023 - index. The largest key is
 // then the largest v (to 2^-41 of it) with the lower index first, and a maximum is one v_max_f64.
-// Without a bias, and where no two scores are added, the logits order the experts as the scores do
-// and stand in for them.
+// Without a bias, and where no two scores are added, the logits stand in for the scores: they order the
+// experts as the scores do, and go on doing so where scores saturate or fall out of 64 bits, as the
+// choice of moe_route does.
 //
 // L lanes work on a token, 16 where there are many tokens of no more than 256 experts, so that a
 // wave's rounds of the top-k serve four tokens, else a wave; expert i belongs to lane i % L. The

@@ -22,6 +22,8 @@ def choose(logits, k, score, groups=1, topk_groups=1, group_top=2, bias=None):
     v = scores(logits, score)
     if bias is not None:
         v = v + np.asarray(bias, np.float64)
+    elif groups == 1 or group_top == 1:  # nothing is added: by the logits, which do not saturate
+        v = np.asarray(logits, np.float64)
     v = np.where(np.isneginf(logits), -np.inf, v)
     T, E = v.shape
     size = E // groups
