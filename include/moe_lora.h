@@ -171,6 +171,7 @@ moe_status moe_route_bwd(const float *logits, const int32_t *topk_ids, const flo
  * or group_top = 1 experts and groups go by their logits instead, which order them as v does and
  * differ where scores saturate: a sigmoid of 45 comes before one of 40, whose v is the same (so a
  * bias of zeros may choose otherwise than NULL).
+ * Logits of +infinity share a softmax in equal parts, and the others of the row have none of it.
  * An expert masked by a logit of -infinity has v = -infinity whatever its bias: it is chosen only
  * where the others in the kept groups do not suffice, and weighs 0, as does every expert of a row of
  * nothing else. Groups whose sum is -infinity come after the others, by their largest v. */

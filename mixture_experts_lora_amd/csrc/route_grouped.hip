@@ -135,8 +135,11 @@ __device__ __forceinline__ double route_rcp(double x) {
 // -infinity. Ratios are formed so that neither a large negative row nor an
 // overflowing exponential turns them into 0 / 0: with m the largest chosen logit,
 //   sigmoid(l) / sigmoid(m) = e^(l-m) (1 + e^m) / (1 + e^l)   for m <= 0,  sigmoid itself above.
-// A row whose chosen logits are all -infinity gets weights 0.
+// A row whose chosen logits are all -infinity gets weights 0; logits of +infinity share the whole of a
+// softmax.
 __device__ __forceinline__ float sigmoid_precise(float l) { return 1.0f / (1.0f + expf(-l)); }
+// e^(l - m) for l <= m, 1 where both are the same infinity
+__device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
 
 template <int L>
 __device__ __forceinline__ float renorm_weight(float l, bool act, int sigmoid, float c) {
@@ -144,7 +147,7 @@ __device__ __forceinline__ float renorm_weight(float l, bool act, int sigmoid, f
   if (m == -INFINITY) return 0.f;
   float e;
   if (!sigmoid) {
-    e = act ? expf(l - m) : 0.f;
+    e = act ? exp_below(l, m) : 0.f;
   } else if (m > 0.f) {
     e = act ? sigmoid_precise(l) : 0.f;
   } else {
@@ -185,14 +188,16 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = static_cast<double>(lg[i]);
   } else {
-    // sigmoid(l) = 1 / (1 + e^-l); softmax from l - max. A logit of -infinity adds nothing to the sum
-    // and gives v = -infinity after the bias, NaN stays NaN.
+    // sigmoid(l) = 1 / (1 + e^-l); softmax from l - max, whose exponential is 1 at the largest logit,
+    // an infinite one too. A logit of -infinity adds nothing to the sum and gives v = -infinity after
+    // the bias, NaN stays NaN.
     const double shift = sigmoid || mx == -INFINITY ? 0.0 : static_cast<double>(mx);
     const double sign = sigmoid ? -1.0 : 1.0, one = sigmoid ? 1.0 : 0.0;
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       v[i] = one + route_exp((static_cast<double>(lg[i]) - shift) * sign);
+      if (lg[i] == mx && !sigmoid) v[i] = 1.0;
       if (lg[i] == -INFINITY && !sigmoid) v[i] = 0.0;
       sum += v[i];
     }
@@ -201,7 +206,8 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
       for (int i = 0; i < NV; ++i) v[i] = route_rcp(v[i]);
     } else {
       sum = lanes_sum<L>(sum);
-      const double inv = sum > 0.0 ? route_rcp(sum) : 0.0;  // sum >= 1 or 0
+      // below 1 only where no logit is a number above -infinity
+      const double inv = sum >= 1.0 ? route_rcp(sum) : 0.0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) v[i] *= inv;
     }
@@ -321,9 +327,9 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_kernel(
     float s = 0.f;
     const float m = mx == -INFINITY ? 0.f : mx;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s += expf(lg[i] - m);
+    for (int i = 0; i < NV; ++i) s += exp_below(lg[i], m);
     s = lanes_sum<L>(s);
-    wj = s == 0.f ? 0.f : r.scale * (expf(chosen - m) / s);
+    wj = s == 0.f ? 0.f : r.scale * (exp_below(chosen, m) / s);
   }
   if (there && act) {
     ids[t * r.k + lane] = id;
@@ -401,7 +407,7 @@ __global__ __launch_bounds__(kRouteBlock) void route_grouped_bwd_kernel(
     float s = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      lg[i] = expf(lg[i] - m);
+      lg[i] = exp_below(lg[i], m);
       s += lg[i];
       dot = fmaf(lg[i], out[i], dot);
     }

@@ -4,16 +4,22 @@ from __future__ import annotations
 import numpy as np
 
 
+def _shares(x):
+    """exp(x) over its sum, row by row; -inf has no share, and +infs have all of it in equal parts."""
+    m = x.max(1, keepdims=True)
+    with np.errstate(invalid="ignore"):
+        e = np.where(np.isneginf(x), 0.0, np.where(x == m, 1.0, np.exp(x - m)))
+    s = e.sum(1, keepdims=True)
+    return np.divide(e, s, out=np.zeros_like(e), where=s != 0)
+
+
 def scores(logits, score):
     """softmax over each row, or sigmoid; a softmax row of -inf alone scores 0 everywhere."""
     l = np.asarray(logits, np.float64)
-    with np.errstate(over="ignore", invalid="ignore"):
-        if score == "sigmoid":
-            return 1.0 / (1.0 + np.exp(-l))
-        m = l.max(1, keepdims=True)
-        e = np.where(np.isneginf(m), 0.0, np.exp(l - np.where(np.isneginf(m), 0.0, m)))
-        s = e.sum(1, keepdims=True)
-        return np.divide(e, s, out=np.zeros_like(e), where=s != 0)
+    if score == "softmax":
+        return _shares(l)
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(-l))
 
 
 def choose(logits, k, score, groups=1, topk_groups=1, group_top=2, bias=None):
@@ -42,11 +48,7 @@ def weights(logits, ids, score, renorm, scale):
     l = np.take_along_axis(np.asarray(logits, np.float64), ids, 1)
     if not renorm:
         return scale * np.take_along_axis(scores(logits, score), ids, 1)
-    log_s = -np.logaddexp(0.0, -l) if score == "sigmoid" else l
-    m = log_s.max(1, keepdims=True)
-    e = np.exp(log_s - np.where(np.isneginf(m), 0.0, m))
-    s = e.sum(1, keepdims=True)
-    return scale * np.divide(e, s, out=np.zeros_like(e), where=s != 0)
+    return scale * _shares(-np.logaddexp(0.0, -l) if score == "sigmoid" else l)
 
 
 def weights_backward(logits, ids, dw, score, renorm, scale):
