@@ -765,6 +765,12 @@ class GradList:
     def _tensors(self):
         return self.grads if self.out is self.grads else self.grads + self.out
 
+    def clips(self, grads) -> bool:
+        """Whether the list is these very tensors in place, none of which has moved."""
+        return (self.out is self.grads and len(grads) == len(self.grads)
+                and all(a is b for a, b in zip(grads, self.grads))
+                and [t.data_ptr() for t in grads] == self._at)
+
     def _args(self, *others):
         if [t.data_ptr() for t in self._tensors()] != self._at:
             raise ValueError("a tensor of the list has moved: make a new GradList")

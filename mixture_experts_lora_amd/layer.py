@@ -98,10 +98,11 @@ class _Clipped:
     def clip_grads(self, max_norm: float, eps: float = 1e-6, stream=None):
         """Scales the layer's gradients in place by min(1, max_norm / (norm + eps)); returns norm
         (float32 [1], on the device), the 2-norm of all of them before."""
-        if not hasattr(self, "_clip"):
-            grads = GradList(self._grad_buffers())
-            u8, dev = torch.uint8, grads.grads[0].device
-            ws = torch.empty(max(moe_grad_norm_workspace_bytes(grads), 1), device=dev, dtype=u8)
+        bufs = self._grad_buffers()
+        if not hasattr(self, "_clip") or not self._clip[0].clips(bufs):
+            grads, dev = GradList(bufs), bufs[0].device
+            ws = torch.empty(max(moe_grad_norm_workspace_bytes(grads), 1), device=dev,
+                             dtype=torch.uint8)
             self._clip = grads, torch.empty(1, device=dev), ws
         grads, norm, ws = self._clip
         moe_grad_norm(grads, norm, ws, stream)

@@ -1,0 +1,39 @@
+"""clip_grads() of a layer whose gradient buffers were replaced or moved. A norm is within 2^-23 of the exact one, a clipped gradient within the roundings of
+test_gpu_layer_grouped.py."""
+import pytest
+import torch
+
+from gpu_util import say
+from test_gpu_layer_grouped import _clipped, _mel, _rand
+
+pytestmark = pytest.mark.gpu
+
+
+def _layer(mel, dtype="bf16"):
+    layer = mel.MoELoRALayer(mel.Shape(16, 64, 32, 8, 2, 4, dtype), "softmax_topk")
+    for i, g in enumerate(layer.grads.values()):
+        g.copy_(_rand(*g.shape, dtype=dtype, seed=i))
+    return layer
+
+
+@pytest.mark.parametrize("how", ["replaced", "moved"])
+def test_other_buffers_than_at_the_first_call(how):
+    mel = _mel()
+    say(f"[clip_grads] {how}")
+    layer = _layer(mel)
+    layer.clip_grads(1e9)
+    old = layer.grads["db_gu"]
+    fresh = _rand(*old.shape, seed=9) * 3
+    kept = old.clone()
+    if how == "replaced":
+        layer.grads["db_gu"] = fresh
+    else:
+        old_data = old.data
+        old.data = fresh
+    bufs = layer._grad_buffers()
+    before = [g.clone() for g in bufs]
+    norm = layer.clip_grads(0.5)
+    torch.cuda.synchronize()
+    assert layer.grads["db_gu"].data_ptr() == fresh.data_ptr()
+    _clipped(bufs, before, norm, 0.5)
+    assert torch.equal(old if how == "replaced" else old_data, kept)
