@@ -51,6 +51,8 @@ its 8-bit rows beside those that the router reads (moe_residual_norm_mx_fwd).
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import (GradList, GroupedRouter, LinearShape, MXLinear, Residual, Shape, moe_accumulate,
@@ -92,6 +94,16 @@ def _route_bwd(router, logits, topk_ids, d_topk_w, d_logits, stream):
         moe_route_bwd(logits, topk_ids, d_topk_w, topk_ids.shape[1], router, d_logits, stream)
 
 
+def _allocating(stream, device):
+    """Context in which torch allocates for `stream` (None: the current one): a block that the current
+    stream has just released may still be in use there."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
 class _Clipped:
     """clip_grads() of a layer that owns its gradients' buffers (_grad_buffers())."""
 
@@ -101,9 +113,10 @@ class _Clipped:
         bufs = self._grad_buffers()
         if not hasattr(self, "_clip") or not self._clip[0].clips(bufs):
             grads, dev = GradList(bufs), bufs[0].device
-            ws = torch.empty(max(moe_grad_norm_workspace_bytes(grads), 1), device=dev,
-                             dtype=torch.uint8)
-            self._clip = grads, torch.empty(1, device=dev), ws
+            with _allocating(stream, dev):
+                ws = torch.empty(max(moe_grad_norm_workspace_bytes(grads), 1), device=dev,
+                                 dtype=torch.uint8)
+                self._clip = grads, torch.empty(1, device=dev), ws
         grads, norm, ws = self._clip
         moe_grad_norm(grads, norm, ws, stream)
         moe_grad_clip(grads, norm, max_norm, eps, stream)

@@ -1,4 +1,5 @@
-"""clip_grads() of a layer whose gradient buffers were replaced or moved. A norm is within 2^-23 of the exact one, a clipped gradient within the roundings of
+"""clip_grads() of a layer whose gradient buffers were replaced or moved, and on another
+stream. A norm is within 2^-23 of the exact one, a clipped gradient within the roundings of
 test_gpu_layer_grouped.py."""
 import pytest
 import torch
@@ -37,3 +38,27 @@ def test_other_buffers_than_at_the_first_call(how):
     assert layer.grads["db_gu"].data_ptr() == fresh.data_ptr()
     _clipped(bufs, before, norm, 0.5)
     assert torch.equal(old if how == "replaced" else old_data, kept)
+
+
+def stream_of(t):
+    """The stream for which torch allocated a tensor's memory."""
+    at = t.data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return s["stream"]
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_memory_belongs_to_the_stream_of_the_call(raw):
+    mel = _mel()
+    say(f"[clip_grads stream] raw={raw}")
+    layer = _layer(mel)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    bufs = layer._grad_buffers()
+    before = [g.clone() for g in bufs]
+    torch.cuda.synchronize()
+    norm = layer.clip_grads(0.5, stream=side.cuda_stream if raw else side)
+    assert stream_of(norm) == side.cuda_stream
+    side.synchronize()
+    _clipped(bufs, before, norm, 0.5)
