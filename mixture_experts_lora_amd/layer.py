@@ -107,9 +107,11 @@ def _allocating(stream, device):
 class _Clipped:
     """clip_grads() of a layer that owns its gradients' buffers (_grad_buffers())."""
 
-    def clip_grads(self, max_norm: float, eps: float = 1e-6, stream=None):
+    def clip_grads(self, max_norm: float, eps: float = 1e-6, stream=None, norm=None):
         """Scales the layer's gradients in place by min(1, max_norm / (norm + eps)); returns norm
-        (float32 [1], on the device), the 2-norm of all of them before."""
+        (float32 [1], on the device), the 2-norm of all of them before. It is `norm` where that is
+        given, else a buffer of the layer, which the next call writes over. The workspace is the
+        layer's too: its calls have to be ordered, whichever streams they are on."""
         bufs = self._grad_buffers()
         if not hasattr(self, "_clip") or not self._clip[0].clips(bufs):
             grads, dev = GradList(bufs), bufs[0].device
@@ -117,7 +119,8 @@ class _Clipped:
                 ws = torch.empty(max(moe_grad_norm_workspace_bytes(grads), 1), device=dev,
                                  dtype=torch.uint8)
                 self._clip = grads, torch.empty(1, device=dev), ws
-        grads, norm, ws = self._clip
+        grads, own, ws = self._clip
+        norm = own if norm is None else norm
         moe_grad_norm(grads, norm, ws, stream)
         moe_grad_clip(grads, norm, max_norm, eps, stream)
         return norm

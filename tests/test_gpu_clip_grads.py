@@ -1,6 +1,8 @@
-"""clip_grads() of a layer whose gradient buffers were replaced or moved, and on another
-stream. A norm is within 2^-23 of the exact one, a clipped gradient within the roundings of
+"""clip_grads() of a layer whose gradient buffers were replaced or moved, on another stream, and with norms
+that are kept. A norm is within 2^-23 of the exact one, a clipped gradient within the roundings of
 test_gpu_layer_grouped.py."""
+import math
+
 import pytest
 import torch
 
@@ -15,6 +17,10 @@ def _layer(mel, dtype="bf16"):
     for i, g in enumerate(layer.grads.values()):
         g.copy_(_rand(*g.shape, dtype=dtype, seed=i))
     return layer
+
+
+def _exact(bufs):
+    return math.sqrt(sum(float((g.double() ** 2).sum()) for g in bufs))
 
 
 @pytest.mark.parametrize("how", ["replaced", "moved"])
@@ -38,6 +44,23 @@ def test_other_buffers_than_at_the_first_call(how):
     assert layer.grads["db_gu"].data_ptr() == fresh.data_ptr()
     _clipped(bufs, before, norm, 0.5)
     assert torch.equal(old if how == "replaced" else old_data, kept)
+
+
+def test_norms_that_are_kept():
+    mel = _mel()
+    say("[clip_grads norms]")
+    layer = _layer(mel, "f32")
+    norms, exact = [torch.empty(1, device="cuda") for _ in range(3)], []
+    for n in norms:
+        exact.append(_exact(layer.grads.values()))
+        assert layer.clip_grads(exact[-1] / 2, norm=n) is n
+        torch.cuda.synchronize()
+    for n, e in zip(norms, exact):
+        assert abs(float(n) - e) <= 2.0 ** -23 * e
+    assert exact[2] < 0.3 * exact[0]
+    assert layer.clip_grads(1e9).data_ptr() == layer.clip_grads(1e9).data_ptr()
+    with pytest.raises(ValueError):
+        layer.clip_grads(1.0, norm=torch.empty(2, device="cuda"))
 
 
 def stream_of(t):
