@@ -108,8 +108,8 @@ class _Clipped:
     """clip_grads() of a layer that owns its gradients' buffers (_grad_buffers())."""
 
     def clip_grads(self, max_norm: float, eps: float = 1e-6, stream=None, norm=None):
-        """Scales the layer's gradients in place by min(1, max_norm / (norm + eps)); returns norm
-        (float32 [1], on the device), the 2-norm of all of them before. It is `norm` where that is
+        """Scales the gradients of the layer's weights and vectors in place by min(1, max_norm /
+        (norm + eps)); returns norm (float32 [1], on the device), the 2-norm of all of them before. It is `norm` where that is
         given, else a buffer of the layer, which the next call writes over. The workspace is the
         layer's too: its calls have to be ordered, whichever streams they are on."""
         bufs = self._grad_buffers()
@@ -540,7 +540,11 @@ class MoELoRASublayer(_Clipped):
         return s
 
     def _grad_buffers(self):
-        return [*self.grads.values(), *self.block._grad_buffers()]
+        """Of what is trained: a gate for every token or element is computed from the tokens, and its
+        gradient goes on from here, unscaled like dh."""
+        computed = self.after.gate in ("token", "full")
+        return [*(g for n, g in self.grads.items() if not (computed and n == "dgate")),
+                *self.block._grad_buffers()]
 
     def _sub(self, d: dict, desc: Residual, prefix="") -> dict:
         """The entries of d (vectors, or with prefix "d" gradients) that desc's call takes."""
