@@ -604,12 +604,14 @@ class MoELoRASublayer(_Clipped):
 
 def mx_weights(w_gu, w_d, stream=None) -> dict:
     """Merged expert weights w_gu [E, 2I, H] and w_d [E, H, I] (or one expert's, without E) in 4
-    bits: {"w_gu", "s_gu", "w_d", "s_d"}, codes and scales, for MoEMXLayer."""
+    bits: {"w_gu", "s_gu", "w_d", "s_d"}, codes and scales, for MoEMXLayer, in memory allocated for
+    `stream` (None: the current one)."""
     out = {}
     for n, w in (("gu", w_gu), ("d", w_d)):
         u8 = dict(device=w.device, dtype=torch.uint8)
-        out["w_" + n] = torch.empty(*w.shape[:-1], w.shape[-1] // 2, **u8)
-        out["s_" + n] = torch.empty(*w.shape[:-1], mx_scale_cols(w.shape[-1]), **u8)
+        with _allocating(stream, w.device):
+            out["w_" + n] = torch.empty(*w.shape[:-1], w.shape[-1] // 2, **u8)
+            out["s_" + n] = torch.empty(*w.shape[:-1], mx_scale_cols(w.shape[-1]), **u8)
         moe_mx_quantize(w, out["w_" + n], out["s_" + n], "fp4", stream)
     return out
 
