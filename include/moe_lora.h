@@ -631,7 +631,8 @@ moe_status moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_
  * with experts, an unknown format or out, T * k >= 2^31, T * k * max(K, N) above 2^34, codes of one
  * weight matrix, or of a gathered a, of 2 GiB or more, a pointer off a 16-byte boundary (rows,
  * offsets: 4), an output that overlaps another buffer; MOE_ERR_UNSUPPORTED: K not a multiple of 32,
- * N not a multiple of 8 (of 32 with MOE_MX_OUT_FP8), K or N above 2^20. */
+ * N not a multiple of 8 (of 32 with MOE_MX_OUT_FP8), K or N above 2^20, with swiglu
+ * (T * k / 64 + E) * N of 2^30 or more. */
 enum { MOE_MX_OUT_FP8 = 3 /* beside moe_dtype's values */ };
 typedef struct {
   int32_t T, K, N, E, k;

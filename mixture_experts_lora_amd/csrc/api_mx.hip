@@ -52,6 +52,11 @@ moe_status check_mx_linear(const moe_mx_linear_shape* s) {
     return fail(MOE_ERR_INVALID_ARG, "the codes of a weight matrix must be smaller than 2 GiB");
   if (s->gather && moe::mx_code_bytes(s->a_format, int64_t(s->T) * s->K) >= (int64_t(1) << 31))
     return fail(MOE_ERR_INVALID_ARG, "the codes of a gathered a must be smaller than 2 GiB");
+  // a grid holds fewer than 2^32 threads: tiles of 64 rows and 128 weight rows at 256 each, with one
+  // tile that is not full for every expert (larger tiles are taken only for far fewer)
+  const int64_t M = int64_t(s->T) * s->k, cols = s->swiglu ? 64 : 128;
+  if ((M / 64 + std::max<int64_t>(1, std::min<int64_t>(s->E, M))) * ((s->N + cols - 1) / cols) >= (1 << 24))
+    return fail(MOE_ERR_UNSUPPORTED, "more tiles of the experts than a grid holds");
   return MOE_OK;
 }
 
