@@ -4,7 +4,9 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -1213,18 +1215,19 @@ moe_status check_grads(int32_t count, const moe_grad* grads, bool clip) {
   if (count > 0) CHECK_PTR(grads);
   for (int32_t i = 0; i < count; ++i) {
     const moe_grad& g = grads[i];
-    const std::string at = "gradient " + std::to_string(i);
-    if (!known_dtype(g.dtype)) return fail(MOE_ERR_INVALID_ARG, at + ": unknown dtype");
-    if (g.n < 0 || g.n > (int64_t(1) << 40))
-      return fail(MOE_ERR_INVALID_ARG, at + ": n must be in [0, 2^40]");
+    auto refuse = [i](const char* what) {
+      return fail(MOE_ERR_INVALID_ARG, "gradient " + std::to_string(i) + ": " + what);
+    };
+    if (!known_dtype(g.dtype)) return refuse("unknown dtype");
+    if (g.n < 0 || g.n > (int64_t(1) << 40)) return refuse("n must be in [0, 2^40]");
     if (g.n == 0) continue;
-    if (!g.src) return fail(MOE_ERR_INVALID_ARG, at + ": null src");
+    if (!g.src) return refuse("null src");
     if (reinterpret_cast<uintptr_t>(g.src) % esize(g.dtype))
-      return fail(MOE_ERR_INVALID_ARG, at + ": src is not aligned to its type");
+      return refuse("src is not aligned to its type");
     if (!clip) continue;
-    if (!g.dst) return fail(MOE_ERR_INVALID_ARG, at + ": null dst");
+    if (!g.dst) return refuse("null dst");
     if (reinterpret_cast<uintptr_t>(g.dst) % esize(g.dtype))
-      return fail(MOE_ERR_INVALID_ARG, at + ": dst is not aligned to its type");
+      return refuse("dst is not aligned to its type");
   }
   return MOE_OK;
 }
@@ -1237,10 +1240,13 @@ moe_status check_grad_ranges(int32_t count, const moe_grad* grads, const float* 
     int32_t index;
     bool out;
   };
-  std::vector<Span> spans;
+  // no exception may leave a C entry point
+  const std::unique_ptr<Span[]> spans(new (std::nothrow) Span[2 * size_t(count) + 1]);
+  if (!spans) return hip_fail(hipErrorOutOfMemory, "moe_grad_clip");
+  Span* end = spans.get();
   auto add = [&](const void* p, int64_t bytes, int32_t index, bool out) {
     const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    spans.push_back({lo, lo + static_cast<uintptr_t>(bytes), index, out});
+    *end++ = {lo, lo + static_cast<uintptr_t>(bytes), index, out};
   };
   add(norm, 4, -1, false);
   for (int32_t i = 0; i < count; ++i) {
@@ -1249,10 +1255,11 @@ moe_status check_grad_ranges(int32_t count, const moe_grad* grads, const float* 
     add(g.dst, g.n * esize(g.dtype), i, true);
     if (g.src != g.dst) add(g.src, g.n * esize(g.dtype), i, false);
   }
-  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  std::sort(spans.get(), end, [](const Span& a, const Span& b) { return a.lo < b.lo; });
   // the span that reaches furthest so far, among all and among the outputs
   const Span *all = nullptr, *outs = nullptr;
-  for (const Span& s : spans) {
+  for (const Span* at = spans.get(); at != end; ++at) {
+    const Span& s = *at;
     const Span* hit = s.out ? all : outs;
     if (hit && hit->hi > s.lo) {
       auto name = [](const Span& x) {
