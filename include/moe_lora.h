@@ -626,8 +626,8 @@ moe_status moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_
  *           (rows [M] = moe_permute's sorted_pair); else a holds the M rows, rows is not read
  *   out     MOE_BF16 or MOE_F16: y [M, N]; MOE_MX_OUT_FP8: y [M, N] E4M3 codes and y_scales
  *           [M, moe_mx_scale_cols(N)], quantised from the float32 result (the a of the next product)
- * a, a_scales, w, w_scales as moe_mx_quantize gives them. ws: moe_mx_linear_workspace_bytes (0: may
- * be NULL). Results repeat bit for bit. Errors: T, K, N or k < 1, E < 0 or > 1024, k > E or k > 32
+ * a, a_scales, w, w_scales as moe_mx_quantize gives them. No shape needs a workspace today:
+ * moe_mx_linear_workspace_bytes is 0, and ws and ws_bytes are reserved (NULL and 0 will do). Results repeat bit for bit. Errors: T, K, N or k < 1, E < 0 or > 1024, k > E or k > 32
  * with experts, an unknown format or out, T * k >= 2^31, T * k * max(K, N) above 2^34, codes of one
  * weight matrix, or of a gathered a, of 2 GiB or more, a pointer off a 16-byte boundary (rows,
  * offsets: 4), an output that overlaps another buffer; MOE_ERR_UNSUPPORTED: K not a multiple of 32,

@@ -905,6 +905,7 @@ class MXLinear:
 
 
 def moe_mx_linear_workspace_bytes(shape: MXLinear) -> int:
+    """Workspace bytes of moe_mx_linear: none today, for every shape."""
     return shape._ws
 
 

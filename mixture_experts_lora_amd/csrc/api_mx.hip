@@ -110,14 +110,14 @@ moe_status moe_mx_linear_workspace_bytes(const moe_mx_linear_shape* shape, size_
   moe_status st = check_mx_linear(shape);
   if (st != MOE_OK) return st;
   CHECK_PTR(ws);
-  *ws = moe::mx_linear_ws_bytes(*shape);
+  *ws = 0;
   return MOE_OK;
 }
 
 moe_status moe_mx_linear(const moe_mx_linear_shape* shape, const void* a, const uint8_t* a_scales,
                          const int32_t* rows, const int32_t* offsets, const void* w,
-                         const uint8_t* w_scales, void* y, uint8_t* y_scales, void* ws,
-                         size_t ws_bytes, void* stream) {
+                         const uint8_t* w_scales, void* y, uint8_t* y_scales, void*, size_t,
+                         void* stream) {
   moe_status st = check_mx_linear(shape);
   if (st != MOE_OK) return st;
   const moe_mx_linear_shape& s = *shape;
@@ -137,25 +137,19 @@ moe_status moe_mx_linear(const moe_mx_linear_shape* shape, const void* a, const 
   CHECK_ROWS(w_scales);
   CHECK_ROWS(y);
   CHECK_ROWS(y_scales);
-  CHECK_ROWS(ws);
   if ((s.gather && (reinterpret_cast<uintptr_t>(rows) & 3)) ||
       (s.E > 0 && (reinterpret_cast<uintptr_t>(offsets) & 3)))
     return fail(MOE_ERR_INVALID_ARG, "rows or offsets do not start on a 4-byte boundary");
-  const size_t need = moe::mx_linear_ws_bytes(s);
-  if (need > 0) CHECK_PTR(ws);
-  if (ws_bytes < need)
-    return fail(MOE_ERR_WORKSPACE, "product workspace needs " + std::to_string(need) + " bytes");
   const int64_t M = int64_t(s.T) * s.k, ar = s.gather ? s.T : M, sk = moe::mx_scale_cols(s.K);
   const int64_t wr = int64_t(s.N) * (s.swiglu ? 2 : 1) * (s.E > 0 ? s.E : 1);
   st = check_ranges(
-      {{y, M * s.N * (mx ? 1 : 2), "y"}, {y_scales, M * moe::mx_scale_cols(s.N), "y_scales"},
-       {need ? ws : nullptr, int64_t(need), "ws"}},
+      {{y, M * s.N * (mx ? 1 : 2), "y"}, {y_scales, M * moe::mx_scale_cols(s.N), "y_scales"}},
       {{a, moe::mx_code_bytes(s.a_format, ar * s.K), "a"}, {a_scales, ar * sk, "a_scales"},
        {w, wr * (s.K / 2), "w"}, {w_scales, wr * sk, "w_scales"},
        {s.gather ? rows : nullptr, M * 4, "rows"},
        {s.E > 0 ? offsets : nullptr, (int64_t(s.E) + 1) * 4, "offsets"}});
   if (st != MOE_OK) return st;
-  hipError_t e = moe::launch_mx_linear(s, a, a_scales, rows, offsets, w, w_scales, y, y_scales, ws,
+  hipError_t e = moe::launch_mx_linear(s, a, a_scales, rows, offsets, w, w_scales, y, y_scales,
                                        as_stream(stream), moe::active_timer());
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_mx_linear");
 }

@@ -229,10 +229,9 @@ hipError_t launch_mx_quantize(int fmt, int dtype, int64_t rows, int cols, const 
                               void* codes, uint8_t* scales, hipStream_t s, KernelTimer* tm);
 hipError_t launch_mx_dequantize(int fmt, int dtype, int64_t rows, int cols, const void* codes,
                                 const uint8_t* scales, void* dst, hipStream_t s, KernelTimer* tm);
-size_t mx_linear_ws_bytes(const moe_mx_linear_shape& s);
 hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const uint8_t* a_scales,
                             const int32_t* rows, const int32_t* offsets, const void* w,
-                            const uint8_t* w_scales, void* y, uint8_t* y_scales, void* ws,
-                            hipStream_t st, KernelTimer* tm);
+                            const uint8_t* w_scales, void* y, uint8_t* y_scales, hipStream_t st,
+                            KernelTimer* tm);
 
 }  // namespace moe

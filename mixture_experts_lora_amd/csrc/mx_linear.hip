@@ -596,14 +596,8 @@ __global__ __launch_bounds__(kSmallWaves * 64) void mx_rows_kernel(MxGemm p) {
       }
     }
   } else if (there) {
-    Out16<OUT>* y = static_cast<Out16<OUT>*>(p.y) + row * p.N + col;
-    const uint32_t lo = __builtin_bit_cast(uint16_t, from_f32<Out16<OUT>>(v[0]));
-    if constexpr (CPT == 2) {  // N and the column are even
-      const uint32_t hi = __builtin_bit_cast(uint16_t, from_f32<Out16<OUT>>(v[1]));
-      *reinterpret_cast<uint32_t*>(y) = lo | (hi << 16);
-    } else {
-      *reinterpret_cast<uint16_t*>(y) = static_cast<uint16_t>(lo);
-    }
+    static_assert(CPT == 1, "a column a thread");
+    static_cast<Out16<OUT>*>(p.y)[row * p.N + col] = from_f32<Out16<OUT>>(v[0]);
   }
 }
 
@@ -641,12 +635,10 @@ hipError_t by_product(const moe_mx_linear_shape& s, F&& go) {
 
 }  // namespace
 
-size_t mx_linear_ws_bytes(const moe_mx_linear_shape&) { return 0; }
-
 hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const uint8_t* a_scales,
                             const int32_t* rows, const int32_t* offsets, const void* w,
-                            const uint8_t* w_scales, void* y, uint8_t* y_scales, void*,
-                            hipStream_t st, KernelTimer* tm) {
+                            const uint8_t* w_scales, void* y, uint8_t* y_scales, hipStream_t st,
+                            KernelTimer* tm) {
   TimedScope ts(tm, MOE_K_MX_LINEAR, st);
   MxGemm p{};
   p.a = static_cast<const uint8_t*>(a);

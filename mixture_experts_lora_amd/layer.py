@@ -622,16 +622,16 @@ class _MXExperts:
     def __init__(self, T, H, I, dtype, E, k, device):
         self.up = MXLinear(T, H, I, "fp8", "mx8", "swiglu", E, k, gather=E > 0)
         self.down = MXLinear(T, I, H, "fp8", dtype, E=E, k=k)
+        for s in (self.up, self.down):  # of 0 bytes; refuses what the products do not take
+            moe_mx_linear_workspace_bytes(s)
         u8 = dict(device=device, dtype=torch.uint8)
         self.act = torch.empty(T * k, I, **u8)
         self.act_scales = torch.empty(T * k, mx_scale_cols(I), **u8)
-        ws = max(moe_mx_linear_workspace_bytes(s) for s in (self.up, self.down))
-        self.ws = torch.empty(max(ws, 1), **u8)
 
     def __call__(self, x, x_scales, w, y, rows, offsets, stream):
-        moe_mx_linear(self.up, x, x_scales, w["w_gu"], w["s_gu"], self.act, self.ws,
+        moe_mx_linear(self.up, x, x_scales, w["w_gu"], w["s_gu"], self.act,
                       y_scales=self.act_scales, rows=rows, offsets=offsets, stream=stream)
-        moe_mx_linear(self.down, self.act, self.act_scales, w["w_d"], w["s_d"], y, self.ws,
+        moe_mx_linear(self.down, self.act, self.act_scales, w["w_d"], w["s_d"], y,
                       offsets=offsets, stream=stream)
 
 
