@@ -614,10 +614,12 @@ moe_status moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_
 /* Products of microscaled operands, the forward of an exported layer's projections:
  *   z = a w^T                         a E4M3 or E2M1, w E2M1
  *   y = z, or with swiglu y = silu(z[:, :N]) * z[:, N:]
- * Products are exact. The matrix cores sum them in float32; with an 8-bit a they first align each
- * eight neighbours to the largest of the eight and drop what lies below 2^-13 of its power of two:
- * a few 1e-6 of the result on random rows, more where the terms cancel (so there is no float32
- * output).
+ * Products are exact and summed in float32 (beside a code of a below 2^-5 a multiple of 2^-10 can
+ * be dropped, in units of the two scales).
+ *   fast    nonzero: a caller's choice of speed over that, for an 8-bit a (of no effect with 4): one
+ *           matrix instruction where there are two otherwise, and it aligns each eight neighbouring
+ *           products to the largest of the eight and drops what lies below 2^-13 of its power of two:
+ *           a few 1e-6 of the result on random rows, more where the terms cancel
  *   E = 0   one weight matrix: k = 1, gather = 0, M = T rows; w [Nw, K], Nw = N or with swiglu 2N
  *   E > 0   one per expert, w [E, Nw, K]: M = T * k rows in expert order, rows
  *           [offsets[e], offsets[e + 1]) with expert e's weights (moe_permute's offsets); rows
@@ -637,7 +639,7 @@ enum { MOE_MX_OUT_FP8 = 3 /* beside moe_dtype's values */ };
 typedef struct {
   int32_t T, K, N, E, k;
   int32_t a_format; /* moe_mx_format */
-  int32_t gather, swiglu, out;
+  int32_t gather, swiglu, out, fast;
 } moe_mx_linear_shape;
 moe_status moe_mx_linear_workspace_bytes(const moe_mx_linear_shape *shape, size_t *ws);
 moe_status moe_mx_linear(const moe_mx_linear_shape *shape, const void *a, const uint8_t *a_scales,

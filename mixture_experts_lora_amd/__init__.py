@@ -859,7 +859,9 @@ class MXLinear:
     """A product of microscaled operands: y = a w^T, or with act "swiglu" silu of its first N
     columns times the others. a_format: "fp8" or "fp4"; w is "fp4". E = 0: one w [Nw, K] for T
     rows (Nw = N, or 2N with swiglu). E > 0: w [E, Nw, K] and T * k rows in expert order; gather:
-    a holds the T token rows. out: "bf16", "f16" or "mx8" (codes and scales as "fp8")."""
+    a holds the T token rows. out: "bf16", "f16" or "mx8" (codes and scales as "fp8"). Sums are
+    float32's; fast: with an "fp8" a half the matrix instructions, for sums that are off by a few
+    1e-6."""
     T: int
     K: int
     N: int
@@ -869,6 +871,7 @@ class MXLinear:
     E: int = 0
     k: int = 1
     gather: bool = False
+    fast: bool = False
 
     @property
     def M(self) -> int:
@@ -881,7 +884,8 @@ class MXLinear:
         if not 0 <= self.E < 1 << 31:
             raise ValueError(f"E must be in [0, 2^31), got {self.E}")
         return MoeMxLinearShape(self.T, self.K, self.N, self.E, self.k, MX_IDS[self.a_format],
-                                int(self.gather), int(self.act == "swiglu"), MX_OUT_IDS[self.out])
+                                int(self.gather), int(self.act == "swiglu"), MX_OUT_IDS[self.out],
+                                int(self.fast))
 
     @functools.cached_property
     def _c(self) -> MoeMxLinearShape:

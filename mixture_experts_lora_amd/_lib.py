@@ -93,7 +93,7 @@ class MoeGroupedRouter(ctypes.Structure):
 
 class MoeMxLinearShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "K", "N", "E", "k", "a_format", "gather",
-                                              "swiglu", "out")]
+                                              "swiglu", "out", "fast")]
 
 
 class MoeGrad(ctypes.Structure):

@@ -3,10 +3,17 @@
 // bits or microscaled 8 bits (mx.h has the formats).
 //
 // The scaled MFMA takes the codes as they are stored, with one scale byte per row and 32 elements of
-// the reduction, and accumulates in float32. With 8-bit codes it aligns each eight neighbouring products
-// to the largest of them and cuts off what lies below 2^-13 of its power of two (measured; sums of
-// random rows are then off by about 4e-6); with two 4-bit operands nothing is lost. Its operand layout for 32 x 32 x 64 (16 x 16 x 128): lane
-// l holds row l % 32 (l % 16) and, with g = l / 32 (l / 16), in 4 bits the 32 elements of block g; in
+// the reduction, and accumulates in float32. With two 4-bit operands nothing is lost on the way. With
+// 8-bit codes it aligns each eight neighbouring products to the largest of them and cuts off what lies
+// below 2^-13 of its power of two (measured; sums of random rows are then off by about 4e-6, where
+// float32 sums are off by 1e-7). So an 8-bit a is multiplied in two parts, the codes of 4 and more and
+// the others: a product of the first is a multiple of 2^-2 and at most 2688, which is cut at 2^-2; one
+// of the others is at most 22.5, cut at 2^-9, and a multiple of that unless its code is below 2^-5, where
+// 2^-10 can go. Sums are then float32's (of 94 million 8-bit results of 2880-element sums 76 are not the
+// nearest to the exact one, 75 by a float32 product in torch, 49764 in one part), for twice the matrix
+// instructions: the experts below 828 us in two parts and 525 in one, one token 11.4 and 10.3.
+//
+// Its operand layout for 32 x 32 x 64 (16 x 16 x 128): lane l holds row l % 32 (l % 16) and, with g = l / 32 (l / 16), in 4 bits the 32 elements of block g; in
 // 8 bits the 16 elements from 16 g on and the 16 from 16 g on of the second half. The scale that lane
 // (row, g) brings is that of block g. w is the first operand, so that an output row's columns lie
 // along a lane's registers.
@@ -149,6 +156,20 @@ __device__ __forceinline__ i32x8 mx_operand(const i32x4& lo, const i32x4& hi, bo
              : __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// The codes of 4 and more in magnitude, with zeros in the place of the others. Magnitude bits past 0x47
+// carry into a byte's bit 7, which is then spread over the byte.
+__device__ __forceinline__ i32x8 mx_large(const i32x8& x) {
+  i32x8 r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t v = static_cast<uint32_t>(x[i]);
+    const uint32_t t = (v & 0x7f7f7f7fu) + 0x38383838u;
+    // bytes 0 to 3 of all ones or zeros by bits 7, 15, 23 and 31 of t
+    r[i] = static_cast<int>(v & __builtin_amdgcn_perm(t, t << 8, 0x0b090a08u));
+  }
+  return r;
+}
+
 // 16 bytes per lane, global -> LDS at byte `lds` of the block's memory (dma16 of gemm16.h, whose
 // generic pointers cost a check for null each); rs and soff are uniform.
 __device__ __forceinline__ void dma16_at(uint32_t lds, const u32x4& rs, uint32_t vo, uint32_t soff) {
@@ -166,7 +187,8 @@ __device__ __forceinline__ void dma16_at(uint32_t lds, const u32x4& rs, uint32_t
 template <int BN, bool SWIGLU>
 constexpr int out_cols() { return SWIGLU ? BN / 2 : BN; }
 
-template <int AF, int OUT, bool SWIGLU, int BM, int BN, int WM, int WN, int NST>
+// PARTS: that a is multiplied in.
+template <int AF, int PARTS, int OUT, bool SWIGLU, int BM, int BN, int WM, int WN, int NST>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
     __attribute__((amdgpu_waves_per_eu(2, 2))) void mx_gemm_kernel(MxGemm p) {
   constexpr int WAVES_N = BN / WN, NW = (BM / WM) * WAVES_N;
@@ -286,7 +308,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
       c.w[f] = *reinterpret_cast<const int*>(ss + (BM + wn * WN + f * 32 + r) * 16) >> (8 * g);
   };
   // Piece i of a step's fragments: 16 bytes of a weight fragment, or of one of a's.
-  constexpr int PIECES = NF + MF * (AB / 64), PRODUCTS = NF * MF;
+  constexpr int PIECES = NF + MF * (AB / 64), PRODUCTS = NF * MF * PARTS;
   auto load = [&](int at, auto jc, int i, Frags& x) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value;
     if (i < NF) {
@@ -301,12 +323,21 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
   };
   // Product i of a step. The empty statement holds it in place: neither it nor what stands beside it
   // moves across, so that the wave's other instructions go out while the matrix core is busy.
+  i32x8 large, rest;
   auto multiply = [&](auto jc, int i, const Frags& x, const Scales& c) __attribute__((always_inline)) {
     constexpr int j = decltype(jc)::value;
-    const int f = i / MF, m = i % MF;
+    const int f = PARTS == 1 ? i / MF : i % NF, m = PARTS == 1 ? i % MF : i / (NF * PARTS);
+    i32x8 a = mx_operand(x.a[m][0], x.a[m][AB / 64 - 1], AB == 64);
+    if constexpr (PARTS == 2) {
+      if (i % (NF * PARTS) == 0) {
+        large = mx_large(a);
+        rest = a ^ large;
+      }
+      a = i / NF % PARTS == 0 ? large : rest;
+    }
     acc[f][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-        mx_operand(x.w[f], x.w[f], true), mx_operand(x.a[m][0], x.a[m][AB / 64 - 1], AB == 64),
-        acc[f][m], 4, AF == MOE_MX_FP4 ? 4 : 0, 2 * j, c.w[f], 2 * j, c.a[m]);
+        mx_operand(x.w[f], x.w[f], true), a, acc[f][m], 4, AF == MOE_MX_FP4 ? 4 : 0, 2 * j, c.w[f],
+        2 * j, c.a[m]);
     asm volatile("" : "+v"(acc[f][m])::"memory");
   };
   const std::integral_constant<int, 0> first;
@@ -452,7 +483,7 @@ constexpr int kSmallRows = 16, kSmallWaves = 4, kBatch = 4;
 template <int OUT>
 constexpr int small_cols() { return OUT == kMxOut8 ? 32 : 16; }
 
-template <int AF, int OUT, bool SWIGLU>
+template <int AF, int PARTS, int OUT, bool SWIGLU>
 __global__ __launch_bounds__(kSmallWaves * 64) void mx_rows_kernel(MxGemm p) {
   constexpr int COLS = small_cols<OUT>(), OF = COLS / 16, NF = SWIGLU ? 2 * OF : OF;
   constexpr int AB = row_bytes_of<AF>(128), AC = AB / 64;  // bytes a step; 16-byte pieces a lane
@@ -532,12 +563,21 @@ __global__ __launch_bounds__(kSmallWaves * 64) void mx_rows_kernel(MxGemm p) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (s0 + u >= last) break;
-      const i32x8 fa = mx_operand(x.a[u][0], x.a[u][AC - 1], AC == 1);
+      const i32x8 all = mx_operand(x.a[u][0], x.a[u][AC - 1], AC == 1);
+      auto products = [&](const i32x8& fa) __attribute__((always_inline)) {
 #pragma unroll
-      for (int f = 0; f < NF; ++f)
-        acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            mx_operand(x.w[u][f], x.w[u][f], true), fa, acc[f], 4, AF == MOE_MX_FP4 ? 4 : 0, 0,
-            x.sw[f][u] >> (8 * g), 0, x.sa[u] >> (8 * g));
+        for (int f = 0; f < NF; ++f)
+          acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              mx_operand(x.w[u][f], x.w[u][f], true), fa, acc[f], 4, AF == MOE_MX_FP4 ? 4 : 0, 0,
+              x.sw[f][u] >> (8 * g), 0, x.sa[u] >> (8 * g));
+      };
+      if constexpr (PARTS == 1) {
+        products(all);
+      } else {
+        const i32x8 large = mx_large(all);
+        products(large);
+        products(all ^ large);
+      }
     }
   };
   if (first < last) load_a(first, x0);
@@ -618,19 +658,24 @@ __global__ __launch_bounds__(kSmallWaves * 64) void mx_rows_kernel(MxGemm p) {
 //  in 4 bits 69.5 / 74.2; 2048 tokens of 4 of 32 experts, 2880 -> 2880, 94.4 / 106.3.
 constexpr int kCUs = 256, kRowsBlocks = 3 * kCUs, kTilesToFill = kCUs * 3 / 4;
 
-// Calls go with the format of a, the output and SwiGLU as constants.
+// Calls go with the format of a, its parts, the output and SwiGLU as constants.
 template <typename F>
 hipError_t by_product(const moe_mx_linear_shape& s, F&& go) {
   using std::integral_constant;
-  return by_format(s.a_format, [&](auto af) {
+  auto operand = [&](auto af, auto parts) {
     auto out = [&](auto o) {
-      return s.swiglu ? go(af, o, integral_constant<bool, true>())
-                      : go(af, o, integral_constant<bool, false>());
+      return s.swiglu ? go(af, parts, o, integral_constant<bool, true>())
+                      : go(af, parts, o, integral_constant<bool, false>());
     };
     if (s.out == MOE_MX_OUT_FP8) return out(integral_constant<int, kMxOut8>());
     if (s.out == MOE_BF16) return out(integral_constant<int, 1>());
     return out(integral_constant<int, 0>());
-  });
+  };
+  typedef integral_constant<int, 1> One;
+  typedef integral_constant<int, 2> Two;
+  if (s.a_format == MOE_MX_FP4) return operand(integral_constant<int, MOE_MX_FP4>(), One());
+  if (s.fast) return operand(integral_constant<int, MOE_MX_FP8>(), One());
+  return operand(integral_constant<int, MOE_MX_FP8>(), Two());
 }
 
 }  // namespace
@@ -656,8 +701,8 @@ hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const u
   p.E = s.E;
   p.k = s.k;
   const int experts = std::max(1, std::min(s.E, p.M));
-  return by_product(s, [&](auto af, auto out, auto glu) {
-    constexpr int AF = decltype(af)::value, OUT = decltype(out)::value;
+  return by_product(s, [&](auto af, auto parts, auto out, auto glu) {
+    constexpr int AF = decltype(af)::value, PARTS = decltype(parts)::value, OUT = decltype(out)::value;
     constexpr bool GLU = decltype(glu)::value;
     // at most this many tiles of bm rows and bn weight rows, whatever the experts' counts are
     auto tiles = [&](int bm, int cols) {
@@ -667,7 +712,7 @@ hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const u
     auto tiled = [&](auto bm, auto bn, auto wm, auto wn, auto nst) {
       constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value;
       constexpr int WM = decltype(wm)::value, WN = decltype(wn)::value;
-      hipLaunchKernelGGL((mx_gemm_kernel<AF, OUT, GLU, BM, BN, WM, WN, decltype(nst)::value>),
+      hipLaunchKernelGGL((mx_gemm_kernel<AF, PARTS, OUT, GLU, BM, BN, WM, WN, decltype(nst)::value>),
                          dim3(static_cast<unsigned>(tiles(BM, out_cols<BN, GLU>()))),
                          dim3((BM / WM) * (BN / WN) * 64), 0, st, p);
     };
@@ -683,7 +728,7 @@ hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const u
     };
     using std::integral_constant;
     if (tiles(kSmallRows, small_cols<OUT>()) * (small_cols<OUT>() / 16) <= kRowsBlocks) {
-      hipLaunchKernelGGL((mx_rows_kernel<AF, OUT, GLU>),
+      hipLaunchKernelGGL((mx_rows_kernel<AF, PARTS, OUT, GLU>),
                          dim3(static_cast<unsigned>(tiles(kSmallRows, small_cols<OUT>()))),
                          dim3(kSmallWaves * 64), 0, st, p);
     } else if (!GLU && fills(256, 256) && rounds(192) * 10 < rounds(256) * 9) {

@@ -619,9 +619,9 @@ def mx_weights(w_gu, w_d, stream=None) -> dict:
 class _MXExperts:
     """gate, up and down of one expert or of E, over T tokens' 8-bit rows in token order."""
 
-    def __init__(self, T, H, I, dtype, E, k, device):
-        self.up = MXLinear(T, H, I, "fp8", "mx8", "swiglu", E, k, gather=E > 0)
-        self.down = MXLinear(T, I, H, "fp8", dtype, E=E, k=k)
+    def __init__(self, T, H, I, dtype, E, k, device, fast):
+        self.up = MXLinear(T, H, I, "fp8", "mx8", "swiglu", E, k, gather=E > 0, fast=fast)
+        self.down = MXLinear(T, I, H, "fp8", dtype, E=E, k=k, fast=fast)
         for s in (self.up, self.down):  # of 0 bytes; refuses what the products do not take
             moe_mx_linear_workspace_bytes(s)
         u8 = dict(device=device, dtype=torch.uint8)
@@ -640,10 +640,11 @@ class MoEMXLayer:
     float32. shape.dtype ("bf16" or "f16") is that of x and y; shape.r is not used. H and I are
     multiples of 32. Layers of other T share the weights; the buffers are the layer's own.
 
-    shared_I: width of an always-on shared expert, whose weights are mx_weights of its own."""
+    shared_I: width of an always-on shared expert, whose weights are mx_weights of its own. fast: of
+    the products (MXLinear)."""
 
     def __init__(self, shape: Shape, router: str | GroupedRouter, shared_I: int | None = None,
-                 device="cuda"):
+                 device="cuda", fast: bool = False):
         if shape.dtype not in ("bf16", "f16"):
             raise ValueError(f"results have 16 bits: dtype bf16 or f16, got {shape.dtype}")
         _check_router(router, shape)
@@ -651,10 +652,10 @@ class MoEMXLayer:
         self.shape, self.router = shape, router
         z = lambda *s, dtype=dt: torch.empty(s, device=device, dtype=dtype)  # noqa: E731
         i32, u8 = torch.int32, torch.uint8
-        self.experts = _MXExperts(T, H, shape.I, shape.dtype, E, k, device)
+        self.experts = _MXExperts(T, H, shape.I, shape.dtype, E, k, device, fast)
         self.shared = None
         if shared_I:
-            self.shared = _MXExperts(T, H, int(shared_I), shape.dtype, 0, 1, device)
+            self.shared = _MXExperts(T, H, int(shared_I), shape.dtype, 0, 1, device, fast)
             self.shared_y = z(T, H)
         self.x_codes, self.x_scales = z(T, H, dtype=u8), z(T, mx_scale_cols(H), dtype=u8)
         self.topk_ids, self.topk_w = z(T, k, dtype=i32), z(T, k, dtype=torch.float32)
@@ -688,19 +689,19 @@ class MoEMXSublayer:
 
         h2 = h + alpha * g * post(layer(norm(h)))
 
-    norm, post, gate, gate_sigmoid, alpha, eps and weight_shift as in MoELoRASublayer, shared_I as
-    in MoEMXLayer; param_shapes() names the vectors in `params`. w_r [E, H] is the router's
+    norm, post, gate, gate_sigmoid, alpha, eps and weight_shift as in MoELoRASublayer, shared_I and
+    fast as in MoEMXLayer; param_shapes() names the vectors in `params`. w_r [E, H] is the router's
     projection, of the stream's dtype."""
 
     def __init__(self, shape: Shape, router: str | GroupedRouter, shared_I: int | None = None,
                  norm: str = "rms", post: str = "none", gate: str = "none",
                  gate_sigmoid: bool = False, alpha: float = 1.0, eps: float = 1e-5,
-                 weight_shift: float = 0.0, device="cuda"):
+                 weight_shift: float = 0.0, device="cuda", fast: bool = False):
         if norm == "none":
             raise ValueError("the layer's input needs a norm: \"rms\" or \"layer\"")
         T, H, E, dt = shape.T, shape.H, shape.E, shape.torch_dtype
         self.shape = shape
-        self.layer = MoEMXLayer(shape, router, shared_I, device)
+        self.layer = MoEMXLayer(shape, router, shared_I, device, fast)
         common = dict(eps=eps, weight_shift=weight_shift)
         self.before = Residual(T, H, shape.dtype, pre=norm, **common)
         self.after = Residual(T, H, shape.dtype, post=post, pre="none", gate=gate,
