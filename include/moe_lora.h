@@ -614,8 +614,8 @@ moe_status moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_
 /* Products of microscaled operands, the forward of an exported layer's projections:
  *   z = a w^T                         a E4M3 or E2M1, w E2M1
  *   y = z, or with swiglu y = silu(z[:, :N]) * z[:, N:]
- * Products are exact and summed in float32 (beside a code of a below 2^-5 a multiple of 2^-10 can
- * be dropped, in units of the two scales).
+ * Products are exact and summed in float32 (a product of an E4M3 code below 2^-5 can lose 2^-10, in
+ * units of the two scales).
  *   fast    nonzero: a caller's choice of speed over that, for an 8-bit a (of no effect with 4): one
  *           matrix instruction where there are two otherwise, and it aligns each eight neighbouring
  *           products to the largest of the eight and drops what lies below 2^-13 of its power of two:

@@ -11,12 +11,13 @@
 // of the others is at most 22.5, cut at 2^-9, and a multiple of that unless its code is below 2^-5, where
 // 2^-10 can go. Sums are then float32's (of 94 million 8-bit results of 2880-element sums 76 are not the
 // nearest to the exact one, 75 by a float32 product in torch, 49764 in one part), for twice the matrix
-// instructions: the experts below 828 us in two parts and 525 in one, one token 11.4 and 10.3.
+// instructions: the experts below 790 to 880 us in two parts and 510 to 540 in one, one token 11.5 and
+// 10.3. One part is a caller's choice (fast).
 //
-// Its operand layout for 32 x 32 x 64 (16 x 16 x 128): lane l holds row l % 32 (l % 16) and, with g = l / 32 (l / 16), in 4 bits the 32 elements of block g; in
-// 8 bits the 16 elements from 16 g on and the 16 from 16 g on of the second half. The scale that lane
-// (row, g) brings is that of block g. w is the first operand, so that an output row's columns lie
-// along a lane's registers.
+// Its operand layout for 32 x 32 x 64 (16 x 16 x 128): lane l holds row l % 32 (l % 16) and, with
+// g = l / 32 (l / 16), in 4 bits the 32 elements of block g; in 8 bits the 16 elements from 16 g on and
+// the 16 from 16 g on of the second half. The scale that lane (row, g) brings is that of block g. w is
+// the first operand, so that an output row's columns lie along a lane's registers.
 #include <algorithm>
 #include <type_traits>
 
@@ -129,10 +130,13 @@ __device__ __forceinline__ constexpr int row_bytes_of(int k) {
 }
 
 // ------------------------------------------------------------------ many rows: tiles through LDS
-// Bound by power and by what stands outside the loop: 32 experts, 8192 tokens of 4, 2880 -> 2 x 2880,
-// 8-bit result, 513 us in all (2.1 PFLOP/s), of which 9.5 us a tile, 13 tiles a CU, are the tile's
-// lookup, its first stages and its epilogue; the loop runs at 2.7 PFLOP/s, where products of such
-// data from registers alone reach 3.6 to 4.1. Dense, 4 bits by 4, 8192 x 4096 x 2880: 64 to 70 us.
+// 32 experts, 8192 tokens of 4, 2880 -> 2 x 2880, 8-bit result: in two parts 790 to 880 us, the matrix
+// cores busy for 59 % of the cycles (executed 2.5 to 2.75 PFLOP/s, where products of such data from
+// registers alone reach 3.6 to 3.9); in one 510 to 540 us, busy for 50 %. Most of the rest stands outside
+// the loop: 9.5 us a tile, 13 tiles a CU one after another, are the tile's lookup, its first stages and
+// its epilogue, in which nothing else runs on the CU. Power is the smaller part (zeros in the place of
+// data: 749 us for 793, and 473 for 509). Dense, 4 bits by 4, 8192 x 4096 x 2880: 63 to 66 us, the matrix
+// cores busy for 31 %, on zeros 53.
 //
 // A stage is 128 elements of every row; NST stages have places in LDS. 16-byte chunk c of row r is
 // kept at c ^ swizzle(r), so that 16 lanes of a fragment read (16 rows, one chunk) touch every bank
@@ -474,7 +478,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64)
 // for 16 rows, in batches of four steps of 128 elements with the next batch on its way: a row's four
 // steps are 256 bytes of codes and 16 of scales. Loads go by buffer resources, whose bounds make
 // zeros of steps past the operand; what a batch reads behind its own steps is not multiplied. One
-// token of 4 of 32 experts, 2880 -> 2 x 2880, 10 us, 3.5 TB/s: bound by the latency of 23 steps.
+// token of 4 of 32 experts, 2880 -> 2 x 2880, 11.5 us (3.1 TB/s; in one part 10.3): bound by a chain of
+// latencies, the offsets, the scan over the experts, then the tile's weights (and rows[], then a). A
+// wave's six steps are two batches, the second on its way while the first is multiplied. Into 8 bits 14.6
+// us (13.1): with 32 columns a block there are half the blocks, at one wave a SIMD.
 constexpr int kSmallRows = 16, kSmallWaves = 4, kBatch = 4;
 
 // Output columns of a block: as few as there can be, so that even one token's experts give every CU
@@ -641,22 +648,27 @@ __global__ __launch_bounds__(kSmallWaves * 64) void mx_rows_kernel(MxGemm p) {
   }
 }
 
-// Which kernel takes a call, measured on both sides of each line.
-//  Few rows: while its blocks (in units of 16 output columns) are at most three a CU, since weights
-//  are read again for every 16 rows. 4096 -> 2880, 64 rows 11.9 us against 14.5 of the smallest
-//  tiles, 96 rows 18.3 against 14.7; 8192 -> 8192, 16 rows 15.3 / 25.3, 32 rows 27.5 / 24.9; SwiGLU
-//  2880 -> 2880 of 4 of 32 experts, one token 10.5 / 13.2, 8 tokens 41.9 / 36.7.
+// Which kernel takes a call, measured on both sides of each line with an 8-bit a in one part and
+// [in two].
+//  Few rows: while its blocks (in units of 16 output columns) are at most three [four] a CU, since
+//  weights are read again for every 16 rows. 4096 -> 2880, 64 rows 11.9 us against 14.5 of the smallest
+//  tiles [12.9 / 21.3], 96 rows 18.3 against 14.7 [19.5 / 21.4]; 8192 -> 8192, 16 rows 15.3 / 25.3
+//  [16.5 / 37], 32 rows 27.5 / 24.9 [29.4 / 37]; SwiGLU 2880 -> 2880 of 4 of 32 experts, one token
+//  10.5 / 13.2 [11.5 / 17.9], 8 tokens 41.9 / 36.7 [44.8 / 43.8].
 //  Larger tiles, which read less from L2 for a product: where they give three quarters of the CUs a
 //  tile, and experts on average rows for half of one. 4096 -> 2880, 256 x 256 against 128 x 128:
-//  4096 rows (192 tiles) 51.6 / 54.8 us, 2048 rows 43.4 / 31.4; the experts above, 1024 tokens (128
-//  rows each) 122.6 / 143.0, 768 tokens 114.7 / 103.5. 128 x 128 against 64 x 128: 1024 rows (184
-//  tiles) 20.1 / 21.4, 512 rows 17.8 / 15.6; the experts, 512 tokens (64 rows each) 93.5 / 111.8,
-//  256 tokens 81 / 75. (128 x 256 lies within 7 % of one of the others everywhere.)
+//  4096 rows (192 tiles) 51.6 / 54.8 us [81.5 / 87], 2048 rows 43.4 / 31.4 [80 / 57]; the experts
+//  above, 1024 tokens (128 rows each) 122.6 / 143.0 [177 / 176], 768 tokens 114.7 / 103.5 [136 / 138].
+//  128 x 128 against 64 x 128: 1024 rows (184 tiles) 20.1 / 21.4 [33.6 / 31.6], 512 rows 17.8 / 15.6
+//  [31.8 / 23.1]; the experts, 512 tokens (64 rows each) 93.5 / 111.8 [118 / 121], 256 tokens 81 / 75
+//  [109 / 86].
 //  256 x 192 in the place of 256 x 256 where the last round of tiles would leave many CUs idle, so
 //  that rounds times columns fall by a tenth or more (without SwiGLU, whose halves of 96 rows no
-//  instruction's step divides): 8192 rows of 4096 -> 2880 (480 tiles for 384) 87.3 us against 97.6,
-//  in 4 bits 69.5 / 74.2; 2048 tokens of 4 of 32 experts, 2880 -> 2880, 94.4 / 106.3.
-constexpr int kCUs = 256, kRowsBlocks = 3 * kCUs, kTilesToFill = kCUs * 3 / 4;
+//  instruction's step divides): 8192 rows of 4096 -> 2880 (480 tiles for 384) 87.3 us against 97.6
+//  [140 / 160], in 4 bits 69.5 / 74.2; 2048 tokens of 4 of 32 experts, 2880 -> 2880, 94.4 / 106.3
+//  [157 / 179], 8192 tokens [458 / 432]. Rounds are counted as if only the last of all tiles were not
+//  full: what each expert's last tile adds is not known on the host.
+constexpr int kCUs = 256, kTilesToFill = kCUs * 3 / 4;
 
 // Calls go with the format of a, its parts, the output and SwiGLU as constants.
 template <typename F>
@@ -727,7 +739,7 @@ hipError_t launch_mx_linear(const moe_mx_linear_shape& s, const void* a, const u
              p.M / bm * static_cast<int64_t>((s.N + cols - 1) / cols) >= kTilesToFill;
     };
     using std::integral_constant;
-    if (tiles(kSmallRows, small_cols<OUT>()) * (small_cols<OUT>() / 16) <= kRowsBlocks) {
+    if (tiles(kSmallRows, small_cols<OUT>()) * (small_cols<OUT>() / 16) <= (PARTS == 2 ? 4 : 3) * kCUs) {
       hipLaunchKernelGGL((mx_rows_kernel<AF, PARTS, OUT, GLU>),
                          dim3(static_cast<unsigned>(tiles(kSmallRows, small_cols<OUT>()))),
                          dim3(kSmallWaves * 64), 0, st, p);
