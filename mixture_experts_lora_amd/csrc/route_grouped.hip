@@ -17,14 +17,12 @@
 // L lanes work on a token, 16 where there are many tokens of no more than 256 experts, so that a
 // wave's rounds of the top-k serve four tokens, else a wave; expert i belongs to lane i % L. The
 // kernel is bound by instructions (64-bit exponentials and k rounds over the keys), not by its
-// 4 E + 8 k bytes a token: 8192 tokens, 8 of 256 experts in 8 groups, 11 us where the bytes take 1.7;
-// one token 4.6 us.
+// 4 E + 8 k bytes a token: 8192 tokens, 8 of 256 experts in 8 groups, 11 to 12 us where the bytes take
+// 1.7; one token 4.6 us.
 #include <algorithm>
 
 #include "device_common.h"
 #include "launch.h"
-
-#include <float.h>
 
 namespace moe {
 
@@ -109,15 +107,16 @@ __device__ __forceinline__ int key_index(double key) {
 }
 
 // e^x to 2^-45 for |x| <= 708, larger |x| taken as 708 (e^-708 is 0 beside any other score): x is cut
-// at a multiple of ln 2, taken off in two parts, and the rest (at most ln 2 / 2) goes
-// through the Taylor polynomial of degree 12, whose next term is below 2^-52. Equal arguments give
-// equal values, so ties stay ties.
+// at a multiple of ln 2, taken off in two parts (Cody and Waite's reduction, Software Manual for the
+// Elementary Functions, 1980), and the rest (at most ln 2 / 2) goes through the Taylor polynomial of
+// degree 12, whose next term is below 2^-52. Equal arguments give equal values, so ties stay ties.
 __device__ __forceinline__ double route_exp(double x) {
   x = __builtin_fmin(__builtin_fmax(x, -708.0), 708.0);
   const double n = __builtin_rint(x * 1.4426950408889634);
-  // ln 2 to 20 bits, so that n times it is exact, and what is left of ln 2
-  double r = __builtin_fma(n, -0.693145751953125, x);
-  r = __builtin_fma(n, -1.4286068203094172321e-06, r);
+  // the first 15 bits of ln 2, so that n times them is exact, and what is left of it
+  constexpr double high = 22713.0 / 32768, low = 1.4286068203094172e-06;
+  double r = __builtin_fma(n, -high, x);
+  r = __builtin_fma(n, -low, r);
   constexpr double c[] = {1.0 / 479001600, 1.0 / 39916800, 1.0 / 3628800, 1.0 / 362880, 1.0 / 40320,
                           1.0 / 5040,      1.0 / 720,      1.0 / 120,     1.0 / 24,     1.0 / 6,
                           0.5,             1.0,            1.0};
