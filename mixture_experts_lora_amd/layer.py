@@ -99,8 +99,9 @@ def _allocating(stream, device):
     stream has just released may still be in use there."""
     if stream is None:
         return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # 0, the default stream, would give a new one
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
     return torch.cuda.stream(stream)
 
 

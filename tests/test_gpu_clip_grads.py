@@ -71,6 +71,21 @@ def stream_of(t):
             return s["stream"]
 
 
+def test_memory_for_the_default_stream_by_its_number():
+    mel = _mel()
+    say("[clip_grads stream 0]")
+    layer = _layer(mel)
+    bufs = layer._grad_buffers()
+    before = [g.clone() for g in bufs]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        norm = layer.clip_grads(0.5, stream=0)
+    assert stream_of(norm) == torch.cuda.default_stream().cuda_stream == 0
+    torch.cuda.synchronize()
+    _clipped(bufs, before, norm, 0.5)
+
+
 @pytest.mark.parametrize("raw", [False, True])
 def test_memory_belongs_to_the_stream_of_the_call(raw):
     mel = _mel()
