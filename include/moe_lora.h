@@ -571,7 +571,7 @@ moe_status moe_linear_bwd(const moe_linear_shape *shape, const void *dy, const v
  * Errors: an unknown dtype, n outside [0, 2^40], a tensor not aligned to its type, max_norm < 0
  * or not finite, eps <= 0 or not finite, a dst that overlaps another dst, another tensor's src or
  * the norm; norm or ws (16-byte boundary) overlapping a src; MOE_ERR_UNSUPPORTED: more than 2^20
- * tensors. */
+ * tensors; MOE_ERR_HIP: also where the host has no memory left to check the list. */
 typedef struct {
   const void *src;
   void *dst;
@@ -629,12 +629,12 @@ moe_status moe_mx_dequantize(int32_t format, int32_t dtype, int64_t rows, int32_
  *   out     MOE_BF16 or MOE_F16: y [M, N]; MOE_MX_OUT_FP8: y [M, N] E4M3 codes and y_scales
  *           [M, moe_mx_scale_cols(N)], quantised from the float32 result (the a of the next product)
  * a, a_scales, w, w_scales as moe_mx_quantize gives them. No shape needs a workspace today:
- * moe_mx_linear_workspace_bytes is 0, and ws and ws_bytes are reserved (NULL and 0 will do). Results repeat bit for bit. Errors: T, K, N or k < 1, E < 0 or > 1024, k > E or k > 32
- * with experts, an unknown format or out, T * k >= 2^31, T * k * max(K, N) above 2^34, codes of one
- * weight matrix, or of a gathered a, of 2 GiB or more, a pointer off a 16-byte boundary (rows,
- * offsets: 4), an output that overlaps another buffer; MOE_ERR_UNSUPPORTED: K not a multiple of 32,
- * N not a multiple of 8 (of 32 with MOE_MX_OUT_FP8), K or N above 2^20, with swiglu
- * (T * k / 64 + E) * N of 2^30 or more. */
+ * moe_mx_linear_workspace_bytes is 0, and ws and ws_bytes are reserved (NULL and 0 will do). Results
+ * repeat bit for bit. Errors: T, K, N or k < 1, E < 0 or > 1024, k > E or k > 32 with experts, an
+ * unknown format or out, T * k >= 2^31, T * k * max(K, N) above 2^34, codes of one weight matrix, or
+ * of a gathered a, of 2 GiB or more, a pointer off a 16-byte boundary (rows, offsets: 4), an output
+ * that overlaps another buffer; MOE_ERR_UNSUPPORTED: K not a multiple of 32, N not a multiple of 8 (of
+ * 32 with MOE_MX_OUT_FP8), K or N above 2^20, with swiglu (T * k / 64 + E) * N of 2^30 or more. */
 enum { MOE_MX_OUT_FP8 = 3 /* beside moe_dtype's values */ };
 typedef struct {
   int32_t T, K, N, E, k;
