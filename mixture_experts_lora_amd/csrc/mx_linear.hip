@@ -135,7 +135,7 @@ __device__ __forceinline__ constexpr int row_bytes_of(int k) {
 // registers alone reach 3.6 to 3.9); in one 510 to 540 us, busy for 50 %. Most of the rest stands outside
 // the loop: 9.5 us a tile, 13 tiles a CU one after another, are the tile's lookup, its first stages and
 // its epilogue, in which nothing else runs on the CU. Power is the smaller part (zeros in the place of
-// data: 749 us for 793, and 473 for 509). Dense, 4 bits by 4, 8192 x 4096 x 2880: 63 to 66 us, the matrix
+// data: 749 us for 793, and 473 for 509). Dense, 4 bits by 4, 8192 x 4096 x 2880: 60 to 66 us, the matrix
 // cores busy for 31 %, on zeros 53.
 //
 // A stage is 128 elements of every row; NST stages have places in LDS. 16-byte chunk c of row r is
